@@ -35,13 +35,15 @@ PER_ROW_BLOCK128 = 1
 PER_TENSOR = 2
 PER_GROUP_COL = 3
 MX32 = 4  # MXFP8: uint8 E8M0 codes, K-block-major [cols/128, rows, 4]
+MX4 = 5  # MXFP4: packed e2m1 codes, two a byte, with scale codes as MX32
 
 __all__ = [
     "PER_ROW", "PER_ROW_BLOCK128", "PER_TENSOR", "PER_GROUP_COL", "MoEError", "lib", "device_error",
     "quantize_rows", "quantize_weights", "ragged_sort", "gmm", "gmm_swiglu", "swiglu_fusable", "swiglu_fuse_pays", "swiglu_quant", "ragged_gather_reduce",
     "gather_scale_quant", "swiglu_bwd_quant", "quantize_group_cols", "tgmm", "transpose_u8",
     "router_topk", "router_backward", "MX32", "quantize_rows_mx", "quantize_weights_mx", "quantize_sort_mx",
-    "gmm_mx", "gmm_mx_swiglu", "swiglu_quant_mx", "quantize_weights_int8", "gmm_w8", "gmm_w8_workspace_bytes",
+    "gmm_mx", "gmm_mx_swiglu", "swiglu_quant_mx", "MX4", "quantize_rows_mx4", "quantize_weights_mx4",
+    "dequantize_rows_mx4", "quantize_sort_mx4", "swiglu_quant_mx4", "gmm_mx4", "quantize_weights_int8", "gmm_w8", "gmm_w8_workspace_bytes",
     "prepare_weights_w8",
     "ExpertWeights", "prepare_weights", "FFNBuffers", "ffn_forward", "ffn_backward",
 ]
@@ -65,6 +67,17 @@ def _s():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _arg(what: str, t: Optional[torch.Tensor], dtype, shape) -> Optional[torch.Tensor]:
+    """`t`, checked against the type and shape that the call `what` takes (None in `shape`: any size)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise MoEError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise MoEError(f"{what}: a tensor on {t.device}, but the current device is {torch.cuda.current_device()}")
+    return t
+
+
 def _nb(cols: int) -> int:
     return (cols + 127) // 128
 
@@ -85,7 +98,7 @@ def _scale_buf(mode: int, rows: int, cols: int, device, out=None):
         return torch.empty(rows, dtype=torch.float32, device=device)
     if mode == PER_ROW_BLOCK128:
         return torch.empty(rows, _nb(cols), dtype=torch.float32, device=device)
-    if mode == MX32:
+    if mode in (MX32, MX4):
         return torch.empty(cols // 128, rows, 4, dtype=torch.uint8, device=device)
     return None
 
@@ -263,6 +276,103 @@ def swiglu_quant_mx(a: torch.Tensor, h_q=None, h_sf=None):
     h_q = torch.empty(R, F, dtype=torch.uint8, device=a.device) if h_q is None else h_q
     h_sf = _scale_buf(MX32, R, F, a.device, h_sf)
     check(lib().moe_swiglu_quant_mx(_p(a), R, F, _p(h_q), _p(h_sf), _s()), "moe_swiglu_quant_mx")
+    return h_q, h_sf
+
+
+def quantize_rows_mx4(x: torch.Tensor, q=None, sf=None):
+    """MXFP4: bf16 [rows, cols] -> (packed e2m1 codes uint8 [rows, cols/2], E8M0 codes uint8 [cols/128, rows, 4])."""
+    rows, cols = _arg("quantize_rows_mx4", x, torch.bfloat16, (None, None)).shape
+    q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device) if q is None else q
+    sf = _scale_buf(MX4, rows, cols, x.device, sf)
+    _arg("quantize_rows_mx4 q", q, torch.uint8, (rows, cols // 2))
+    _arg("quantize_rows_mx4 sf", sf, torch.uint8, (cols // 128, rows, 4))
+    if x.numel():
+        check(lib().moe_quantize_rows_mx4(_p(x), rows, cols, _p(q), _p(sf), _s()), "moe_quantize_rows_mx4")
+    return q, sf
+
+
+def quantize_weights_mx4(w: torch.Tensor):
+    """MXFP4 weights: bf16 [E, N, K] -> (codes [E, N, K/2], E8M0 codes [K/128, E*N, 4])."""
+    E, N, K = _arg("quantize_weights_mx4", w, torch.bfloat16, (None, None, None)).shape
+    q, sf = quantize_rows_mx4(w.reshape(E * N, K))
+    return q.view(E, N, K // 2), sf
+
+
+def dequantize_rows_mx4(q: torch.Tensor, sf: torch.Tensor, out=None) -> torch.Tensor:
+    """MXFP4 codes [rows, cols/2] and scale codes [cols/128, rows, 4] -> their bf16 values [rows, cols]."""
+    rows, half = _arg("dequantize_rows_mx4", q, torch.uint8, (None, None)).shape
+    cols = 2 * half
+    _arg("dequantize_rows_mx4 sf", sf, torch.uint8, (cols // 128, rows, 4))
+    out = torch.empty(rows, cols, dtype=torch.bfloat16, device=q.device) if out is None else out
+    _arg("dequantize_rows_mx4 out", out, torch.bfloat16, (rows, cols))
+    if q.numel():
+        check(lib().moe_dequantize_rows_mx4(_p(q), _p(sf), rows, cols, _p(out), _s()), "moe_dequantize_rows_mx4")
+    return out
+
+
+def quantize_sort_mx4(x: torch.Tensor, topk_ids: torch.Tensor, E: int, out: Optional[dict] = None):
+    """MXFP4 steps 1 + 2: the dict of quantize_sort with xs_q = packed codes [T*k, D/2] and
+    xs_scale = E8M0 codes [D/128, T*k, 4]."""
+    T, k = _arg("quantize_sort_mx4 topk_ids", topk_ids, torch.int32, (None, None)).shape
+    D = _arg("quantize_sort_mx4 x", x, torch.bfloat16, (T, None)).shape[1]
+    R = T * k
+    dev = x.device
+    o = out if out is not None else {}
+    if "sorted_src" not in o:
+        o["sorted_src"] = torch.empty(R, dtype=torch.int32, device=dev)
+        o["pos"] = torch.empty(R, dtype=torch.int32, device=dev)
+        o["group_sizes"] = torch.empty(E, dtype=torch.int32, device=dev)
+        o["group_offsets"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        o["xs_q"] = torch.empty(R, D // 2, dtype=torch.uint8, device=dev)
+        o["xs_scale"] = _scale_buf(MX4, R, D, dev)
+    for key, n in (("sorted_src", R), ("pos", R), ("group_sizes", E), ("group_offsets", E + 1)):
+        _arg(f"quantize_sort_mx4 {key}", o[key], torch.int32, (n,))
+    _arg("quantize_sort_mx4 xs_q", o["xs_q"], torch.uint8, (R, D // 2))
+    _arg("quantize_sort_mx4 xs_scale", o["xs_scale"], torch.uint8, (D // 128, R, 4))
+    if not R:
+        o["group_sizes"].zero_()
+        o["group_offsets"].zero_()
+        return o
+    nws = lib().moe_ragged_sort_workspace_bytes(T, k, E)
+    if "sort_ws" not in o or o["sort_ws"].numel() < nws:
+        o["sort_ws"] = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
+    check(lib().moe_quantize_sort_mx4(_p(x), _p(topk_ids), T, k, E, D, _p(o["sorted_src"]), _p(o["pos"]),
+                                      _p(o["group_sizes"]), _p(o["group_offsets"]), _p(o["xs_q"]), _p(o["xs_scale"]),
+                                      _p(o["sort_ws"]), o["sort_ws"].numel(), _s()), "moe_quantize_sort_mx4")
+    return o
+
+
+def gmm_mx4(lhs_q, lhs_sf, rhs_q, rhs_sf, group_sizes, group_offset: int = 0, E_local: Optional[int] = None,
+            out=None):
+    """MXFP4 grouped matmul of packed codes lhs_q [M, K/2] and rhs_q [E_local, N, K/2] -> bf16 [M, N];
+    lhs_sf [K/128, M, 4], rhs_sf [K/128, E_local*N, 4]."""
+    M, half = _arg("gmm_mx4 lhs_q", lhs_q, torch.uint8, (None, None)).shape
+    El, N, _ = _arg("gmm_mx4 rhs_q", rhs_q, torch.uint8, (None, None, half)).shape
+    K = 2 * half
+    E = _arg("gmm_mx4 group_sizes", group_sizes, torch.int32, (None,)).numel()
+    E_local = El if E_local is None else E_local
+    if E_local != El:
+        raise MoEError(f"gmm_mx4: E_local is {E_local}, but rhs_q holds {El} experts")
+    _arg("gmm_mx4 lhs_sf", lhs_sf, torch.uint8, (K // 128, M, 4))
+    _arg("gmm_mx4 rhs_sf", rhs_sf, torch.uint8, (K // 128, El * N, 4))
+    out = torch.empty(M, N, dtype=torch.bfloat16, device=lhs_q.device) if out is None else out
+    _arg("gmm_mx4 out", out, torch.bfloat16, (M, N))
+    if M:
+        check(lib().gmm_fp4_mx(_p(lhs_q), _p(lhs_sf), _p(rhs_q), _p(rhs_sf), _p(group_sizes), E, group_offset,
+                               E_local, M, K, N, _p(out), _s()), "gmm_fp4_mx")
+    return out
+
+
+def swiglu_quant_mx4(a: torch.Tensor, h_q=None, h_sf=None):
+    """MXFP4 step 4: a = [a0 | a1] bf16 [R, 2F] -> (h codes [R, F/2], h E8M0 codes [F/128, R, 4])."""
+    R, F2 = _arg("swiglu_quant_mx4", a, torch.bfloat16, (None, None)).shape
+    F = F2 // 2
+    h_q = torch.empty(R, F // 2, dtype=torch.uint8, device=a.device) if h_q is None else h_q
+    h_sf = _scale_buf(MX4, R, F, a.device, h_sf)
+    _arg("swiglu_quant_mx4 h_q", h_q, torch.uint8, (R, F // 2))
+    _arg("swiglu_quant_mx4 h_sf", h_sf, torch.uint8, (F // 128, R, 4))
+    if a.numel():
+        check(lib().moe_swiglu_quant_mx4(_p(a), R, F, _p(h_q), _p(h_sf), _s()), "moe_swiglu_quant_mx4")
     return h_q, h_sf
 
 

@@ -50,6 +50,11 @@ SIGNATURES = {
     "gmm_fp8_mx": ([P, P, P, P, P, i32, i32, i32, i64, i64, i64, P, P], i32),
     "gmm_fp8_mx_swiglu": ([P, P, P, P, P, i32, i32, i32, i64, i64, i64, P, P, P, P], i32),
     "moe_swiglu_quant_mx": ([P, i64, i64, P, P, P], i32),
+    "moe_quantize_rows_mx4": ([P, i64, i64, P, P, P], i32),
+    "moe_dequantize_rows_mx4": ([P, P, i64, i64, P, P], i32),
+    "moe_quantize_sort_mx4": ([P, P, i64, i32, i32, i64, P, P, P, P, P, P, P, sz, P], i32),
+    "moe_swiglu_quant_mx4": ([P, i64, i64, P, P, P], i32),
+    "gmm_fp4_mx": ([P, P, P, P, P, i32, i32, i32, i64, i64, i64, P, P], i32),
     "moe_quantize_weights_int8": ([P, i64, i64, i64, i32, P, P, P, P], i32),
     "gmm_fp8_w8": ([P, P, i32, P, P, i32, P, i32, i32, i32, i64, i64, i64, P, P, sz, P], i32),
     "gmm_fp8_w8_workspace_bytes": ([i64, i64], sz),

@@ -423,13 +423,17 @@ extern "C" moe_status moe_quantize_sort(const uint16_t* x, const int32_t* topk_i
 extern "C" __attribute__((visibility("hidden"))) moe_status moe_detail_quantize_gather_mx(
     const uint16_t* x, const int32_t* pos, int64_t T, int k, int64_t D, uint8_t* xs_q, uint8_t* xs_sf,
     cudaStream_t st);
+extern "C" __attribute__((visibility("hidden"))) moe_status moe_detail_quantize_gather_mx4(
+    const uint16_t* x, const int32_t* pos, int64_t T, int k, int64_t D, uint8_t* xs_q, uint8_t* xs_sf,
+    cudaStream_t st);
 
-// MXFP8 form of moe_quantize_sort: the codes and the E8M0 codes of each token
-// row go to its k sorted rows.
-extern "C" moe_status moe_quantize_sort_mx(const uint16_t* x, const int32_t* topk_ids, int64_t T, int k, int E,
-                                           int64_t D, int32_t* sorted_src, int32_t* pos, int32_t* group_sizes,
-                                           int32_t* group_offsets, uint8_t* xs_q, uint8_t* xs_sf, void* workspace,
-                                           size_t workspace_bytes, moe_stream_t stream) {
+// The block-scaled forms of moe_quantize_sort: the codes and the E8M0 codes
+// of each token row, as `gather` makes them, go to its k sorted rows.
+static moe_status quantize_sort_blocks(decltype(&moe_detail_quantize_gather_mx) gather, const uint16_t* x,
+                                       const int32_t* topk_ids, int64_t T, int k, int E, int64_t D,
+                                       int32_t* sorted_src, int32_t* pos, int32_t* group_sizes,
+                                       int32_t* group_offsets, uint8_t* xs_q, uint8_t* xs_sf, void* workspace,
+                                       size_t workspace_bytes, moe_stream_t stream) {
   MOE_HOST_CHECK(x && topk_ids && sorted_src && pos && group_sizes && group_offsets && xs_q && xs_sf && workspace,
                  MOE_ERR_INVALID_ARG);
   MOE_HOST_CHECK(T >= 0 && k > 0 && k <= 32 && E > 0 && E <= kMaxE && D > 0 && D % 128 == 0, MOE_ERR_INVALID_ARG);
@@ -441,7 +445,24 @@ extern "C" moe_status moe_quantize_sort_mx(const uint16_t* x, const int32_t* top
   moe_status stt = sort_indices(topk_ids, T, k, E, sorted_src, pos, group_sizes, group_offsets,
                                 static_cast<int*>(workspace), st);
   if (stt != MOE_OK || T * k == 0) return stt;
-  return moe_detail_quantize_gather_mx(x, pos, T, k, D, xs_q, xs_sf, st);
+  return gather(x, pos, T, k, D, xs_q, xs_sf, st);
+}
+
+extern "C" moe_status moe_quantize_sort_mx(const uint16_t* x, const int32_t* topk_ids, int64_t T, int k, int E,
+                                           int64_t D, int32_t* sorted_src, int32_t* pos, int32_t* group_sizes,
+                                           int32_t* group_offsets, uint8_t* xs_q, uint8_t* xs_sf, void* workspace,
+                                           size_t workspace_bytes, moe_stream_t stream) {
+  return quantize_sort_blocks(moe_detail_quantize_gather_mx, x, topk_ids, T, k, E, D, sorted_src, pos, group_sizes,
+                              group_offsets, xs_q, xs_sf, workspace, workspace_bytes, stream);
+}
+
+extern "C" moe_status moe_quantize_sort_mx4(const uint16_t* x, const int32_t* topk_ids, int64_t T, int k, int E,
+                                            int64_t D, int32_t* sorted_src, int32_t* pos, int32_t* group_sizes,
+                                            int32_t* group_offsets, uint8_t* xs_q, uint8_t* xs_sf, void* workspace,
+                                            size_t workspace_bytes, moe_stream_t stream) {
+  MOE_HOST_CHECK(D <= 32768 && (reinterpret_cast<uintptr_t>(xs_sf) & 3) == 0, MOE_ERR_INVALID_ARG);
+  return quantize_sort_blocks(moe_detail_quantize_gather_mx4, x, topk_ids, T, k, E, D, sorted_src, pos, group_sizes,
+                              group_offsets, xs_q, xs_sf, workspace, workspace_bytes, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -469,6 +469,66 @@ moe_status moe_swiglu_quant_mx(const uint16_t* a, int64_t R, int64_t F, uint8_t*
                                moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * MXFP4 variant of steps 1-5: the MXFP8 path above with 4-bit e2m1 elements
+ * (OCP MX v1.0, MXFP4), for activations, h and weights.
+ *
+ * A block of 32 consecutive values along the contracted dimension shares one
+ * E8M0 scale 2^X, stored as the byte X + 127:
+ *   X = floor(log2(amax)) - 2   at least -127; X = -127 when amax = 0
+ *   q = e2m1(x / 2^X)           round to nearest even, |v| > 6 saturates, the
+ *                               sign of zero is kept.
+ *   (2 is the exponent of 4, the largest power of two in e2m1, whose values
+ *   are 0, 0.5, 1, 1.5, 2, 3, 4, 6.)
+ * e2m1 has no infinity or NaN: a block that holds one gets the scale code 255
+ * (E8M0's NaN) and codes 0 with the elements' signs, and what is computed
+ * from it is NaN.
+ * Codes are packed two a byte, the even column in the low half: [rows,
+ * cols/2].  The scale codes have the K-block-major layout of MXFP8,
+ * uint8_t [cols/128][rows][4] (4-byte aligned).  cols is a multiple of 128.
+ * ------------------------------------------------------------------------ */
+
+/* Step 1 (MXFP4).  x bf16 [rows, cols] -> q [rows, cols/2], sf
+ * [cols/128][rows][4].  Expert weights w[E, N, K] are passed as rows = E*N,
+ * cols = K.  cols % 128 == 0, cols <= 32768, rows < 2^31; x and q 16-byte
+ * aligned. */
+moe_status moe_quantize_rows_mx4(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* q, uint8_t* sf,
+                                 moe_stream_t stream);
+
+/* The values that MXFP4 codes stand for: x[r, c] = bf16(e2m1(q[r, c]) *
+ * 2^(sf - 127)).  Every code that moe_quantize_rows_mx4 makes has its value
+ * exactly (bf16 holds 2^-128 to 6 * 2^125); a scale code of 254 with an
+ * element above 1.5 rounds to infinity, a scale code of 255 gives NaN. */
+moe_status moe_dequantize_rows_mx4(const uint8_t* q, const uint8_t* sf, int64_t rows, int64_t cols, uint16_t* x,
+                                   moe_stream_t stream);
+
+/* Steps 1 + 2 (MXFP4), as moe_quantize_sort_mx: xs_q [T*k, D/2], xs_sf
+ * [D/128][T*k][4]. */
+moe_status moe_quantize_sort_mx4(const uint16_t* x, const int32_t* topk_ids, int64_t T, int k, int E, int64_t D,
+                                 int32_t* sorted_src, int32_t* pos, int32_t* group_sizes, int32_t* group_offsets,
+                                 uint8_t* xs_q, uint8_t* xs_sf, void* workspace, size_t workspace_bytes,
+                                 moe_stream_t stream);
+
+/* Steps 3 / 5 (MXFP4).  out[m, n] = bf16( sum_k deq(lhs)[m, k]
+ * deq(rhs)[g(m), n, k] ) with deq(x)[.., k] = e2m1(x[.., k]) *
+ * 2^(sf[.., k/32] - 127); the tensor core applies both scales and accumulates
+ * in fp32.
+ *   lhs_q [M, K/2], lhs_sf [K/128][M][4]; rhs_q [E_local, N, K/2], rhs_sf
+ *   [K/128][E_local * N][4] (row e * N + n); out bf16 [M, N].
+ * Groups, group_offset and E_local are as in gmm_fp8: rows outside the local
+ * groups are zero.  K % 128 == 0, N % 16 == 0, E <= 1024; lhs_q, rhs_q and
+ * out 16-byte aligned, the scale codes 4-byte.  MOE_ERR_UNSUPPORTED off
+ * sm_103. */
+moe_status gmm_fp4_mx(const uint8_t* lhs_q, const uint8_t* lhs_sf, const uint8_t* rhs_q, const uint8_t* rhs_sf,
+                      const int32_t* group_sizes, int E, int group_offset, int E_local, int64_t M, int64_t K,
+                      int64_t N, uint16_t* out, moe_stream_t stream);
+
+/* Step 4 (MXFP4): a = [a0 | a1] bf16 [R, 2F] -> h = bf16(silu(a0) a1) (the h
+ * of moe_swiglu_quant) quantised per 32 columns: h_q [R, F/2], h_sf
+ * [F/128][R][4].  F % 128 == 0, F <= 32768. */
+moe_status moe_swiglu_quant_mx4(const uint16_t* a, int64_t R, int64_t F, uint8_t* h_q, uint8_t* h_sf,
+                                moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * int8-weight variant of steps 3 and 5 ([Q-FUSE], "Keep qwix out of
  * tpu-inference's fused MoE kernel and pre-quantize weights", description:
  * the weights are pre-quantised to float8_e4m3fn or int8 with [E, blocks, 1,

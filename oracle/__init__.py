@@ -27,6 +27,9 @@ import threading
 
 import numpy as np
 
+from .mx4 import (E2M1, e8m0_to_f64, f64_to_e2m1, ffn_decode, gmm_mx4, grouped_matmul, mx4_to_f64,  # noqa: F401
+                  quantize_rows_mx4, quantize_weights_mx4)
+
 PER_ROW = 0
 PER_ROW_BLOCK128 = 1
 PER_TENSOR = 2
@@ -634,6 +637,28 @@ def ffn_forward_mx(x_bits, topk_ids, topk_w, wq, E: int, tokens=None):
         o = o_rows
     return dict(x_q=x_q, x_sf=x_sf, sorted_src=sorted_src, pos=pos, sizes=sizes, offsets=offsets,
                 xs_q=xs_q, xs_sf=xs_sf, rows=rows, a=a, h_q=h_q, h_sf=h_sf, h_b=h_b, o=o, y=y)
+
+
+def swiglu_quant_mx4(a_bits):
+    """a = [a0 | a1] bf16 [R, 2F] -> (h codes [R, F], h scale codes [R, F/32], h bf16 bits)."""
+    _, _, hb = swiglu_quant_mx(a_bits)  # h itself does not depend on the codes made of it
+    hq, hsf = quantize_rows_mx4(hb)
+    return hq, hsf, hb
+
+
+def ffn_forward_mx4(x_bits, topk_ids, topk_w, wq, E: int):
+    """The forward pass on MXFP4 operands, in the order of ffn_forward_mx;
+    wq = (w_in codes, scale codes, w_out codes, scale codes)."""
+    qin, sin, qo, so = wq
+    k = topk_ids.shape[1]
+    x_q, x_sf = quantize_rows_mx4(x_bits)
+    sorted_src, pos, sizes, offsets = ragged_sort(topk_ids, E)
+    t = sorted_src // k
+    a = f64_to_bf16(gmm_mx4(x_q[t], x_sf[t], qin, sin, sizes))
+    h_q, h_sf, h_b = swiglu_quant_mx4(a)
+    o = f64_to_bf16(gmm_mx4(h_q, h_sf, qo, so, sizes))
+    return dict(xs_q=x_q[t], xs_sf=x_sf[t], sorted_src=sorted_src, pos=pos, sizes=sizes, offsets=offsets, a=a,
+                h_q=h_q, h_sf=h_sf, h_b=h_b, o=o, y=combine(o, pos, topk_w, k))
 
 
 def ffn_backward(fwd: dict, G_bits, topk_w, wq, k: int, static: dict):
