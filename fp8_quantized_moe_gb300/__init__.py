@@ -17,6 +17,9 @@ The MXFP8 variant (MX32: OCP MX v1.0 blocks of 32 e4m3 values sharing one
 E8M0 power-of-two scale along the contracted dimension) runs the same
 forward path on the block-scaled tensor-core MMA: quantize_sort_mx ->
 gmm_mx_swiglu (or gmm_mx + swiglu_quant_mx) -> gmm_mx -> ragged_gather_reduce.
+The MXFP4 variant (MX4: the same blocks of e2m1 values, two a byte) runs
+quantize_sort_mx4 -> gmm_mx4 -> swiglu_quant_mx4 -> gmm_mx4 ->
+ragged_gather_reduce.
 """
 
 from __future__ import annotations
@@ -649,6 +652,10 @@ def prepare_weights(w_in: torch.Tensor, w_out: torch.Tensor, w_mode: int, static
         qin, sin = quantize_weights_mx(w_in)
         qo, so = quantize_weights_mx(w_out)
         return ExpertWeights(qin, sin, MX32, qo, so, MX32)
+    if w_mode == MX4:
+        qin, sin = quantize_weights_mx4(w_in)
+        qo, so = quantize_weights_mx4(w_out)
+        return ExpertWeights(qin, sin, MX4, qo, so, MX4)
     if w_mode == PER_TENSOR:
         s0 = torch.tensor([static["w0"]], dtype=torch.float32, device=dev)
         s1 = torch.tensor([static["w1"]], dtype=torch.float32, device=dev)
@@ -701,7 +708,7 @@ class FFNBuffers:
         self.a = f(R, 2 * F, dt=torch.bfloat16)
         self.h = f(R, F, dt=torch.bfloat16)  # scratch of the fused per-row path
         self.keep_a = backward
-        self.h_q = f(R, F)
+        self.h_q = f(R, F // 2 if act_mode == MX4 else F)
         self.h_s = _scale_buf(act_mode, R, F, device)
         self.o = f(R, D, dt=torch.bfloat16)
         self.y = f(T, D, dt=torch.bfloat16)
@@ -747,6 +754,17 @@ def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W
         gmm_mx(buf.h_q, buf.h_s, W.w_out, W.s_out, s["group_sizes"], out=buf.o)
         ragged_gather_reduce(buf.o, s["pos"], topk_w, k, out=buf.y)
         return buf.y
+    if act_mode == MX4:
+        if W.in_mode != MX4:
+            raise MoEError("the MXFP4 forward needs MXFP4 weights")
+        s = quantize_sort_mx4(x, topk_ids, E, out=buf.sort)
+        gmm_mx4(s["xs_q"], s["xs_scale"], W.w_in, W.s_in, s["group_sizes"], out=buf.a)
+        swiglu_quant_mx4(buf.a, h_q=buf.h_q, h_sf=buf.h_s)
+        gmm_mx4(buf.h_q, buf.h_s, W.w_out, W.s_out, s["group_sizes"], out=buf.o)
+        ragged_gather_reduce(buf.o, s["pos"], topk_w, k, out=buf.y)
+        return buf.y
+    if W.in_mode == MX4:
+        raise MoEError("MXFP4 weights take MXFP4 activations (act_mode MX4)")
     w8 = W.w_in.dtype == torch.int8
     if w8 and act_mode not in (PER_ROW, PER_TENSOR):
         raise MoEError("int8 weights take per-token or static activation scales")

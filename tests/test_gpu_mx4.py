@@ -196,3 +196,45 @@ def test_gmm_bad_group_sizes():
         assert moe.device_error() == 0x2
     out = moe.gmm_mx4(*args, dev(sizes))
     assert_product(out, sizes, a, asf, w, wsf)
+
+
+# ---------------------------------------------------------------- the forward
+
+@pytest.mark.parametrize("T,k,E,D,F", [(1, 1, 2, 128, 128), (96, 2, 4, 256, 128), (200, 4, 16, 512, 384)])
+def test_forward(T, k, E, D, F):
+    """Every step of ffn_forward against the oracle fed what the GPU made one
+    step before, so that no rounding is counted twice."""
+    rng = np.random.default_rng(T)
+    w_in = bf16(rng.standard_normal((E, 2 * F, D)).astype(np.float32) * 0.05)
+    w_out = bf16(rng.standard_normal((E, D, F)).astype(np.float32) * 0.05)
+    xb = bf16(rng.standard_normal((T, D)).astype(np.float32))
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32)
+    W = moe.prepare_weights(dev(w_in), dev(w_out), moe.MX4)
+    buf = moe.FFNBuffers(T, D, E, k, F, moe.MX4, "cuda")
+    y = moe.ffn_forward(dev(xb), dev(ids), dev(w), W, moe.MX4, buf)
+    assert moe.device_error() == 0
+    qin, sin = oracle.quantize_weights_mx4(w_in)
+    qo, so = oracle.quantize_weights_mx4(w_out)
+    ref = oracle.ffn_forward_mx4(xb, ids, w, (qin, sin, qo, so), E)
+    assert np.array_equal(unpack(host(buf.sort["xs_q"])), ref["xs_q"])
+    assert_product(buf.a, ref["sizes"], ref["xs_q"], ref["xs_sf"], qin, sin)
+    hq, hsf, _ = oracle.swiglu_quant_mx4(host(buf.a))
+    assert np.array_equal(unpack(host(buf.h_q)), hq) and np.array_equal(sf_rows(host(buf.h_s)), hsf)
+    assert_product(buf.o, ref["sizes"], hq, hsf, qo, so)
+    want = oracle.combine(host(buf.o), ref["pos"], w, k, want="f64")
+    mass = oracle.combine_f64(np.abs(buf.o.double().cpu().numpy()), ref["pos"], w, k)
+    # k fp32 multiply-adds and one rounding to bf16
+    assert (np.abs(y.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + (k + 1) * 2.0 ** -24 * mass).all()
+
+
+def test_forward_refuses_mixed_weights():
+    W = moe.prepare_weights(torch.zeros(2, 256, 128, dtype=torch.bfloat16, device="cuda"),
+                            torch.zeros(2, 128, 128, dtype=torch.bfloat16, device="cuda"), moe.MX4)
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    ids, w = torch.zeros(4, 1, dtype=torch.int32, device="cuda"), torch.ones(4, 1, device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.ffn_forward(x, ids, w, W, moe.PER_ROW, moe.FFNBuffers(4, 128, 2, 1, 128, moe.PER_ROW, "cuda"))
+    W8 = moe.ExpertWeights(W.w_in, W.s_in, moe.MX32, W.w_out, W.s_out, moe.MX32)
+    with pytest.raises(moe.MoEError):
+        moe.ffn_forward(x, ids, w, W8, moe.MX4, moe.FFNBuffers(4, 128, 2, 1, 128, moe.MX4, "cuda"))
