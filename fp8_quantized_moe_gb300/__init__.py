@@ -48,7 +48,7 @@ __all__ = [
     "gmm_mx", "gmm_mx_swiglu", "swiglu_quant_mx", "MX4", "quantize_rows_mx4", "quantize_weights_mx4",
     "dequantize_rows_mx4", "quantize_sort_mx4", "swiglu_quant_mx4", "gmm_mx4", "quantize_weights_int8", "gmm_w8", "gmm_w8_workspace_bytes",
     "prepare_weights_w8",
-    "ExpertWeights", "prepare_weights", "FFNBuffers", "ffn_forward", "ffn_backward",
+    "ExpertWeights", "prepare_weights", "FFNBuffers", "ffn_forward", "ffn_backward", "DecodeBuffers", "ffn_decode",
 ]
 
 
@@ -792,6 +792,63 @@ def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W
         gmm(buf.h_q, h_s, act_mode, W.w_out, W.s_out, W.out_mode, s["group_sizes"], out=buf.o)
     ragged_gather_reduce(buf.o, s["pos"], topk_w, k, out=buf.y)
     return buf.y
+
+
+class DecodeBuffers:
+    """The output and the workspace of ffn_decode for up to T tokens, allocated once."""
+
+    def __init__(self, T, D, E, k, F, device):
+        self.T, self.D, self.E, self.k, self.F = T, D, E, k, F
+        n = int(lib().moe_ffn_decode_workspace_bytes(T, k, D, F))
+        if not n:
+            raise MoEError(f"ffn_decode does not take T = {T}, k = {k}, D = {D}, F = {F}")
+        self.y = torch.empty(T, D, dtype=torch.bfloat16, device=device)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.Tensor], W: ExpertWeights,
+               buf: Optional[DecodeBuffers] = None, E: Optional[int] = None, group_offset: int = 0) -> torch.Tensor:
+    """The expert FFN of a decoding step, T <= 64 tokens, in two kernels; bf16 [T, D].
+
+    x bf16 [T, D] and h are not quantised (with a few tokens the weights' bytes
+    are the cost); W as prepare_weights or prepare_weights_w8 made it, in every
+    type.  topk_ids int32 [T, k], topk_w fp32
+    [T, k] or None (ones).  W may hold the experts [group_offset, group_offset
+    + W.w_in.shape[0]) of E; the others add nothing.  With `buf` (made for T
+    tokens or more) the result is a part of buf.y and nothing is allocated; calls
+    that may overlap on the GPU need buffers of their own."""
+    T, k = _arg("ffn_decode topk_ids", topk_ids, torch.int32, (None, None)).shape
+    D = _arg("ffn_decode x", x, torch.bfloat16, (T, None)).shape[1]
+    _arg("ffn_decode topk_w", topk_w, torch.float32, (T, k))
+    El, F2 = W.w_in.shape[:2]
+    F = F2 // 2
+    E = group_offset + El if E is None else E
+    kind = {MX32: 2, MX4: 3}.get(W.in_mode, 1 if W.w_in.dtype == torch.int8 else 0)
+    if (W.out_mode in (MX32, MX4) or kind > 1) and W.out_mode != W.in_mode:
+        raise MoEError("ffn_decode: w_in and w_out hold different weight types")
+    code = torch.int8 if kind == 1 else torch.uint8
+    half = 2 if kind == 3 else 1
+    _arg("ffn_decode w_in", W.w_in, code, (El, 2 * F, D // half))
+    _arg("ffn_decode w_out", W.w_out, code, (El, D, F // half))
+    for what, s, mode, N, K in (("s_in", W.s_in, W.in_mode, 2 * F, D), ("s_out", W.s_out, W.out_mode, D, F)):
+        if kind > 1:
+            _arg(f"ffn_decode {what}", s, torch.uint8, (K // 128, El * N, 4))
+        elif mode in (PER_ROW, PER_ROW_BLOCK128, PER_TENSOR):
+            shape = {PER_ROW: (El, N), PER_ROW_BLOCK128: (El, _nb(K), N), PER_TENSOR: (1,)}[mode]
+            _arg(f"ffn_decode {what}", s, torch.float32, shape)
+        else:
+            raise MoEError(f"ffn_decode: scale mode {mode} of {what}")
+    if buf is None:
+        buf = DecodeBuffers(max(T, 1), D, E, k, F, x.device)
+    elif buf.T < T or buf.k != k or buf.D != D or buf.F != F:
+        raise MoEError("ffn_decode: the buffers were made for another shape")
+    y = buf.y[:T]
+    if T:
+        check(lib().moe_ffn_decode(_p(x), _p(topk_ids), _p(topk_w), T, k, E, group_offset, El, D, F, kind, _p(W.w_in),
+                                   _p(W.s_in), 0 if kind > 1 else W.in_mode, _p(W.w_out), _p(W.s_out),
+                                   0 if kind > 1 else W.out_mode, _p(y), _p(buf.ws), buf.ws.numel(), _s()),
+              "moe_ffn_decode")
+    return y
 
 
 def ffn_backward(dY: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, buf: FFNBuffers,

@@ -57,6 +57,8 @@ SIGNATURES = {
     "gmm_fp4_mx": ([P, P, P, P, P, i32, i32, i32, i64, i64, i64, P, P], i32),
     "moe_quantize_weights_int8": ([P, i64, i64, i64, i32, P, P, P, P], i32),
     "gmm_fp8_w8": ([P, P, i32, P, P, i32, P, i32, i32, i32, i64, i64, i64, P, P, sz, P], i32),
+    "moe_ffn_decode": ([P, P, P, i64, i32, i32, i32, i32, i64, i64, i32, P, P, i32, P, P, i32, P, P, sz, P], i32),
+    "moe_ffn_decode_workspace_bytes": ([i64, i32, i64, i64], sz),
     "gmm_fp8_w8_workspace_bytes": ([i64, i64], sz),
 }
 

@@ -6,6 +6,7 @@ extern "C" cudaError_t moe_detail_take_error_sort(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_combine(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_gmm(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_gmm_mx4(unsigned int* out);
+extern "C" cudaError_t moe_detail_take_error_decode(unsigned int* out);
 
 extern "C" const char* moe_status_string(moe_status s) {
   switch (s) {
@@ -25,7 +26,7 @@ extern "C" moe_status moe_get_device_error(moe_stream_t stream, int* code) {
   unsigned int all = 0, v = 0;
   cudaError_t (*take[])(unsigned int*) = {moe_detail_take_error_quantize, moe_detail_take_error_sort,
                                           moe_detail_take_error_combine, moe_detail_take_error_gmm,
-                                          moe_detail_take_error_gmm_mx4};
+                                          moe_detail_take_error_gmm_mx4, moe_detail_take_error_decode};
   for (auto fn : take) {
     if (fn(&v) != cudaSuccess) return MOE_ERR_CUDA;
     all |= v;

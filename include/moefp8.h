@@ -580,6 +580,54 @@ moe_status gmm_fp8_w8(const uint8_t* lhs_q, const float* lhs_scale, moe_scale_mo
  * out-of-range shape). */
 size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
 
+/* ------------------------------------------------------------------------
+ * The expert FFN of a decoding step (a few tokens), in two kernels:
+ *   y[t] = bf16( sum_j topk_w[t, j] * Wo[e] (silu(W0[e] x[t]) * (W1[e] x[t])) ),
+ *   e = topk_ids[t, j], in ascending j.
+ * With a few tokens the bytes of the chosen experts' weights are the cost, so
+ * the activations stay bf16 and h fp32 (held as f16 with a scale for each 128
+ * or 256 values while they are multiplied, relative error at most 2^-12); only
+ * the weights are quantised, and the sums are fp32.  (The prompt's path above
+ * quantises x and h as well, so the two do not agree bit for bit.)  Results do
+ * not depend on the order in which CTAs run.
+ *
+ *   x         bf16 [T, D], T <= 64, T * k <= 1024
+ *   topk_ids  int32 [T, k], expert ids in [0, E), the same one twice allowed;
+ *             an id outside adds nothing and sets MOE_DEVERR_BAD_EXPERT_ID
+ *   topk_w    fp32 [T, k], or NULL (all ones)
+ *   w_in      [E_local, 2F, D] (wi_0 channels, then wi_1 channels), s_in
+ *   w_out     [E_local, D, F], s_out; by `type`:
+ *     MOE_WEIGHT_E4M3, MOE_WEIGHT_INT8: codes and fp32 scales as for gmm_fp8 and
+ *       gmm_fp8_w8 (modes PER_ROW, PER_ROW_BLOCK128, PER_TENSOR; the two
+ *       tensors may have different modes)
+ *     MOE_WEIGHT_MXFP8, MOE_WEIGHT_MXFP4: codes and scale codes as for
+ *       gmm_fp8_mx and gmm_fp4_mx; in_mode and out_mode are not read
+ *   Experts outside [group_offset, group_offset + E_local) add nothing.
+ *   y         bf16 [T, D]
+ *   workspace moe_ffn_decode_workspace_bytes(T, k, D, F) bytes of device
+ *             memory, not initialised, 16-byte aligned.  Calls that may overlap
+ *             on the GPU need workspaces of their own.
+ * D % 16 == 0, F % 16 == 0 (both % 128 with blockwise or MX scales), D and
+ * F <= 32768, E <= 1024; every pointer but topk_ids and topk_w 16-byte
+ * aligned.  MOE_ERR_UNSUPPORTED off sm_103.  The call can be captured into a
+ * graph. */
+typedef enum {
+  MOE_WEIGHT_E4M3 = 0,
+  MOE_WEIGHT_INT8 = 1,
+  MOE_WEIGHT_MXFP8 = 2,
+  MOE_WEIGHT_MXFP4 = 3
+} moe_weight_type;
+
+moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int k, int E,
+                          int group_offset, int E_local, int64_t D, int64_t F, moe_weight_type type, const void* w_in,
+                          const void* s_in, moe_scale_mode in_mode, const void* w_out, const void* s_out,
+                          moe_scale_mode out_mode, uint16_t* y, void* workspace, size_t workspace_bytes,
+                          moe_stream_t stream);
+
+/* Bytes of moe_ffn_decode's workspace: 4 T k (D + F) and a little (0 for a
+ * shape that the call refuses). */
+size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F);
+
 #ifdef __cplusplus
 }
 #endif
