@@ -19,30 +19,33 @@
 // weights of wo and only then waits for kernel 1's results.
 //
 // Every CTA first sorts the pairs by expert for itself (at most 1024): a
-// chunk is up to `cap` pairs of one expert, a unit of work one chunk and one
-// block of RB weight rows (PHASE 1: RB/2 channels of wi_0 and the same of
-// wi_1), all of K.  Units of the same rows are adjacent, so that two chunks of
-// one expert read its weights together.
+// chunk is up to `cap` pairs of one expert.  A unit of work is one chunk, one
+// block of 128 weight rows (PHASE 1: 64 channels of wi_0 and the same of wi_1)
+// and one segment of K (more than one segment where there are too few blocks
+// to fill the SMs evenly; the segments' sums meet in fp32 in ascending order,
+// PHASE 1's where kernel 2 reads them).  Units run expert-major: the CTAs then
+// read a few experts at a time, long runs of memory each (with the blocks of
+// all experts side by side the same kernel streamed 1.1 TB/s instead of 3.9).
 //
-// Roles: warp 0 moves the stages (TMA boxes of 128-byte weight rows, 16 KB a
-// stage; bulk copies of the activations' rows and of the weight scales).
-// Warps 1..4 turn the stage's activations into f16, each (row, 128-byte span
-// of the weights) scaled by the power of two that puts its largest value in
-// [2^14, 2^15): f16 then holds every bf16 value to within 2^-39 of the span's
-// largest, and h to 2^-12 relative (against 2^-9 of the result's bf16).
-// Warps 5..12 contract: ldmatrix brings 16 rows x 32 bytes of weights, one
-// conversion makes two f16 weights (exact for e4m3, int8 and e2m1, NaN codes
-// included), and mma.m16n8k16 multiplies them with eight tokens.  The tensor
-// core is nowhere near its limit, so the plain warp-wide MMA serves: its
-// operands come from registers, where the weights are converted, and its M is
-// only 16.  In PHASE 1 rows 0..7 of a fragment are wi_0 channels and rows
-// 8..15 the same wi_1 channels, so a thread holds both factors of its h.
-// Span sums are scaled (weight block scale, activation span scale) into fp32
-// accumulators.
-//
-// RB = 32 (8 warps = 2 row tiles x 4 spans of K, summed at the end) makes
-// small units, for few of them; RB = 128 (8 row tiles) reads the activations
-// a quarter as often.
+// Roles: warp 0 moves the weights, one TMA box of 128 rows x 128 bytes a
+// stage.  One copy instruction a stage and no more: a stream of single 16 KB
+// boxes runs at 7.2 TB/s here, with four small bulk copies beside each (rows
+// of activations, scales) at 5.1.  So warps 1..4 fetch those themselves, each
+// every fourth stage, the next one's loads in flight while it waits: they
+// store the stage's weight scale words, and its activations as f16, each
+// (row, 128-byte span of the weights) scaled by the power of two that puts its
+// largest value in [2^14, 2^15): f16 then holds every bf16 value to within
+// 2^-39 of the span's largest, and h to 2^-12 relative (against 2^-9 of the
+// result's bf16).
+// Warps 5..12 contract, 16 weight rows each: ldmatrix brings 16 rows x 32
+// bytes of weights, one conversion makes two f16 weights (exact for e4m3, int8
+// and e2m1, NaN codes included), and mma.m16n8k16 multiplies them with eight
+// tokens.  The tensor core is nowhere near its limit, so the plain warp-wide
+// MMA serves: its operands come from registers, where the weights are
+// converted, and its M is only 16.  In PHASE 1 rows 0..7 of a fragment are
+// wi_0 channels and rows 8..15 the same wi_1 channels, so a thread holds both
+// factors of its h.  Span sums are scaled (weight block scale, activation span
+// scale) into fp32 accumulators.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets
 // its copies land and returns.
@@ -59,8 +62,10 @@ __device__ unsigned int g_err;
 
 constexpr int kConvWarps = 4, kMmaWarps = 8;
 constexpr int kThreads = 32 * (1 + kConvWarps + kMmaWarps);
-constexpr int kStageW = 16384;  // weight bytes of a stage
+constexpr int kRows = 128;              // weight rows of a unit
+constexpr int kStageW = kRows * 128;    // weight bytes of a stage
 constexpr int kMaxStages = 10;
+constexpr int kMaxSegs = 8;
 constexpr int kMaxPairs = 1024;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 1024;
@@ -70,18 +75,21 @@ enum { kE4M3 = 0, kInt8 = 1, kMx8 = 2, kMx4 = 3 };
 enum { kScaleChannel = 0, kScaleBlock = 1, kScaleTensor = 2, kScaleMx = 3 };
 
 struct Params {
-  const void* act;  // PHASE 1: x bf16 [T, K]; PHASE 2: h fp32 [slots, K]
+  const void* act;  // PHASE 1: x bf16 [T, K]; PHASE 2: h fp32 [slots, K], or partial a [segs][slots, 2K]
   const int32_t* ids;
   const float* topk_w;
   const float* scale;  // fp32 scales, or the MX scale words
-  float* out;          // PHASE 1: h [slots, F]; PHASE 2: o [slots, D]
+  float* out;          // PHASE 1: h [slots, N], or partial a [segs][slots, 2N]; PHASE 2: o [segs][slots, N]
   uint16_t* y;
   unsigned int* count;  // finished units of every block of output rows (PHASE 1 clears them)
   int ncount;
   int T, k, E, g0, El;
   int K, N;  // N: channels (PHASE 1: F, PHASE 2: D)
   int mode;
-  int cap, stages, pitch;  // pairs a chunk; bytes of an activation row in shared memory
+  int cap, stages;  // pairs a chunk; ring stages
+  int smax;         // segments of K at most
+  int grid1;        // CTAs of kernel 1
+  int nblock1, nst1;  // row blocks and K stages of kernel 1
 };
 
 struct Ctl {
@@ -94,20 +102,31 @@ struct Ctl {
   uint16_t num[kMaxExperts];
 };
 
-template <int WT, int PHASE, int RB>
+template <int WT>
 struct Cfg {
-  static constexpr int ROWTILES = RB / 16, SUBS = kMmaWarps / ROWTILES;
-  static constexpr int KE = WT == kMx4 ? 256 : 128;   // values of K in 128 bytes of weights
-  static constexpr int KC = KE / 8;                   // and in a 16-byte chunk
-  static constexpr int ES = PHASE == 1 ? 2 : 4;       // bytes of an activation as it arrives
-  static constexpr int STAGE_K = SUBS * KE;
-  static constexpr int SPANS = KE / 128;              // scale words of a row and sub-tile
-  static constexpr int SCALE_BYTES = SUBS * SPANS * RB * 4;
-  static constexpr int PAD = WT == kMx4 ? 64 : 32;    // keeps eight rows' fragments in different banks
-  static constexpr int PITCH = STAGE_K * ES + PAD;
-  static constexpr int RED_BYTES = SUBS > 1 ? 2 * kMmaWarps * 32 * 16 : 0;
-  static_assert(SUBS * RB * 128 == kStageW, "stage");
+  static constexpr int KE = WT == kMx4 ? 256 : 128;  // values of K in a stage (128 bytes of weights a row)
+  static constexpr int KC = KE / 8;                  // and in a 16-byte chunk
+  static constexpr int SPANS = KE / 128;             // scale words of a row and stage
+  static constexpr int SCALE_BYTES = SPANS * kRows * 4;
+  // bytes of an f16 activation row; the padding keeps eight rows' fragments in different banks
+  static constexpr int PITCH = KE * 2 + (WT == kMx4 ? 64 : 32);
+  static constexpr int PER = KE / 32;  // values of a span a lane converts
 };
+
+// How many segments of K: the fewest stages on the busiest CTA, a unit's
+// start and end counted as two stages.
+__device__ __forceinline__ int pick_segs(int units, int nst, int grid, int smax) {
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= smax && s <= nst; ++s) {
+    const int64_t c = static_cast<int64_t>((static_cast<int64_t>(units) * s + grid - 1) / grid) * ((nst + s - 1) / s + 2);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
 
 constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
 
@@ -258,115 +277,183 @@ __device__ void build_chunks(const Params& p, Ctl* c) {
   }
 }
 
-template <int WT, int PHASE, int RB, int NT>
-struct Mma {
-  using C = Cfg<WT, PHASE, RB>;
-
-  // One sub-tile: 16 rows x nch 16-byte chunks (at most 8) of weights at `wt`
-  // (row A + lane / 4 and row B + lane / 4 of the fragment), activations at
-  // `xb` (already this lane's), the weights' scale words of this lane's two
-  // rows at sA, sB and the activations' span scales at `xs`.
-  static __device__ __forceinline__ void sub_tile(float (&acc)[NT][4], uint32_t wt, uint32_t swz, uint32_t xb,
-                                                  int pitch8, int nch, uint32_t sA, uint32_t sB, uint32_t xs,
-                                                  int mode) {
-    float blk[NT][4], sum[NT][4];
+// One stage: 16 rows x nch 16-byte chunks (at most 8) of weights at `wt` (row
+// A + lane / 4 and row B + lane / 4 of the fragment), activations at `xb`
+// (already this lane's), the weights' scale words of this lane's two rows at
+// sA, sB and the activations' span scales at `xs`.
+template <int WT, int NT>
+__device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t wt, uint32_t swz, uint32_t xb, int nch,
+                                         uint32_t sA, uint32_t sB, uint32_t xs, bool block_scale) {
+  using C = Cfg<WT>;
+  constexpr bool MX = WT == kMx8 || WT == kMx4;
+  // two chains of sums (MX: the sum of the scaled 32-wide blocks, and the block at hand)
+  float s0[NT][4], s1[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) blk[n][i] = sum[n][i] = 0.0f;
-    const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
-    uint32_t wA = 0, wB = 0;
+    for (int i = 0; i < 4; ++i) s0[n][i] = s1[n][i] = 0.0f;
+  const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
+  uint32_t wA = 0, wB = 0;
 #pragma unroll
-    for (int c = 0; c < 8; c += 2) {
-      if (c >= nch) break;
-      if (WT == kMx8 || WT == kMx4) {
-        if (c == 0 || (WT == kMx4 && c == 4)) {
-          wA = lds32(sA + (c == 4 ? RB * 4 : 0));
-          wB = lds32(sB + (c == 4 ? RB * 4 : 0));
-        }
-      }
-      uint32_t r[4];
-      ldmatrix_x4(wt + (((c + hi) * 16) ^ swz), r);
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        if (WT != kMx8 && WT != kMx4 && c + cc >= nch) break;
-        if (WT == kMx4) {
-          uint32_t va[4], vb[4];
-          weights8(r[2 * cc], va);
-          weights8(r[2 * cc + 1], vb);
-          const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]}, a1[4] = {va[2], vb[2], va[3], vb[3]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 b = lds128(xb + n * pitch8 + (c + cc) * 64);
-            mma_f16(blk[n], a0, b.x, b.y);
-            mma_f16(blk[n], a1, b.z, b.w);
-          }
-        } else {
-          uint32_t a[4];
-          weights4<WT>(r[2 * cc], a[0], a[2]);
-          weights4<WT>(r[2 * cc + 1], a[1], a[3]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint2 b = lds64(xb + n * pitch8 + (c + cc) * 32);
-            mma_f16(blk[n], a, b.x, b.y);
-          }
-        }
-        if (WT == kMx4 || (WT == kMx8 && cc == 1)) {  // a 32-wide block is done: its scales
-          const int b = WT == kMx4 ? (c + cc) & 3 : c / 2;
-          const float fa = e8m0_value((wA >> (8 * b)) & 0xFFu), fb = e8m0_value((wB >> (8 * b)) & 0xFFu);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            sum[n][0] = __fmaf_rn(blk[n][0], fa, sum[n][0]);
-            sum[n][1] = __fmaf_rn(blk[n][1], fa, sum[n][1]);
-            sum[n][2] = __fmaf_rn(blk[n][2], fb, sum[n][2]);
-            sum[n][3] = __fmaf_rn(blk[n][3], fb, sum[n][3]);
-            blk[n][0] = blk[n][1] = blk[n][2] = blk[n][3] = 0.0f;
-          }
-        }
-      }
+  for (int c = 0; c < 8; c += 2) {
+    if (c >= nch) break;
+    if (MX && (c == 0 || (WT == kMx4 && c == 4))) {
+      wA = lds32(sA + (c == 4 ? kRows * 4 : 0));
+      wB = lds32(sB + (c == 4 ? kRows * 4 : 0));
     }
-    float fa = 1.0f, fb = 1.0f;
-    if (WT == kE4M3 || WT == kInt8) {
-      if (mode == kScaleBlock) {
-        fa = __uint_as_float(lds32(sA));
-        fb = __uint_as_float(lds32(sB));
-      }
-    }
+    uint32_t r[4];
+    ldmatrix_x4(wt + (((c + hi) * 16) ^ swz), r);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint2 s = lds64(xs + n * 32);
-      const float s0 = __uint_as_float(s.x), s1 = __uint_as_float(s.y);
-      if (WT == kMx8 || WT == kMx4) {
-        acc[n][0] = __fmaf_rn(sum[n][0], s0, acc[n][0]);
-        acc[n][1] = __fmaf_rn(sum[n][1], s1, acc[n][1]);
-        acc[n][2] = __fmaf_rn(sum[n][2], s0, acc[n][2]);
-        acc[n][3] = __fmaf_rn(sum[n][3], s1, acc[n][3]);
+    for (int cc = 0; cc < 2; ++cc) {
+      if (!MX && c + cc >= nch) break;
+      if (WT == kMx4) {
+        uint32_t va[4], vb[4];
+        weights8(r[2 * cc], va);
+        weights8(r[2 * cc + 1], vb);
+        const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]}, a1[4] = {va[2], vb[2], va[3], vb[3]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 b = lds128(xb + n * 8 * C::PITCH + (c + cc) * 64);
+          mma_f16(s1[n], a0, b.x, b.y);
+          mma_f16(s1[n], a1, b.z, b.w);
+        }
       } else {
-        acc[n][0] = __fmaf_rn(blk[n][0], s0 * fa, acc[n][0]);
-        acc[n][1] = __fmaf_rn(blk[n][1], s1 * fa, acc[n][1]);
-        acc[n][2] = __fmaf_rn(blk[n][2], s0 * fb, acc[n][2]);
-        acc[n][3] = __fmaf_rn(blk[n][3], s1 * fb, acc[n][3]);
+        uint32_t a[4];
+        weights4<WT>(r[2 * cc], a[0], a[2]);
+        weights4<WT>(r[2 * cc + 1], a[1], a[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint2 b = lds64(xb + n * 8 * C::PITCH + (c + cc) * 32);
+          mma_f16(MX || cc == 1 ? s1[n] : s0[n], a, b.x, b.y);
+        }
       }
+      if (WT == kMx4 || (WT == kMx8 && cc == 1)) {  // a 32-wide block is done: its scales
+        const int b = WT == kMx4 ? (c + cc) & 3 : c / 2;
+        const float fa = e8m0_value((wA >> (8 * b)) & 0xFFu), fb = e8m0_value((wB >> (8 * b)) & 0xFFu);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          s0[n][0] = __fmaf_rn(s1[n][0], fa, s0[n][0]);
+          s0[n][1] = __fmaf_rn(s1[n][1], fa, s0[n][1]);
+          s0[n][2] = __fmaf_rn(s1[n][2], fb, s0[n][2]);
+          s0[n][3] = __fmaf_rn(s1[n][3], fb, s0[n][3]);
+          s1[n][0] = s1[n][1] = s1[n][2] = s1[n][3] = 0.0f;
+        }
+      }
+    }
+  }
+  float fa = 1.0f, fb = 1.0f;
+  if (!MX && block_scale) {
+    fa = __uint_as_float(lds32(sA));
+    fb = __uint_as_float(lds32(sB));
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint2 v = lds64(xs + n * 32);
+    const float x0 = __uint_as_float(v.x), x1 = __uint_as_float(v.y);
+    if (MX) {
+      acc[n][0] = __fmaf_rn(s0[n][0], x0, acc[n][0]);
+      acc[n][1] = __fmaf_rn(s0[n][1], x1, acc[n][1]);
+      acc[n][2] = __fmaf_rn(s0[n][2], x0, acc[n][2]);
+      acc[n][3] = __fmaf_rn(s0[n][3], x1, acc[n][3]);
+    } else {
+      acc[n][0] = __fmaf_rn(s0[n][0] + s1[n][0], x0 * fa, acc[n][0]);
+      acc[n][1] = __fmaf_rn(s0[n][1] + s1[n][1], x1 * fa, acc[n][1]);
+      acc[n][2] = __fmaf_rn(s0[n][2] + s1[n][2], x0 * fb, acc[n][2]);
+      acc[n][3] = __fmaf_rn(s0[n][3] + s1[n][3], x1 * fb, acc[n][3]);
+    }
+  }
+}
+
+// One span of an activation row, PER values a lane: scaled to f16 in shared
+// memory at `at`, the scale to put back at `sc`.
+template <int PER>
+__device__ __forceinline__ void store_span(float (&v)[PER], uint32_t at, uint32_t sc, int lane) {
+  // largest finite magnitude of the span; infinities and NaN pass through
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+    m = max(m, b < 0x7F800000u ? b : 0u);
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  // 2^(14 - e), e = floor(log2(m)) held at or above -100
+  const int e = max(static_cast<int>(m >> 23) - 127, -100);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+#pragma unroll
+  for (int j = 0; j < PER; ++j) v[j] = __fmul_rn(v[j], up);
+  if (PER == 4)
+    sts64(at + lane * 8, f16x2(v[0], v[1]), f16x2(v[2], v[3]));
+  else
+    sts128(at + lane * 16, make_uint4(f16x2(v[0], v[1]), f16x2(v[2], v[3]), f16x2(v[PER - 4], v[PER - 3]),
+                                      f16x2(v[PER - 2], v[PER - 1])));
+  if (lane == 0) sts32f(sc, __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23));
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Where a CTA is: unit u = (chunk, row block, segment), stages [kst, end) of
+// it left.  Units are numbered expert-major.
+struct Step {
+  int u, ch, blk, seg, kst, end;
+};
+struct Walk {
+  int nblock, segs, nst, total;
+  __device__ __forceinline__ void open(Step& q) const {
+    const int per = nblock * segs;
+    q.ch = q.u / per;
+    const int r = q.u - q.ch * per;
+    q.blk = r / segs;
+    q.seg = r - q.blk * segs;
+    q.kst = q.seg * nst / segs;
+    q.end = (q.seg + 1) * nst / segs;
+  }
+  __device__ __forceinline__ Step begin() const {
+    Step q{static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0};
+    if (q.u < total) open(q);
+    return q;
+  }
+  __device__ __forceinline__ bool done(const Step& q) const { return q.u >= total; }
+  __device__ __forceinline__ void next(Step& q) const {
+    if (++q.kst == q.end) {
+      q.u += gridDim.x;
+      if (q.u < total) open(q);
+    }
+  }
+  __device__ __forceinline__ void skip(Step& q, int n) const {  // n stages on
+    while (n > 0 && q.u < total) {
+      if (q.kst + n < q.end) {
+        q.kst += n;
+        return;
+      }
+      n -= q.end - q.kst;
+      q.u += gridDim.x;
+      if (q.u < total) open(q);
     }
   }
 };
 
-template <int WT, int PHASE, int RB>
+template <int WT, int PHASE>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
-  using C = Cfg<WT, PHASE, RB>;
+  using C = Cfg<WT>;
+  constexpr int PER = C::PER;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* bp = smem_raw + (base - raw);
-  // stages of weights | activations | weight scales | activation span scales | control | partial sums
+  // stages of weights | f16 activations | weight scales | activation span scales | control
   const uint32_t S = p.stages;
   const int cap = p.cap;
   const uint32_t x_ring = base + S * kStageW;
   const uint32_t x_bytes = cap * C::PITCH;
   const uint32_t s_ring = x_ring + S * x_bytes;
-  const uint32_t v_ring = s_ring + S * C::SCALE_BYTES;  // [stage][sub][cap] floats
-  const uint32_t v_bytes = C::SUBS * cap * 4;
+  const uint32_t v_ring = s_ring + S * C::SCALE_BYTES;
+  const uint32_t v_bytes = cap * 4;
   Ctl* ctl = reinterpret_cast<Ctl*>(bp + (v_ring + S * v_bytes - base));
-  float* red = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ctl) + kCtlBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.T * p.k;
 
@@ -378,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
-      mbar_init(smem_u32(&ctl->xfull[s]), kConvWarps);
+      mbar_init(smem_u32(&ctl->xfull[s]), 1);
       mbar_init(smem_u32(&ctl->empty[s]), kMmaWarps);
     }
     ctl->abort_flag = 0;
@@ -398,10 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   __syncthreads();
 
   const int nchunk = ctl->nchunk;
-  const int rows_per = PHASE == 1 ? RB / 2 : RB;  // channels of a unit
-  const int nblock = (p.N + rows_per - 1) / rows_per;
-  const int total = nchunk * nblock;
-  const int nst = (p.K + C::STAGE_K - 1) / C::STAGE_K;
+  constexpr int kPer = PHASE == 1 ? kRows / 2 : kRows;  // channels of a unit
+  const int segs1 = pick_segs(nchunk * p.nblock1, p.nst1, p.grid1, p.smax);  // kernel 1's, in both kernels
+  Walk walk;
+  walk.nblock = (p.N + kPer - 1) / kPer;
+  walk.nst = (p.K + C::KE - 1) / C::KE;
+  walk.segs = PHASE == 1 ? segs1 : pick_segs(nchunk * walk.nblock, walk.nst, gridDim.x, p.smax);
+  walk.total = nchunk * walk.nblock * walk.segs;
   volatile int* abort_flag = &ctl->abort_flag;
   bool timed_out = false;
 
@@ -415,176 +505,161 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   }
 
   if (warp == 0) {
-    // ------------------------------------------------------------- producer
-    const bool words = p.mode == kScaleBlock || p.mode == kScaleMx;  // scales along K, one word a row and 128 values
-    const int nkb = p.K / 128;                                        // (only used with such scales: K % 128 == 0)
-    const int64_t scale_rows = static_cast<int64_t>(PHASE == 1 ? 2 * p.N : p.N);
-    // bytes of stage kst of a chunk of n pairs
-    auto valid_subs = [&](int kst) { return min(C::SUBS, (p.K - kst * C::STAGE_K + C::KE - 1) / C::KE); };
-    auto valid_kb = [&](int kst) { return min(C::SUBS * C::SPANS, nkb - kst * C::SUBS * C::SPANS); };
-    auto x_len = [&](int kst) { return min(C::STAGE_K, p.K - kst * C::STAGE_K) * C::ES; };
-    auto load_weights = [&](int s, int ch, int blk, int kst) {
-      const int e = ctl->cexp[ch], n = ctl->cnum[ch], c0 = blk * rows_per;
-      const uint32_t fb = smem_u32(&ctl->full[s]);
-      const int subs = valid_subs(kst), kbs = words ? valid_kb(kst) : 0;
-      if (lane == 0)
-        mbar_arrive_expect_tx(fb, subs * RB * 128 + n * x_len(kst) + kbs * RB * 4);
-      __syncwarp();
-      const uint32_t dst = base + s * kStageW;
-      constexpr int kBoxes = PHASE == 1 ? 2 : 1;
-      if (lane < subs * kBoxes) {
-        const int sub = lane / kBoxes, half = lane % kBoxes;
-        const int row = PHASE == 1 ? e * 2 * p.N + half * p.N + c0 : e * p.N + c0;
-        tma_load_2d(dst + sub * RB * 128 + half * (RB / 2) * 128, &tmW, (kst * C::SUBS + sub) * 128, row, fb);
+    // ------------------------------------------------------- weights by TMA
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, issued = 0;
+      for (Step q = walk.begin(); !walk.done(q); walk.next(q), ++issued) {
+        if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs)) {
+          timed_out = true;
+          break;
+        }
+        const uint32_t fb = smem_u32(&ctl->full[s]);
+        const int e = ctl->cexp[q.ch];
+        mbar_arrive_expect_tx(fb, kStageW);
+        // rows past the tensor's channels or K arrive as zeros
+        tma_load_3d(base + s * kStageW, &tmW, q.kst * 128, q.blk * kPer, PHASE == 1 ? 2 * e : e, fb);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      if (lane < kbs * kBoxes) {
-        const int kb = lane / kBoxes, half = lane % kBoxes;
-        const int64_t gkb = kst * C::SUBS * C::SPANS + kb;
-        const int64_t n0 = (PHASE == 1 ? half * p.N : 0) + c0;
-        const float* src = p.mode == kScaleMx ? p.scale + gkb * (p.El * scale_rows) + e * scale_rows + n0
-                                              : p.scale + (static_cast<int64_t>(e) * nkb + gkb) * scale_rows + n0;
-        bulk_load(s_ring + s * C::SCALE_BYTES + (kb * RB + half * (RB / 2)) * 4, src, rows_per * 4, fb);
-      }
-    };
-    auto load_acts = [&](int s, int ch, int kst) {
-      const int n = ctl->cnum[ch], st = ctl->cstart[ch];
-      const uint32_t fb = smem_u32(&ctl->full[s]);
-      const uint32_t len = x_len(kst);
-      for (int i = lane; i < n; i += 32) {
-        const int64_t row = PHASE == 1 ? ctl->order[st + i] / p.k : st + i;
-        bulk_load(x_ring + s * x_bytes + i * C::PITCH,
-                  static_cast<const uint8_t*>(p.act) + (row * p.K + static_cast<int64_t>(kst) * C::STAGE_K) * C::ES,
-                  len, fb);
-      }
-    };
-    // the steps of this CTA in order: unit u, its chunk and row block, K stage kst
-    struct Step {
-      int u, ch, blk, kst;
-    };
-    auto begin = [&] {
-      const int u = blockIdx.x;
-      return Step{u, total ? u % nchunk : 0, total ? u / nchunk : 0, 0};
-    };
-    auto next = [&](Step& q) {
-      if (++q.kst == nst) {
-        q.kst = 0;
-        q.u += gridDim.x;
-        q.blk = q.u / nchunk;
-        q.ch = q.u - q.blk * nchunk;
-      }
-    };
-    uint32_t issued = 0;
-    uint32_t s = 0, ph = 0;
-    Step q = begin();
-    if (PHASE == 2) {
-      // the ring's first weights do not depend on kernel 1; its h does
-      Step w = q;
-      for (uint32_t i = 0; i < S && w.u < total; ++i, next(w)) load_weights(i, w.ch, w.blk, w.kst);
-      grid_dep_wait();
-      // h was written through the generic proxy and is read by bulk copies
-      asm volatile("fence.proxy.async;" ::: "memory");
-      for (; issued < S && q.u < total; ++issued, next(q)) load_acts(issued, q.ch, q.kst);
-      ph = 1;  // a full ring is out; where it is not full, no step is left
-    }
-    for (; q.u < total; next(q), ++issued) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs))) {
-        timed_out = true;
-        break;
-      }
-      load_weights(s, q.ch, q.blk, q.kst);
-      load_acts(s, q.ch, q.kst);
-      if (++s == S) {
-        s = 0;
-        ph ^= 1;
-      }
-    }
-    if (timed_out) {
-      if (lane == 0) {
+      if (timed_out) {
         *abort_flag = 1;
         ctl->err = 2;
         for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)  // copies in flight land before the CTA exits
           mbar_wait_bounded(smem_u32(&ctl->full[j % S]), (j / S) & 1, &ctl->no_abort, kWaitLimitNs);
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp <= kConvWarps) {
-    // ------------------------------------------------- activations to f16
-    constexpr int PER = C::KE / 32;  // values a lane: 4 or 8
-    uint32_t s = 0, ph = 0;
-    for (int u = blockIdx.x; u < total && !timed_out; u += gridDim.x) {
-      const int n = ctl->cnum[u % nchunk];
-      for (int kst = 0; kst < nst; ++kst) {
-        if (!mbar_wait_bounded_warp(smem_u32(&ctl->full[s]), ph, abort_flag, kWaitLimitNs)) {
-          timed_out = true;
-          break;
+    // ------------------------------- activations to f16, and the weight scales
+    const bool words = p.mode == kScaleBlock || p.mode == kScaleMx;  // one word a row and 128 values of K
+    const int nkb = p.K / 128;                                        // (used with such scales: K % 128 == 0)
+    const int64_t scale_rows = static_cast<int64_t>(PHASE == 1 ? 2 * p.N : p.N);
+    // activation rows whose loads are in flight together (64 registers of them at most)
+    constexpr int kBatch = WT == kMx4 && PHASE == 2 ? 4 : 8;
+    constexpr int kVec = PHASE == 1 ? PER / 4 : PER / 2;  // 8-byte words a lane loads of a span
+    const int slots = PHASE == 2 ? ctl->cstart[nchunk - 1] + ctl->cnum[nchunk - 1] : 0;
+    const bool partial = PHASE == 2 && segs1 > 1;  // kernel 1 left sums of K segments
+    uint2 d[kBatch][kVec];
+    uint4 sc[C::SPANS];
+    auto load_rows = [&](const Step& q, int first) {
+      const int n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
+      const int col = q.kst * C::KE + lane * PER;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (first + i < n && col < p.K) {
+          const int64_t row = PHASE == 1 ? ctl->order[st + first + i] / p.k : st + first + i;
+          const uint8_t* src = static_cast<const uint8_t*>(p.act) + (row * p.K + col) * (PHASE == 1 ? 2 : 4);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) {
+            if (PHASE == 1)
+              d[i][j] = __ldg(reinterpret_cast<const uint2*>(src) + j);
+            else
+              d[i][j] = __ldcg(reinterpret_cast<const uint2*>(src) + j);
+          }
         }
-        const int left = p.K - kst * C::STAGE_K;
-        const int subs = min(C::SUBS, (left + C::KE - 1) / C::KE);
-        for (int i = warp - 1; i < n * subs; i += kConvWarps) {
-          const int sub = i / n, row = i - sub * n;
-          const uint32_t at = x_ring + s * x_bytes + row * C::PITCH + sub * C::KE * C::ES;
-          const bool ok = sub * C::KE + lane * PER < left;  // K is a multiple of 16: a lane's values are all in or out
+    };
+    auto load_scales = [&](const Step& q) {
+      const int e = ctl->cexp[q.ch];
+      const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * p.N : lane * 4);
+#pragma unroll
+      for (int v = 0; v < C::SPANS; ++v) {
+        const int64_t kb = q.kst * C::SPANS + v;
+        if (kb < nkb) {
+          const float* src = p.mode == kScaleMx ? p.scale + kb * (p.El * scale_rows) + e * scale_rows + n0
+                                                : p.scale + (e * static_cast<int64_t>(nkb) + kb) * scale_rows + n0;
+          sc[v] = __ldg(reinterpret_cast<const uint4*>(src));
+        }
+      }
+    };
+    auto unpack = [&](int i, bool ok, float (&v)[PER]) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[j] = 0.0f;
+      if (!ok) return;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (PHASE == 1) {
+          v[4 * j] = bf16lo(d[i][j].x);
+          v[4 * j + 1] = bf16hi(d[i][j].x);
+          v[4 * j + 2] = bf16lo(d[i][j].y);
+          v[4 * j + 3] = bf16hi(d[i][j].y);
+        } else {
+          v[2 * j] = __uint_as_float(d[i][j].x);
+          v[2 * j + 1] = __uint_as_float(d[i][j].y);
+        }
+      }
+    };
+    // h of kernel 1's segments: their sums in ascending order, then SwiGLU
+    auto join = [&](int slot, int col, bool ok, float (&v)[PER]) {
+      float a0[PER], a1[PER];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) a0[j] = a1[j] = 0.0f;
+      if (ok)
+        for (int g = 0; g < segs1; ++g) {
+          const float* src = static_cast<const float*>(p.act) + (static_cast<int64_t>(g) * slots + slot) * 2 * p.K + col;
+#pragma unroll
+          for (int j = 0; j < PER; j += 4) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(src + j));
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(src + p.K + j));
+            a0[j] += u.x;
+            a0[j + 1] += u.y;
+            a0[j + 2] += u.z;
+            a0[j + 3] += u.w;
+            a1[j] += w.x;
+            a1[j + 1] += w.y;
+            a1[j + 2] += w.z;
+            a1[j + 3] += w.w;
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[j] = ok ? __fmul_rn(silu_f32(a0[j]), a1[j]) : 0.0f;
+    };
+
+    Step q = walk.begin();
+    walk.skip(q, warp - 1);
+    uint32_t step = warp - 1;
+    if (words && !walk.done(q)) load_scales(q);
+    if (PHASE == 2) grid_dep_wait();  // h is kernel 1's
+    if (!walk.done(q) && !partial) load_rows(q, 0);
+    while (!walk.done(q)) {
+      const uint32_t s = step % S, ph = (step / S) & 1;
+      if (!mbar_wait_bounded_warp(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs)) {
+        timed_out = true;
+        break;
+      }
+      const int n = ctl->cnum[q.ch], col = q.kst * C::KE + lane * PER;
+      const bool ok = col < p.K;  // K is a multiple of 16: a lane's values are all in or out
+      const uint32_t at = x_ring + s * x_bytes, av = v_ring + s * v_bytes;
+      if (words) {
+#pragma unroll
+        for (int v = 0; v < C::SPANS; ++v) sts128(s_ring + s * C::SCALE_BYTES + v * kRows * 4 + lane * 16, sc[v]);
+      }
+      if (partial) {
+        for (int i = 0; i < n; ++i) {
           float v[PER];
+          join(ctl->cstart[q.ch] + i, col, ok, v);
+          store_span<PER>(v, at + i * C::PITCH, av + i * 4, lane);
+        }
+      } else {
+        for (int first = 0; first < n; first += kBatch) {
+          if (first) load_rows(q, first);
 #pragma unroll
-          for (int j = 0; j < PER; ++j) v[j] = 0.0f;
-          if (ok) {
-            if (PHASE == 1) {
-              uint32_t w[PER / 2];
-              if (PER == 4) {
-                const uint2 d = lds64(at + lane * 8);
-                w[0] = d.x;
-                w[1] = d.y;
-              } else {
-                const uint4 d = lds128(at + lane * 16);
-                w[0] = d.x;
-                w[1] = d.y;
-                w[PER / 2 - 2] = d.z;
-                w[PER / 2 - 1] = d.w;
-              }
-#pragma unroll
-              for (int j = 0; j < PER / 2; ++j) {
-                v[2 * j] = bf16lo(w[j]);
-                v[2 * j + 1] = bf16hi(w[j]);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < PER / 4; ++j) {
-                const uint4 d = lds128(at + lane * 4 * PER + 16 * j);
-                v[4 * j] = __uint_as_float(d.x);
-                v[4 * j + 1] = __uint_as_float(d.y);
-                v[4 * j + 2] = __uint_as_float(d.z);
-                v[4 * j + 3] = __uint_as_float(d.w);
-              }
+          for (int i = 0; i < kBatch; ++i)
+            if (first + i < n) {
+              float v[PER];
+              unpack(i, ok, v);
+              store_span<PER>(v, at + (first + i) * C::PITCH, av + (first + i) * 4, lane);
             }
-          }
-          // largest finite magnitude of the span; infinities and NaN pass through
-          uint32_t m = 0;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-            m = max(m, b < 0x7F800000u ? b : 0u);
-          }
-          m = __reduce_max_sync(0xffffffffu, m);  // (all lanes have read the span, too)
-          // 2^(14 - e), e = floor(log2(m)) held at or above -100
-          const int e = max(static_cast<int>(m >> 23) - 127, -100);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-#pragma unroll
-          for (int j = 0; j < PER; ++j) v[j] = __fmul_rn(v[j], up);
-          if (PER == 4)
-            sts64(at + lane * 8, f16x2(v[0], v[1]), f16x2(v[2], v[3]));
-          else
-            sts128(at + lane * 16, make_uint4(f16x2(v[0], v[1]), f16x2(v[2], v[3]), f16x2(v[PER - 4], v[PER - 3]),
-                                              f16x2(v[PER - 2], v[PER - 1])));
-          if (lane == 0)
-            sts32f(v_ring + s * v_bytes + (sub * cap + row) * 4, __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->xfull[s]));
-        if (++s == S) {
-          s = 0;
-          ph ^= 1;
-        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->xfull[s]));
+      walk.skip(q, kConvWarps);
+      step += kConvWarps;
+      if (!walk.done(q)) {
+        if (words) load_scales(q);
+        if (!partial) load_rows(q, 0);
       }
     }
     if (timed_out) {
@@ -594,41 +669,35 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   } else {
     // ----------------------------------------------------------- contraction
     const int mw = warp - 1 - kConvWarps;
-    const int tile = mw % C::ROWTILES, sub = mw / C::ROWTILES;
     const int g = lane >> 2, t4 = lane & 3;
     // rows of the fragment: 0..7 from row A, 8..15 from row B
-    const int rowA = PHASE == 1 ? 8 * tile : 16 * tile, rowB = PHASE == 1 ? RB / 2 + 8 * tile : 16 * tile + 8;
+    const int rowA = PHASE == 1 ? 8 * mw : 16 * mw, rowB = PHASE == 1 ? kRows / 2 + 8 * mw : 16 * mw + 8;
     const int lrow = ((lane >> 3) & 1 ? rowB : rowA) + (lane & 7);  // the row this lane addresses for ldmatrix
-    const uint32_t w_off = sub * RB * 128 + lrow * 128, swz = (lrow & 7) * 16;
-    const uint32_t x_off = g * C::PITCH + sub * C::KE * C::ES + t4 * (WT == kMx4 ? 16 : 8);
-    const uint32_t s_off = sub * C::SPANS * RB * 4;
+    const uint32_t w_off = lrow * 128, swz = (lrow & 7) * 16;
+    const uint32_t x_off = g * C::PITCH + t4 * (WT == kMx4 ? 16 : 8);
+    const int slots = ctl->cstart[nchunk > 0 ? nchunk - 1 : 0] + ctl->cnum[nchunk > 0 ? nchunk - 1 : 0];
     uint32_t s = 0, ph = 0;
-    int parity = 0;
     if (PHASE == 2) grid_dep_wait();  // before o and the counters are touched
 
-    auto unit = [&](auto nt_tag, int ch, int blk) {
+    auto unit = [&](auto nt_tag, const Step& q) {
       constexpr int NT = decltype(nt_tag)::value;
       float acc[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-      for (int kst = 0; kst < nst && !timed_out; ++kst) {
-        if (!mbar_wait_bounded_warp(smem_u32(&ctl->full[s]), ph, abort_flag, kWaitLimitNs) ||
-            !mbar_wait_bounded_warp(smem_u32(&ctl->xfull[s]), ph, abort_flag, kWaitLimitNs)) {
+      for (int kst = q.kst; kst < q.end && !timed_out; ++kst) {
+        if (!mbar_wait_bounded_warp(smem_u32(&ctl->xfull[s]), ph, abort_flag, kWaitLimitNs) ||
+            !mbar_wait_bounded_warp(smem_u32(&ctl->full[s]), ph, abort_flag, kWaitLimitNs)) {
           timed_out = true;
           *abort_flag = 1;
           break;
         }
-        const int left = p.K - (kst * C::SUBS + sub) * C::KE;
-        const int nch = min(8, left / C::KC);  // K is a multiple of 16 (e2m1: 128): whole chunks
-        if (nch > 0) {
-          const uint32_t st = s_ring + s * C::SCALE_BYTES + s_off;
-          Mma<WT, PHASE, RB, NT>::sub_tile(acc, base + s * kStageW + w_off, swz, x_ring + s * x_bytes + x_off,
-                                           8 * C::PITCH, nch, st + (rowA + g) * 4, st + (rowB + g) * 4,
-                                           v_ring + s * v_bytes + sub * cap * 4 + t4 * 8, p.mode);
-        }
-        fence_proxy_async_smem();  // this warp's reads of the stage before the next copies into it
+        const int nch = min(8, (p.K - kst * C::KE) / C::KC);  // K is a multiple of 16 (e2m1: 128): whole chunks
+        const uint32_t st = s_ring + s * C::SCALE_BYTES;
+        contract<WT, NT>(acc, base + s * kStageW + w_off, swz, x_ring + s * x_bytes + x_off, nch, st + (rowA + g) * 4,
+                         st + (rowB + g) * 4, v_ring + s * v_bytes + t4 * 8, p.mode == kScaleBlock);
+        fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
         if (++s == S) {
@@ -636,87 +705,80 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           ph ^= 1;
         }
       }
-      if (C::SUBS > 1) {  // the spans of K meet in ascending order
-        float4* r4 = reinterpret_cast<float4*>(red) + parity * kMmaWarps * 32;
-        r4[mw * 32 + lane] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
-        named_barrier_sync(1, kMmaWarps * 32);
-        if (sub == 0) {
-#pragma unroll
-          for (int q = 1; q < C::SUBS; ++q) {
-            const float4 v = r4[(q * C::ROWTILES + tile) * 32 + lane];
-            acc[0][0] += v.x;
-            acc[0][1] += v.y;
-            acc[0][2] += v.z;
-            acc[0][3] += v.w;
-          }
-        }
-        parity ^= 1;  // the other half is free: every warp has passed this barrier since it was read
+      const int e = ctl->cexp[q.ch], n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
+      const int ca = q.blk * kPer + (PHASE == 1 ? 8 * mw : 16 * mw) + g;  // channel of row A
+      const int cb = PHASE == 1 ? ca : ca + 8;
+      float fa = 1.0f, fb = 1.0f;
+      if (p.mode == kScaleChannel) {
+        const float* sc = p.scale + static_cast<int64_t>(e) * (PHASE == 1 ? 2 * p.N : p.N);
+        if (ca < p.N) fa = __ldg(sc + ca);
+        if (cb < p.N) fb = __ldg(sc + (PHASE == 1 ? p.N : 0) + cb);
+      } else if (p.mode == kScaleTensor) {
+        fa = fb = __ldg(p.scale);
       }
-      if (sub == 0) {
-        const int e = ctl->cexp[ch], n = ctl->cnum[ch], st = ctl->cstart[ch];
-        const int ca = blk * rows_per + (PHASE == 1 ? 8 * tile : 16 * tile) + g;  // channel of row A
-        const int cb = PHASE == 1 ? ca : ca + 8;
-        float fa = 1.0f, fb = 1.0f;
-        if (p.mode == kScaleChannel) {
-          const float* sc = p.scale + static_cast<int64_t>(e) * (PHASE == 1 ? 2 * p.N : p.N);
-          if (ca < p.N) fa = __ldg(sc + ca);
-          if (cb < p.N) fb = __ldg(sc + (PHASE == 1 ? p.N : 0) + cb);
-        } else if (p.mode == kScaleTensor) {
-          fa = fb = __ldg(p.scale);
-        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int col = nt * 8 + 2 * t4 + j;
-            if (col < n) {
-              const float va = acc[nt][j] * fa, vb = acc[nt][2 + j] * fb;
-              float* o = p.out + static_cast<int64_t>(st + col) * p.N;
-              if (PHASE == 1) {
-                if (ca < p.N) o[ca] = silu_f32(va) * vb;
-              } else {
-                if (ca < p.N) o[ca] = va;
-                if (cb < p.N) o[cb] = vb;
-              }
+        for (int j = 0; j < 2; ++j) {
+          const int col = nt * 8 + 2 * t4 + j;
+          if (col >= n) continue;
+          const float va = acc[nt][j] * fa, vb = acc[nt][2 + j] * fb;
+          if (PHASE == 1) {
+            if (ca >= p.N) continue;
+            if (walk.segs == 1) {
+              p.out[static_cast<int64_t>(st + col) * p.N + ca] = __fmul_rn(silu_f32(va), vb);
+            } else {
+              float* o = p.out + (static_cast<int64_t>(q.seg) * slots + st + col) * 2 * p.N;
+              o[ca] = va;
+              o[p.N + ca] = vb;
             }
+          } else {
+            float* o = p.out + (static_cast<int64_t>(q.seg) * slots + st + col) * p.N;
+            if (ca < p.N) o[ca] = va;
+            if (cb < p.N) o[cb] = vb;
           }
-      }
+        }
     };
 
     // (a warp that gave up waiting still walks the units, without waits: the
     // other warps count on it at the barriers)
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-      const int blk = u / nchunk, ch = u - blk * nchunk;
-      const int n = ctl->cnum[ch];
-      if (RB == 32 || n <= 8)
-        unit(std::integral_constant<int, 1>{}, ch, blk);
+    for (Step q = walk.begin(); !walk.done(q);) {
+      const int n = ctl->cnum[q.ch];
+      if (n <= 8)
+        unit(std::integral_constant<int, 1>{}, q);
       else if (n <= 16)
-        unit(std::integral_constant<int, RB == 32 ? 1 : 2>{}, ch, blk);
+        unit(std::integral_constant<int, 2>{}, q);
       else
-        unit(std::integral_constant<int, RB == 32 ? 1 : 4>{}, ch, blk);
+        unit(std::integral_constant<int, 4>{}, q);
       if (PHASE == 2) {
         // the block's last unit (over all CTAs) sums its pairs into y
         __threadfence();
         named_barrier_sync(1, kMmaWarps * 32);
-        if (mw == 0 && lane == 0) ctl->last = atomicAdd(p.count + blk, 1u) == static_cast<unsigned>(nchunk - 1);
+        if (mw == 0 && lane == 0)
+          ctl->last = atomicAdd(p.count + q.blk, 1u) == static_cast<unsigned>(nchunk * walk.segs - 1);
         named_barrier_sync(1, kMmaWarps * 32);
         if (ctl->last) {
           __threadfence();
-          const int th = mw * 32 + lane, d0 = blk * RB;
-          for (int i = th; i < p.T * RB; i += kMmaWarps * 32) {
-            const int t = i / RB, d = d0 + i % RB;
+          const int th = mw * 32 + lane, d0 = q.blk * kRows;
+          for (int i = th; i < p.T * kRows; i += kMmaWarps * 32) {
+            const int t = i / kRows, d = d0 + i % kRows;
             if (d >= p.N) continue;
             float a = 0.0f;
             for (int j = 0; j < p.k; ++j) {
-              const int q = t * p.k + j;
-              if (ctl->pos[q] == 0xFFFF) continue;
-              const float w = p.topk_w ? __ldg(p.topk_w + q) : 1.0f;
-              a = __fmaf_rn(w, __ldcg(p.out + static_cast<int64_t>(ctl->pos[q]) * p.N + d), a);
+              const int pr = t * p.k + j;
+              if (ctl->pos[pr] == 0xFFFF) continue;
+              const float w = p.topk_w ? __ldg(p.topk_w + pr) : 1.0f;
+              float o = 0.0f;
+              for (int sg = 0; sg < walk.segs; ++sg)
+                o += __ldcg(p.out + (static_cast<int64_t>(sg) * slots + ctl->pos[pr]) * p.N + d);
+              a = __fmaf_rn(w, o, a);
             }
             p.y[static_cast<int64_t>(t) * p.N + d] = static_cast<uint16_t>(pack_bf16x2(a, 0.0f) & 0xFFFFu);
           }
         }
       }
+      q.u += gridDim.x;
+      if (!walk.done(q)) walk.open(q);
     }
     if (timed_out) {
       *abort_flag = 1;
@@ -740,40 +802,62 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Weight rows as bytes: boxes of box_rows x 128 bytes, 128-byte swizzle;
-// reads past the extents return zeros.
-bool make_map(CUtensorMap* m, const void* ptr, uint64_t bytes, uint64_t rows, uint32_t box_rows) {
+// The weights as bytes [slabs][rows][bytes] (wi: two slabs of F rows an
+// expert; wo: one of D rows), boxes of 128 bytes x box_rows x box_slabs with
+// the 128-byte swizzle; reads past the extents return zeros.
+bool make_map(CUtensorMap* m, const void* ptr, uint64_t bytes, uint64_t rows, uint64_t slabs, uint32_t box_rows,
+              uint32_t box_slabs) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {bytes, rows}, strides[1] = {bytes};
-  cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  cuuint64_t dims[3] = {bytes, rows, slabs}, strides[2] = {bytes, bytes * rows};
+  cuuint32_t box[3] = {128, box_rows, box_slabs}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int WT, int PHASE, int RB>
-moe_status launch(const void* w, Params p, int sms, cudaStream_t st) {
-  using C = Cfg<WT, PHASE, RB>;
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+int64_t blocks(int64_t n, int64_t per) { return (n + per - 1) / per; }
+
+// Segments of K at most: their sums take workspace, and only a few pairs need them.
+int max_segs(int64_t R) {
+  const int64_t s = R > 0 ? 128 / R : 1;
+  return static_cast<int>(s < 1 ? 1 : (s > kMaxSegs ? kMaxSegs : s));
+}
+
+// Workspace: h fp32 [R, F] or partial a [segs][R, 2F] | o fp32 [segs][R, D] |
+// a counter for every block of output columns, each part 256-byte aligned.
+int64_t h_bytes(int64_t R, int64_t F) {
+  const int64_t s = max_segs(R);
+  return align256(R * F * 4 * (s > 1 ? 2 * s : 1));
+}
+int64_t o_bytes(int64_t R, int64_t D) { return align256(R * D * 4 * max_segs(R)); }
+
+bool shape_ok(int64_t T, int k, int64_t D, int64_t F) {
+  return T >= 0 && T <= kMaxTokens && k > 0 && k <= 32 && T * k <= kMaxPairs && D > 0 && F > 0 && D % 16 == 0 &&
+         F % 16 == 0 && D <= 32768 && F <= 32768;
+}
+
+template <int WT, int PHASE>
+moe_status launch(const void* w, Params p, int grid, cudaStream_t st) {
+  using C = Cfg<WT>;
   CUtensorMap tm;
   const uint64_t bytes = WT == kMx4 ? p.K / 2 : p.K;
-  if (!make_map(&tm, w, bytes, static_cast<uint64_t>(p.El) * (PHASE == 1 ? 2 : 1) * p.N, PHASE == 1 ? RB / 2 : RB))
+  if (!make_map(&tm, w, bytes, p.N, static_cast<uint64_t>(p.El) * (PHASE == 1 ? 2 : 1), PHASE == 1 ? kRows / 2 : kRows,
+                PHASE == 1 ? 2 : 1))
     return MOE_ERR_CUDA;
-  p.cap = RB == 32 || p.T <= 8 ? 8 : (p.T <= 16 ? 16 : 32);
-  const size_t stage = kStageW + static_cast<size_t>(p.cap) * C::PITCH + C::SCALE_BYTES + C::SUBS * p.cap * 4;
-  const size_t fixed = 1024 + kCtlBytes + C::RED_BYTES;
+  const size_t stage = kStageW + static_cast<size_t>(p.cap) * (C::PITCH + 4) + C::SCALE_BYTES;
+  const size_t fixed = 1024 + kCtlBytes;
   p.stages = static_cast<int>((kSmemLimit - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = fixed + p.stages * stage;
-  auto kernel = decode_kernel<WT, PHASE, RB>;
+  auto kernel = decode_kernel<WT, PHASE>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  const int per = PHASE == 1 ? RB / 2 : RB;
-  const int64_t units = static_cast<int64_t>(p.T) * p.k * ((p.N + per - 1) / per);  // at most: a chunk a pair
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -783,29 +867,14 @@ moe_status launch(const void* w, Params p, int sms, cudaStream_t st) {
   return MOE_OK;
 }
 
-template <int WT, int PHASE>
-moe_status launch_rb(const void* w, const Params& p, int rb, int sms, cudaStream_t st) {
-  return rb == 32 ? launch<WT, PHASE, 32>(w, p, sms, st) : launch<WT, PHASE, 128>(w, p, sms, st);
-}
-
 template <int PHASE>
-moe_status launch_type(int wt, const void* w, const Params& p, int rb, int sms, cudaStream_t st) {
+moe_status launch_type(int wt, const void* w, const Params& p, int grid, cudaStream_t st) {
   switch (wt) {
-    case kE4M3: return launch_rb<kE4M3, PHASE>(w, p, rb, sms, st);
-    case kInt8: return launch_rb<kInt8, PHASE>(w, p, rb, sms, st);
-    case kMx8: return launch_rb<kMx8, PHASE>(w, p, rb, sms, st);
-    default: return launch_rb<kMx4, PHASE>(w, p, rb, sms, st);
+    case kE4M3: return launch<kE4M3, PHASE>(w, p, grid, st);
+    case kInt8: return launch<kInt8, PHASE>(w, p, grid, st);
+    case kMx8: return launch<kMx8, PHASE>(w, p, grid, st);
+    default: return launch<kMx4, PHASE>(w, p, grid, st);
   }
-}
-
-// Workspace: h fp32 [R, F] | o fp32 [R, D] | a counter for every 32 output
-// columns, each part 256-byte aligned.
-int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
-int64_t counters(int64_t D) { return (D + 31) / 32; }
-
-bool shape_ok(int64_t T, int k, int64_t D, int64_t F) {
-  return T >= 0 && T <= kMaxTokens && k > 0 && k <= 32 && T * k <= kMaxPairs && D > 0 && F > 0 && D % 16 == 0 &&
-         F % 16 == 0 && D <= 32768 && F <= 32768;
 }
 
 // Scale mode of one weight tensor in the kernel's terms, -1 if it is not taken.
@@ -831,7 +900,7 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_take_err
 
 extern "C" size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F) {
   if (!shape_ok(T, k, D, F)) return 0;
-  return static_cast<size_t>(align256(T * k * F * 4) + align256(T * k * D * 4) + align256(counters(D) * 4));
+  return static_cast<size_t>(h_bytes(T * k, F) + o_bytes(T * k, D) + align256(blocks(D, kRows) * 4));
 }
 
 extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int k,
@@ -865,28 +934,33 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int64_t R = T * k;
   float* h = reinterpret_cast<float*>(ws);
-  float* o = reinterpret_cast<float*>(ws + align256(R * F * 4));
-  unsigned int* count = reinterpret_cast<unsigned int*>(ws + align256(R * F * 4) + align256(R * D * 4));
+  float* o = reinterpret_cast<float*>(ws + h_bytes(R, F));
+  const int ke = type == MOE_WEIGHT_MXFP4 ? 256 : 128;
   Params p{};
   p.ids = topk_ids;
   p.topk_w = topk_w;
   p.y = y;
-  p.count = count;
-  p.ncount = static_cast<int>(counters(D));
+  p.count = reinterpret_cast<unsigned int*>(ws + h_bytes(R, F) + o_bytes(R, D));
+  p.ncount = static_cast<int>(blocks(D, kRows));
   p.T = static_cast<int>(T);
   p.k = k;
   p.E = E;
   p.g0 = group_offset;
   p.El = E_local;
-  const int64_t active = R < E_local ? R : E_local;
+  p.cap = T <= 8 ? 8 : (T <= 16 ? 16 : 32);
+  p.smax = max_segs(R);
+  p.nblock1 = static_cast<int>(blocks(F, kRows / 2));
+  p.nst1 = static_cast<int>(blocks(D, ke));
+  // no more CTAs than units (a chunk a pair, all segments)
+  const int64_t u1 = R * p.nblock1 * p.smax, u2 = R * p.ncount * p.smax;
+  p.grid1 = static_cast<int>(u1 < sms ? u1 : sms);
   p.act = x;
   p.scale = static_cast<const float*>(s_in);
   p.out = h;
   p.K = static_cast<int>(D);
   p.N = static_cast<int>(F);
   p.mode = kin;
-  const int rb1 = T <= 8 && active * ((F + 63) / 64) < 8ll * sms ? 32 : 128;
-  moe_status s = launch_type<1>(type, w_in, p, rb1, sms, st);
+  moe_status s = launch_type<1>(type, w_in, p, p.grid1, st);
   if (s != MOE_OK) return s;
   p.act = h;
   p.scale = static_cast<const float*>(s_out);
@@ -894,6 +968,5 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   p.K = static_cast<int>(F);
   p.N = static_cast<int>(D);
   p.mode = kout;
-  const int rb2 = T <= 8 && active * ((D + 127) / 128) < 8ll * sms ? 32 : 128;
-  return launch_type<2>(type, w_out, p, rb2, sms, st);
+  return launch_type<2>(type, w_out, p, static_cast<int>(u2 < sms ? u2 : sms), st);
 }

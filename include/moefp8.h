@@ -624,8 +624,9 @@ moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const floa
                           moe_scale_mode out_mode, uint16_t* y, void* workspace, size_t workspace_bytes,
                           moe_stream_t stream);
 
-/* Bytes of moe_ffn_decode's workspace: 4 T k (D + F) and a little (0 for a
- * shape that the call refuses). */
+/* Bytes of moe_ffn_decode's workspace (0 for a shape that the call refuses):
+ * 4 T k (D + F) and a little, or, for fewer than 128 pairs, about 512 (D + 2 F)
+ * at most (sums of segments of K). */
 size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F);
 
 #ifdef __cplusplus
