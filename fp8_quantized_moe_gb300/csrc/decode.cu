@@ -105,9 +105,11 @@ struct Ctl {
 template <int WT>
 struct Cfg {
   static constexpr int KE = WT == kMx4 ? 256 : 128;  // values of K in a stage (128 bytes of weights a row)
-  static constexpr int KC = KE / 8;                  // and in a 16-byte chunk
   static constexpr int SPANS = KE / 128;             // scale words of a row and stage
-  static constexpr int SCALE_BYTES = SPANS * kRows * 4;
+  static constexpr bool MX = WT == kMx8 || WT == kMx4;
+  // a row's scales of a stage: one float a span, or (MX) its four blocks' floats a span
+  static constexpr int SCALE_ROW = MX ? 16 : 4;
+  static constexpr int SCALE_BYTES = SPANS * kRows * SCALE_ROW;
   // bytes of an f16 activation row; the padding keeps eight rows' fragments in different banks
   static constexpr int PITCH = KE * 2 + (WT == kMx4 ? 64 : 32);
   static constexpr int PER = KE / 32;  // values of a span a lane converts
@@ -141,7 +143,7 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -277,89 +279,123 @@ __device__ void build_chunks(const Params& p, Ctl* c) {
   }
 }
 
-// One stage: 16 rows x nch 16-byte chunks (at most 8) of weights at `wt` (row
-// A + lane / 4 and row B + lane / 4 of the fragment), activations at `xb`
-// (already this lane's), the weights' scale words of this lane's two rows at
-// sA, sB and the activations' span scales at `xs`.
+// One stage: 16 rows x 128 bytes of weights at `wt` (row A + lane / 4 and row
+// B + lane / 4 of the fragment), activations at `xb` (already this lane's), the
+// scales of this lane's two weight rows at sA, sB and the activations' span
+// scales at `xs`.  Past the end of K both the weights and the activations are
+// zeros.  The shared-memory loads run DEPTH pairs of 16-byte chunks ahead of
+// the products (all of them at NT <= 2): taken as they were needed, their
+// latencies made a stage 1.7 times as long.
 template <int WT, int NT>
-__device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t wt, uint32_t swz, uint32_t xb, int nch,
-                                         uint32_t sA, uint32_t sB, uint32_t xs, bool block_scale) {
+__device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t wt, uint32_t swz, uint32_t xb, uint32_t sA,
+                                         uint32_t sB, uint32_t xs, bool block_scale) {
   using C = Cfg<WT>;
-  constexpr bool MX = WT == kMx8 || WT == kMx4;
+  constexpr int DEPTH = WT == kMx4 ? (NT == 1 ? 4 : (NT == 2 ? 2 : 1)) : (NT <= 2 ? 4 : 2);
+  constexpr int BW = WT == kMx4 ? 4 : 2;  // words of a chunk's activation fragment
+  const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
+  uint32_t r[4][4];
+  uint32_t b[DEPTH][2][NT][BW];
+  auto load_b = [&](int c) {
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (WT == kMx4) {
+          const uint4 v = lds128(xb + n * 8 * C::PITCH + (2 * c + cc) * 64);
+          b[c % DEPTH][cc][n][0] = v.x;
+          b[c % DEPTH][cc][n][1] = v.y;
+          b[c % DEPTH][cc][n][BW - 2] = v.z;
+          b[c % DEPTH][cc][n][BW - 1] = v.w;
+        } else {
+          const uint2 v = lds64(xb + n * 8 * C::PITCH + (2 * c + cc) * 32);
+          b[c % DEPTH][cc][n][0] = v.x;
+          b[c % DEPTH][cc][n][1] = v.y;
+        }
+      }
+  };
+#pragma unroll
+  for (int c = 0; c < 4; ++c) ldmatrix_x4(wt + (((2 * c + hi) * 16) ^ swz), r[c]);
+#pragma unroll
+  for (int c = 0; c < DEPTH; ++c) load_b(c);
+  float fA[4] = {1.0f, 1.0f, 1.0f, 1.0f}, fB[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+  auto load_f = [&](int v) {
+    const uint4 a = lds128(sA + v * kRows * 16), d = lds128(sB + v * kRows * 16);
+    fA[0] = __uint_as_float(a.x);
+    fA[1] = __uint_as_float(a.y);
+    fA[2] = __uint_as_float(a.z);
+    fA[3] = __uint_as_float(a.w);
+    fB[0] = __uint_as_float(d.x);
+    fB[1] = __uint_as_float(d.y);
+    fB[2] = __uint_as_float(d.z);
+    fB[3] = __uint_as_float(d.w);
+  };
+  if (C::MX) {
+    load_f(0);
+  } else if (block_scale) {
+    fA[0] = __uint_as_float(lds32(sA));
+    fB[0] = __uint_as_float(lds32(sB));
+  }
+  uint2 xv[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xv[n] = lds64(xs + n * 32);
+
   // two chains of sums (MX: the sum of the scaled 32-wide blocks, and the block at hand)
   float s0[NT][4], s1[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s0[n][i] = s1[n][i] = 0.0f;
-  const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
-  uint32_t wA = 0, wB = 0;
+  auto fold = [&](float fa, float fb) {
 #pragma unroll
-  for (int c = 0; c < 8; c += 2) {
-    if (c >= nch) break;
-    if (MX && (c == 0 || (WT == kMx4 && c == 4))) {
-      wA = lds32(sA + (c == 4 ? kRows * 4 : 0));
-      wB = lds32(sB + (c == 4 ? kRows * 4 : 0));
+    for (int n = 0; n < NT; ++n) {
+      s0[n][0] = __fmaf_rn(s1[n][0], fa, s0[n][0]);
+      s0[n][1] = __fmaf_rn(s1[n][1], fa, s0[n][1]);
+      s0[n][2] = __fmaf_rn(s1[n][2], fb, s0[n][2]);
+      s0[n][3] = __fmaf_rn(s1[n][3], fb, s0[n][3]);
+      s1[n][0] = s1[n][1] = s1[n][2] = s1[n][3] = 0.0f;
     }
-    uint32_t r[4];
-    ldmatrix_x4(wt + (((c + hi) * 16) ^ swz), r);
+  };
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (WT == kMx4 && c == 2) load_f(1);
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc) {
-      if (!MX && c + cc >= nch) break;
       if (WT == kMx4) {
         uint32_t va[4], vb[4];
-        weights8(r[2 * cc], va);
-        weights8(r[2 * cc + 1], vb);
+        weights8(r[c][2 * cc], va);
+        weights8(r[c][2 * cc + 1], vb);
         const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]}, a1[4] = {va[2], vb[2], va[3], vb[3]};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 b = lds128(xb + n * 8 * C::PITCH + (c + cc) * 64);
-          mma_f16(s1[n], a0, b.x, b.y);
-          mma_f16(s1[n], a1, b.z, b.w);
+          mma_f16(s1[n], a0, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
+          mma_f16(s1[n], a1, b[c % DEPTH][cc][n][BW - 2], b[c % DEPTH][cc][n][BW - 1]);
         }
+        fold(fA[(2 * c + cc) & 3], fB[(2 * c + cc) & 3]);
       } else {
         uint32_t a[4];
-        weights4<WT>(r[2 * cc], a[0], a[2]);
-        weights4<WT>(r[2 * cc + 1], a[1], a[3]);
+        weights4<WT>(r[c][2 * cc], a[0], a[2]);
+        weights4<WT>(r[c][2 * cc + 1], a[1], a[3]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint2 b = lds64(xb + n * 8 * C::PITCH + (c + cc) * 32);
-          mma_f16(MX || cc == 1 ? s1[n] : s0[n], a, b.x, b.y);
-        }
-      }
-      if (WT == kMx4 || (WT == kMx8 && cc == 1)) {  // a 32-wide block is done: its scales
-        const int b = WT == kMx4 ? (c + cc) & 3 : c / 2;
-        const float fa = e8m0_value((wA >> (8 * b)) & 0xFFu), fb = e8m0_value((wB >> (8 * b)) & 0xFFu);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          s0[n][0] = __fmaf_rn(s1[n][0], fa, s0[n][0]);
-          s0[n][1] = __fmaf_rn(s1[n][1], fa, s0[n][1]);
-          s0[n][2] = __fmaf_rn(s1[n][2], fb, s0[n][2]);
-          s0[n][3] = __fmaf_rn(s1[n][3], fb, s0[n][3]);
-          s1[n][0] = s1[n][1] = s1[n][2] = s1[n][3] = 0.0f;
-        }
+        for (int n = 0; n < NT; ++n)
+          mma_f16(C::MX || cc == 1 ? s1[n] : s0[n], a, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
+        if (C::MX && cc == 1) fold(fA[c], fB[c]);  // a 32-wide block is done
       }
     }
-  }
-  float fa = 1.0f, fb = 1.0f;
-  if (!MX && block_scale) {
-    fa = __uint_as_float(lds32(sA));
-    fb = __uint_as_float(lds32(sB));
+    if (c + DEPTH < 4) load_b(c + DEPTH);
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const uint2 v = lds64(xs + n * 32);
-    const float x0 = __uint_as_float(v.x), x1 = __uint_as_float(v.y);
-    if (MX) {
+    const float x0 = __uint_as_float(xv[n].x), x1 = __uint_as_float(xv[n].y);
+    if (C::MX) {
       acc[n][0] = __fmaf_rn(s0[n][0], x0, acc[n][0]);
       acc[n][1] = __fmaf_rn(s0[n][1], x1, acc[n][1]);
       acc[n][2] = __fmaf_rn(s0[n][2], x0, acc[n][2]);
       acc[n][3] = __fmaf_rn(s0[n][3], x1, acc[n][3]);
     } else {
-      acc[n][0] = __fmaf_rn(s0[n][0] + s1[n][0], x0 * fa, acc[n][0]);
-      acc[n][1] = __fmaf_rn(s0[n][1] + s1[n][1], x1 * fa, acc[n][1]);
-      acc[n][2] = __fmaf_rn(s0[n][2] + s1[n][2], x0 * fb, acc[n][2]);
-      acc[n][3] = __fmaf_rn(s0[n][3] + s1[n][3], x1 * fb, acc[n][3]);
+      acc[n][0] = __fmaf_rn(s0[n][0] + s1[n][0], x0 * fA[0], acc[n][0]);
+      acc[n][1] = __fmaf_rn(s0[n][1] + s1[n][1], x1 * fA[0], acc[n][1]);
+      acc[n][2] = __fmaf_rn(s0[n][2] + s1[n][2], x0 * fB[0], acc[n][2]);
+      acc[n][3] = __fmaf_rn(s0[n][3] + s1[n][3], x1 * fB[0], acc[n][3]);
     }
   }
 }
@@ -566,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
       for (int v = 0; v < C::SPANS; ++v) {
         const int64_t kb = q.kst * C::SPANS + v;
+        sc[v] = make_uint4(0, 0, 0, 0);  // (past the end of K)
         if (kb < nkb) {
           const float* src = p.mode == kScaleMx ? p.scale + kb * (p.El * scale_rows) + e * scale_rows + n0
                                                 : p.scale + (e * static_cast<int64_t>(nkb) + kb) * scale_rows + n0;
@@ -633,7 +670,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       const uint32_t at = x_ring + s * x_bytes, av = v_ring + s * v_bytes;
       if (words) {
 #pragma unroll
-        for (int v = 0; v < C::SPANS; ++v) sts128(s_ring + s * C::SCALE_BYTES + v * kRows * 4 + lane * 16, sc[v]);
+        for (int v = 0; v < C::SPANS; ++v) {
+          const uint32_t dst = s_ring + s * C::SCALE_BYTES + (v * kRows + lane * 4) * C::SCALE_ROW;
+          if (C::MX) {  // four rows' four codes each, as floats
+            const uint32_t w[4] = {sc[v].x, sc[v].y, sc[v].z, sc[v].w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float f[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) f[b] = e8m0_value((w[r] >> (8 * b)) & 0xFFu);
+              sts128(dst + r * 16, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                              __float_as_uint(f[3])));
+            }
+          } else {
+            sts128(dst, sc[v]);
+          }
+        }
       }
       if (partial) {
         for (int i = 0; i < n; ++i) {
@@ -693,10 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           *abort_flag = 1;
           break;
         }
-        const int nch = min(8, (p.K - kst * C::KE) / C::KC);  // K is a multiple of 16 (e2m1: 128): whole chunks
         const uint32_t st = s_ring + s * C::SCALE_BYTES;
-        contract<WT, NT>(acc, base + s * kStageW + w_off, swz, x_ring + s * x_bytes + x_off, nch, st + (rowA + g) * 4,
-                         st + (rowB + g) * 4, v_ring + s * v_bytes + t4 * 8, p.mode == kScaleBlock);
+        contract<WT, NT>(acc, base + s * kStageW + w_off, swz, x_ring + s * x_bytes + x_off,
+                         st + (rowA + g) * C::SCALE_ROW, st + (rowB + g) * C::SCALE_ROW, v_ring + s * v_bytes + t4 * 8,
+                         p.mode == kScaleBlock);
         fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
