@@ -30,14 +30,14 @@
 // Roles: warp 0 moves the weights, one TMA box of 128 rows x 128 bytes a
 // stage.  One copy instruction a stage and no more: a stream of single 16 KB
 // boxes runs at 7.2 TB/s here, with four small bulk copies beside each (rows
-// of activations, scales) at 5.1.  So warps 1..4 fetch those themselves, each
-// every fourth stage, the next one's loads in flight while it waits: they
+// of activations, scales) at 5.1.  So warps 1..3 fetch those themselves, each
+// every third stage, the next one's loads in flight while it waits: they
 // store the stage's weight scale words, and its activations as f16, each
 // (row, 128-byte span of the weights) scaled by the power of two that puts its
 // largest value in [2^14, 2^15): f16 then holds every bf16 value to within
 // 2^-39 of the span's largest, and h to 2^-12 relative (against 2^-9 of the
 // result's bf16).
-// Warps 5..12 contract, 16 weight rows each: ldmatrix brings 16 rows x 32
+// Warps 4..11 contract, 16 weight rows each: ldmatrix brings 16 rows x 32
 // bytes of weights, one conversion makes two f16 weights (exact for e4m3, int8
 // and e2m1, NaN codes included), and mma.m16n8k16 multiplies them with eight
 // tokens.  The tensor core is nowhere near its limit, so the plain warp-wide
@@ -60,7 +60,7 @@ namespace {
 
 __device__ unsigned int g_err;
 
-constexpr int kConvWarps = 4, kMmaWarps = 8;
+constexpr int kConvWarps = 3, kMmaWarps = 8;
 constexpr int kThreads = 32 * (1 + kConvWarps + kMmaWarps);
 constexpr int kRows = 128;              // weight rows of a unit
 constexpr int kStageW = kRows * 128;    // weight bytes of a stage
@@ -70,6 +70,7 @@ constexpr int kMaxPairs = 1024;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 1024;
 constexpr int kSmemLimit = 232448;
+constexpr int kSmemHalf = 115712;  // two CTAs an SM (228 KB, 1 KB of it reserved for each)
 
 enum { kE4M3 = 0, kInt8 = 1, kMx8 = 2, kMx4 = 3 };
 enum { kScaleChannel = 0, kScaleBlock = 1, kScaleTensor = 2, kScaleMx = 3 };
@@ -81,7 +82,7 @@ struct Params {
   const float* scale;  // fp32 scales, or the MX scale words
   float* out;          // PHASE 1: h [slots, N], or partial a [segs][slots, 2N]; PHASE 2: o [segs][slots, N]
   uint16_t* y;
-  unsigned int* count;  // finished units of every block of output rows (PHASE 1 clears them)
+  unsigned int* count;  // finished units of every 16 output columns (PHASE 1 clears them)
   int ncount;
   int T, k, E, g0, El;
   int K, N;  // N: channels (PHASE 1: F, PHASE 2: D)
@@ -92,17 +93,19 @@ struct Params {
   int nblock1, nst1;  // row blocks and K stages of kernel 1
 };
 
+// SMALL: T <= 8, so at most 256 pairs and chunks of eight.
+template <bool SMALL>
 struct Ctl {
-  uint64_t full[kMaxStages], xfull[kMaxStages], empty[kMaxStages];
-  int abort_flag, no_abort, err, nchunk, last;
-  int pad[3];
-  uint16_t pos[kMaxPairs];     // slot of pair i (pairs sorted by expert), 0xFFFF: not local
-  uint16_t order[kMaxPairs];   // pair of slot s
-  uint16_t cexp[kMaxPairs], cstart[kMaxPairs], cnum[kMaxPairs];
+  static constexpr int PAIRS = SMALL ? 256 : kMaxPairs;
+  uint64_t full[kMaxStages], xraw[kMaxStages], xfull[kMaxStages], empty[kMaxStages];
+  int abort_flag, no_abort, err, nchunk;
+  uint16_t pos[PAIRS];     // slot of pair i (pairs sorted by expert), 0xFFFF: not local
+  uint16_t order[PAIRS];   // pair of slot s
+  uint16_t cexp[PAIRS], cstart[PAIRS], cnum[PAIRS];
   uint16_t num[kMaxExperts];
 };
 
-template <int WT>
+template <int WT, int PHASE>
 struct Cfg {
   static constexpr int KE = WT == kMx4 ? 256 : 128;  // values of K in a stage (128 bytes of weights a row)
   static constexpr int SPANS = KE / 128;             // scale words of a row and stage
@@ -110,9 +113,11 @@ struct Cfg {
   // a row's scales of a stage: one float a span, or (MX) its four blocks' floats a span
   static constexpr int SCALE_ROW = MX ? 16 : 4;
   static constexpr int SCALE_BYTES = SPANS * kRows * SCALE_ROW;
-  // bytes of an f16 activation row; the padding keeps eight rows' fragments in different banks
-  static constexpr int PITCH = KE * 2 + (WT == kMx4 ? 64 : 32);
   static constexpr int PER = KE / 32;  // values of a span a lane converts
+  // bytes of an activation row as it arrives (bf16 x, fp32 h; the f16 form takes
+  // the front of its place), padded so that eight rows' fragments lie in different banks
+  static constexpr int ROW_BYTES = KE * (PHASE == 1 ? 2 : 4);
+  static constexpr int PITCH = ROW_BYTES + (WT == kMx4 ? 64 : 32);
 };
 
 // How many segments of K: the fewest stages on the busiest CTA, a unit's
@@ -130,7 +135,10 @@ __device__ __forceinline__ int pick_segs(int units, int nst, int grid, int smax)
   return best;
 }
 
-constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
+template <bool SMALL>
+constexpr size_t ctl_bytes() {
+  return (sizeof(Ctl<SMALL>) + 127) / 128 * 128;
+}
 
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -176,6 +184,15 @@ __device__ __forceinline__ void sts32f(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
+// 16-byte asynchronous copy; with src_bytes 0 the destination is zero-filled.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// One of the barrier's arrivals, made when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -218,13 +235,60 @@ __device__ __forceinline__ void weights8(uint32_t w, uint32_t (&v)[4]) {
 }
 
 // ---- the pairs by expert ---------------------------------------------------
-// A stable counting sort by warp 0: 32 pairs at a time, the rank of a pair
-// among its expert's earlier ones from a warp-wide match and a running count.
-// Every CTA of both kernels gets the same tables.
-__device__ void build_chunks(const Params& p, Ctl* c) {
+// Every CTA of both kernels sorts for itself, to the same tables.
+
+__device__ __forceinline__ int local_expert(const Params& p, int i) {
+  const int id = __ldg(p.ids + i), e = id - p.g0;
+  if (id < 0 || id >= p.E) {
+    raise_error(&g_err, MOE_DEVERR_BAD_EXPERT_ID);
+    return 0xFFFF;
+  }
+  return e >= 0 && e < p.El ? e : 0xFFFF;
+}
+
+// Up to 32 pairs, one a lane: a pair's slot is the number of pairs before it
+// in (expert, pair) order, its chunk the number of chunks of smaller experts
+// and of earlier pairs of its own.
+template <class C>
+__device__ __forceinline__ void build_chunks_warp(const Params& p, C* c) {
   const int lane = threadIdx.x & 31;
   const int R = p.T * p.k;
-  // c->order holds the local expert of every pair (0xFFFF: none) until the slots are known
+  const int e = lane < R ? local_expert(p, lane) : 0xFFFF;
+  const uint32_t same = __match_any_sync(0xffffffffu, e);
+  const bool mine = e != 0xFFFF;
+  const int rank = __popc(same & ((1u << lane) - 1u)), n = __popc(same);
+  const int nc = mine && rank == 0 ? (n + p.cap - 1) / p.cap : 0;  // a group's first pair counts its chunks
+  int start = 0, chunk = 0, total = 0;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const int ej = __shfl_sync(0xffffffffu, e, j), cj = __shfl_sync(0xffffffffu, nc, j);
+    start += ej < e;
+    chunk += ej < e ? cj : 0;
+    total += cj;
+  }
+  if (mine) {
+    c->pos[lane] = static_cast<uint16_t>(start + rank);
+    c->order[start + rank] = static_cast<uint16_t>(lane);
+    if (rank % p.cap == 0) {
+      const int q = chunk + rank / p.cap;
+      c->cexp[q] = static_cast<uint16_t>(e);
+      c->cstart[q] = static_cast<uint16_t>(start + rank);
+      c->cnum[q] = static_cast<uint16_t>(min(p.cap, n - rank));
+    }
+  } else if (lane < R) {
+    c->pos[lane] = 0xFFFF;
+  }
+  if (lane == 0) c->nchunk = total;
+}
+
+// A stable counting sort by one warp: 32 pairs at a time, the rank of a pair
+// among its expert's earlier ones from a warp-wide match and a running count.
+// c->order holds the local expert of every pair until the slots are known,
+// c->num is zero.
+template <class C>
+__device__ void build_chunks(const Params& p, C* c) {
+  const int lane = threadIdx.x & 31;
+  const int R = p.T * p.k;
   for (int i0 = 0; i0 < R; i0 += 32) {
     const int i = i0 + lane;
     const int e = i < R ? c->order[i] : 0xFFFF;
@@ -244,24 +308,22 @@ __device__ void build_chunks(const Params& p, Ctl* c) {
     const int e = e0 + lane;
     const int n = e < p.El ? c->num[e] : 0;
     const int nc = (n + p.cap - 1) / p.cap;
-    int in = n, ic = nc;
+    int both = (nc << 16) | n;  // at most 1024 of either
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, in, o), b = __shfl_up_sync(0xffffffffu, ic, o);
-      if (lane >= o) {
-        in += a;
-        ic += b;
-      }
+      const int a = __shfl_up_sync(0xffffffffu, both, o);
+      if (lane >= o) both += a;
     }
-    const int off = slots + in - n, c0 = chunks + ic - nc;
+    const int off = slots + (both & 0xFFFF) - n, c0 = chunks + (both >> 16) - nc;
     for (int j = 0; j < nc; ++j) {
       c->cexp[c0 + j] = static_cast<uint16_t>(e);
       c->cstart[c0 + j] = static_cast<uint16_t>(off + j * p.cap);
       c->cnum[c0 + j] = static_cast<uint16_t>(min(p.cap, n - j * p.cap));
     }
     if (e < p.El) c->num[e] = static_cast<uint16_t>(off);
-    slots += __shfl_sync(0xffffffffu, in, 31);
-    chunks += __shfl_sync(0xffffffffu, ic, 31);
+    both = __shfl_sync(0xffffffffu, both, 31);
+    slots += both & 0xFFFF;
+    chunks += both >> 16;
   }
   if (lane == 0) c->nchunk = chunks;
   __syncwarp();
@@ -286,10 +348,10 @@ __device__ void build_chunks(const Params& p, Ctl* c) {
 // zeros.  The shared-memory loads run DEPTH pairs of 16-byte chunks ahead of
 // the products (all of them at NT <= 2): taken as they were needed, their
 // latencies made a stage 1.7 times as long.
-template <int WT, int NT>
+template <int WT, int PHASE, int NT>
 __device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t wt, uint32_t swz, uint32_t xb, uint32_t sA,
                                          uint32_t sB, uint32_t xs, bool block_scale) {
-  using C = Cfg<WT>;
+  using C = Cfg<WT, PHASE>;
   constexpr int DEPTH = WT == kMx4 ? (NT == 1 ? 4 : (NT == 2 ? 2 : 1)) : (NT <= 2 ? 4 : 2);
   constexpr int BW = WT == kMx4 ? 4 : 2;  // words of a chunk's activation fragment
   const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
@@ -474,9 +536,9 @@ struct Walk {
   }
 };
 
-template <int WT, int PHASE>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
-  using C = Cfg<WT>;
+template <int WT, int PHASE, bool SMALL>
+__global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
+  using C = Cfg<WT, PHASE>;
   constexpr int PER = C::PER;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -489,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const uint32_t s_ring = x_ring + S * x_bytes;
   const uint32_t v_ring = s_ring + S * C::SCALE_BYTES;
   const uint32_t v_bytes = cap * 4;
-  Ctl* ctl = reinterpret_cast<Ctl*>(bp + (v_ring + S * v_bytes - base));
+  Ctl<SMALL>* ctl = reinterpret_cast<Ctl<SMALL>*>(bp + (v_ring + S * v_bytes - base));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.T * p.k;
 
@@ -501,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->xraw[s]), 32);
       mbar_init(smem_u32(&ctl->xfull[s]), 1);
       mbar_init(smem_u32(&ctl->empty[s]), kMmaWarps);
     }
@@ -510,14 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
   }
-  for (int i = threadIdx.x; i < R; i += kThreads) {
-    const int id = __ldg(p.ids + i), e = id - p.g0;
-    if (PHASE == 1 && blockIdx.x == 0 && (id < 0 || id >= p.E)) raise_error(&g_err, MOE_DEVERR_BAD_EXPERT_ID);
-    ctl->order[i] = (id >= 0 && id < p.E && e >= 0 && e < p.El) ? static_cast<uint16_t>(e) : 0xFFFF;
+  if (R <= 32) {
+    if (warp == 1) build_chunks_warp(p, ctl);
+  } else {
+    for (int i = threadIdx.x; i < R; i += kThreads) ctl->order[i] = static_cast<uint16_t>(local_expert(p, i));
+    for (int i = threadIdx.x; i < p.El; i += kThreads) ctl->num[i] = 0;
+    __syncthreads();
+    if (warp == 1) build_chunks(p, ctl);
   }
-  for (int i = threadIdx.x; i < p.El; i += kThreads) ctl->num[i] = 0;
-  __syncthreads();
-  if (warp == 0) build_chunks(p, ctl);
   __syncthreads();
 
   const int nchunk = ctl->nchunk;
@@ -540,93 +603,89 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     return;
   }
 
+  const bool words = p.mode == kScaleBlock || p.mode == kScaleMx;  // one scale word a row and 128 values of K
+  const bool partial = PHASE == 2 && segs1 > 1;                    // kernel 1 left sums of K segments
+  // where the raw scale words of span v of stage s arrive: the end of their place
+  auto raw_words = [&](uint32_t s, int v) {
+    return s_ring + s * C::SCALE_BYTES + (v + 1) * kRows * C::SCALE_ROW - kRows * 4;
+  };
+
   if (warp == 0) {
-    // ------------------------------------------------------- weights by TMA
-    if (lane == 0) {
-      uint32_t s = 0, ph = 0, issued = 0;
-      for (Step q = walk.begin(); !walk.done(q); walk.next(q), ++issued) {
-        if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs)) {
-          timed_out = true;
-          break;
-        }
+    // ------------------------- weights by TMA; activations and scales by cp.async
+    const int nkb = p.K / 128;  // (used with scale words: K % 128 == 0)
+    const int64_t scale_rows = static_cast<int64_t>(PHASE == 1 ? 2 * p.N : p.N);
+    auto load_weights = [&](uint32_t s, const Step& q) {
+      if (lane == 0) {
         const uint32_t fb = smem_u32(&ctl->full[s]);
         const int e = ctl->cexp[q.ch];
         mbar_arrive_expect_tx(fb, kStageW);
         // rows past the tensor's channels or K arrive as zeros
         tma_load_3d(base + s * kStageW, &tmW, q.kst * 128, q.blk * kPer, PHASE == 1 ? 2 * e : e, fb);
-        if (++s == S) {
-          s = 0;
-          ph ^= 1;
+      }
+    };
+    auto load_rest = [&](uint32_t s, const Step& q) {
+      if (words) {
+        const int e = ctl->cexp[q.ch];
+        const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * p.N : lane * 4);
+#pragma unroll
+        for (int v = 0; v < C::SPANS; ++v) {
+          const int64_t kb = q.kst * C::SPANS + v;
+          const bool ok = kb < nkb;
+          const float* src = p.mode == kScaleMx ? p.scale + kb * (p.El * scale_rows) + e * scale_rows + n0
+                                                : p.scale + (e * static_cast<int64_t>(nkb) + kb) * scale_rows + n0;
+          cp_async_16(raw_words(s, v) + lane * 16, ok ? src : p.scale, ok ? 16u : 0u);
         }
       }
-      if (timed_out) {
-        *abort_flag = 1;
-        ctl->err = 2;
-        for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)  // copies in flight land before the CTA exits
-          mbar_wait_bounded(smem_u32(&ctl->full[j % S]), (j / S) & 1, &ctl->no_abort, kWaitLimitNs);
+      if (!partial) {
+        constexpr int kChunks = C::ROW_BYTES / 16, kVals = PHASE == 1 ? 8 : 4;  // 16-byte chunks of a row, values in one
+        const int n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
+        for (int i = lane; i < n * kChunks; i += 32) {
+          const int r = i / kChunks, c = i % kChunks;
+          const int64_t row = PHASE == 1 ? ctl->order[st + r] / p.k : st + r;
+          const int col = q.kst * C::KE + c * kVals;
+          const bool ok = col < p.K;  // K is a multiple of 16
+          const uint8_t* src = static_cast<const uint8_t*>(p.act);
+          cp_async_16(x_ring + s * x_bytes + r * C::PITCH + c * 16,
+                      ok ? src + (row * p.K + col) * (PHASE == 1 ? 2 : 4) : src, ok ? 16u : 0u);
+        }
       }
+      cp_async_arrive(smem_u32(&ctl->xraw[s]));
+    };
+    uint32_t s = 0, ph = 0, issued = 0;
+    Step q = walk.begin();
+    if (PHASE == 2) {
+      // the ring's first weights do not depend on kernel 1; its h does
+      Step w = q;
+      for (uint32_t i = 0; i < S && !walk.done(w); ++i, walk.next(w)) load_weights(i, w);
+      grid_dep_wait();
+      for (; issued < S && !walk.done(q); ++issued, walk.next(q)) load_rest(issued, q);
+      ph = 1;  // a full ring is out; where it is not full, no stage is left
+    }
+    for (; !walk.done(q); walk.next(q), ++issued) {
+      if (!mbar_wait_bounded_warp(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs)) {
+        timed_out = true;
+        break;
+      }
+      load_weights(s, q);
+      load_rest(s, q);
+      if (++s == S) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (timed_out) {
+      *abort_flag = 1;
+      ctl->err = 2;
+      // copies in flight land before the CTA exits
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0)
+        for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
+          mbar_wait_bounded(smem_u32(&ctl->full[j % S]), (j / S) & 1, &ctl->no_abort, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp <= kConvWarps) {
-    // ------------------------------- activations to f16, and the weight scales
-    const bool words = p.mode == kScaleBlock || p.mode == kScaleMx;  // one word a row and 128 values of K
-    const int nkb = p.K / 128;                                        // (used with such scales: K % 128 == 0)
-    const int64_t scale_rows = static_cast<int64_t>(PHASE == 1 ? 2 * p.N : p.N);
-    // activation rows whose loads are in flight together (64 registers of them at most)
-    constexpr int kBatch = WT == kMx4 && PHASE == 2 ? 4 : 8;
-    constexpr int kVec = PHASE == 1 ? PER / 4 : PER / 2;  // 8-byte words a lane loads of a span
+    // ---------------------- activations to f16 and MX scale codes to floats, in place
     const int slots = PHASE == 2 ? ctl->cstart[nchunk - 1] + ctl->cnum[nchunk - 1] : 0;
-    const bool partial = PHASE == 2 && segs1 > 1;  // kernel 1 left sums of K segments
-    uint2 d[kBatch][kVec];
-    uint4 sc[C::SPANS];
-    auto load_rows = [&](const Step& q, int first) {
-      const int n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
-      const int col = q.kst * C::KE + lane * PER;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (first + i < n && col < p.K) {
-          const int64_t row = PHASE == 1 ? ctl->order[st + first + i] / p.k : st + first + i;
-          const uint8_t* src = static_cast<const uint8_t*>(p.act) + (row * p.K + col) * (PHASE == 1 ? 2 : 4);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            if (PHASE == 1)
-              d[i][j] = __ldg(reinterpret_cast<const uint2*>(src) + j);
-            else
-              d[i][j] = __ldcg(reinterpret_cast<const uint2*>(src) + j);
-          }
-        }
-    };
-    auto load_scales = [&](const Step& q) {
-      const int e = ctl->cexp[q.ch];
-      const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * p.N : lane * 4);
-#pragma unroll
-      for (int v = 0; v < C::SPANS; ++v) {
-        const int64_t kb = q.kst * C::SPANS + v;
-        sc[v] = make_uint4(0, 0, 0, 0);  // (past the end of K)
-        if (kb < nkb) {
-          const float* src = p.mode == kScaleMx ? p.scale + kb * (p.El * scale_rows) + e * scale_rows + n0
-                                                : p.scale + (e * static_cast<int64_t>(nkb) + kb) * scale_rows + n0;
-          sc[v] = __ldg(reinterpret_cast<const uint4*>(src));
-        }
-      }
-    };
-    auto unpack = [&](int i, bool ok, float (&v)[PER]) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) v[j] = 0.0f;
-      if (!ok) return;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        if (PHASE == 1) {
-          v[4 * j] = bf16lo(d[i][j].x);
-          v[4 * j + 1] = bf16hi(d[i][j].x);
-          v[4 * j + 2] = bf16lo(d[i][j].y);
-          v[4 * j + 3] = bf16hi(d[i][j].y);
-        } else {
-          v[2 * j] = __uint_as_float(d[i][j].x);
-          v[2 * j + 1] = __uint_as_float(d[i][j].y);
-        }
-      }
-    };
     // h of kernel 1's segments: their sums in ascending order, then SwiGLU
     auto join = [&](int slot, int col, bool ok, float (&v)[PER]) {
       float a0[PER], a1[PER];
@@ -652,67 +711,71 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < PER; ++j) v[j] = ok ? __fmul_rn(silu_f32(a0[j]), a1[j]) : 0.0f;
     };
+    // a lane's PER values of the raw row at `at`
+    auto raw = [&](uint32_t at, float (&v)[PER]) {
+#pragma unroll
+      for (int j = 0; j < PER; j += 4) {
+        if (PHASE == 1) {
+          const uint2 d = lds64(at + (lane * PER + j) * 2);
+          v[j] = bf16lo(d.x);
+          v[j + 1] = bf16hi(d.x);
+          v[j + 2] = bf16lo(d.y);
+          v[j + 3] = bf16hi(d.y);
+        } else {
+          const uint4 d = lds128(at + (lane * PER + j) * 4);
+          v[j] = __uint_as_float(d.x);
+          v[j + 1] = __uint_as_float(d.y);
+          v[j + 2] = __uint_as_float(d.z);
+          v[j + 3] = __uint_as_float(d.w);
+        }
+      }
+    };
 
+    if (PHASE == 2) grid_dep_wait();  // h is kernel 1's
     Step q = walk.begin();
     walk.skip(q, warp - 1);
-    uint32_t step = warp - 1;
-    if (words && !walk.done(q)) load_scales(q);
-    if (PHASE == 2) grid_dep_wait();  // h is kernel 1's
-    if (!walk.done(q) && !partial) load_rows(q, 0);
-    while (!walk.done(q)) {
+    for (uint32_t step = warp - 1; !walk.done(q); step += kConvWarps, walk.skip(q, kConvWarps)) {
       const uint32_t s = step % S, ph = (step / S) & 1;
-      if (!mbar_wait_bounded_warp(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs)) {
+      if (!mbar_wait_bounded_warp(smem_u32(&ctl->xraw[s]), ph, abort_flag, kWaitLimitNs)) {
         timed_out = true;
         break;
       }
-      const int n = ctl->cnum[q.ch], col = q.kst * C::KE + lane * PER;
-      const bool ok = col < p.K;  // K is a multiple of 16: a lane's values are all in or out
-      const uint32_t at = x_ring + s * x_bytes, av = v_ring + s * v_bytes;
-      if (words) {
+      if (C::MX) {  // a lane: four rows' words of four codes, as floats
 #pragma unroll
         for (int v = 0; v < C::SPANS; ++v) {
+          const uint4 u = lds128(raw_words(s, v) + lane * 16);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
           const uint32_t dst = s_ring + s * C::SCALE_BYTES + (v * kRows + lane * 4) * C::SCALE_ROW;
-          if (C::MX) {  // four rows' four codes each, as floats
-            const uint32_t w[4] = {sc[v].x, sc[v].y, sc[v].z, sc[v].w};
+          __syncwarp();  // the floats go over the words
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float f[4];
-#pragma unroll
-              for (int b = 0; b < 4; ++b) f[b] = e8m0_value((w[r] >> (8 * b)) & 0xFFu);
-              sts128(dst + r * 16, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                              __float_as_uint(f[3])));
-            }
-          } else {
-            sts128(dst, sc[v]);
-          }
+          for (int r = 0; r < 4; ++r)
+            sts128(dst + r * 16, make_uint4(__float_as_uint(e8m0_value(w[r] & 0xFFu)),
+                                            __float_as_uint(e8m0_value((w[r] >> 8) & 0xFFu)),
+                                            __float_as_uint(e8m0_value((w[r] >> 16) & 0xFFu)),
+                                            __float_as_uint(e8m0_value(w[r] >> 24))));
         }
       }
+      const int n = ctl->cnum[q.ch], col = q.kst * C::KE + lane * PER;
+      const uint32_t at = x_ring + s * x_bytes, av = v_ring + s * v_bytes;
       if (partial) {
+        const int st = ctl->cstart[q.ch];
         for (int i = 0; i < n; ++i) {
           float v[PER];
-          join(ctl->cstart[q.ch] + i, col, ok, v);
+          join(st + i, col, col < p.K, v);
           store_span<PER>(v, at + i * C::PITCH, av + i * 4, lane);
         }
       } else {
-        for (int first = 0; first < n; first += kBatch) {
-          if (first) load_rows(q, first);
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (first + i < n) {
-              float v[PER];
-              unpack(i, ok, v);
-              store_span<PER>(v, at + (first + i) * C::PITCH, av + (first + i) * 4, lane);
-            }
+        for (int i = 0; i < n; i += 2) {  // two rows' latencies together (an odd last row twice)
+          const int i1 = i + 1 < n ? i + 1 : i;
+          float v[PER], w[PER];
+          raw(at + i * C::PITCH, v);
+          raw(at + i1 * C::PITCH, w);
+          store_span<PER>(v, at + i * C::PITCH, av + i * 4, lane);
+          store_span<PER>(w, at + i1 * C::PITCH, av + i1 * 4, lane);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->xfull[s]));
-      walk.skip(q, kConvWarps);
-      step += kConvWarps;
-      if (!walk.done(q)) {
-        if (words) load_scales(q);
-        if (!partial) load_rows(q, 0);
-      }
     }
     if (timed_out) {
       *abort_flag = 1;
@@ -746,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           break;
         }
         const uint32_t st = s_ring + s * C::SCALE_BYTES;
-        contract<WT, NT>(acc, base + s * kStageW + w_off, swz, x_ring + s * x_bytes + x_off,
+        contract<WT, PHASE, NT>(acc, base + s * kStageW + w_off, swz, x_ring + s * x_bytes + x_off,
                          st + (rowA + g) * C::SCALE_ROW, st + (rowB + g) * C::SCALE_ROW, v_ring + s * v_bytes + t4 * 8,
                          p.mode == kScaleBlock);
         fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
@@ -757,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           ph ^= 1;
         }
       }
+      if (timed_out) return;
       const int e = ctl->cexp[q.ch], n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
       const int ca = q.blk * kPer + (PHASE == 1 ? 8 * mw : 16 * mw) + g;  // channel of row A
       const int cb = PHASE == 1 ? ca : ca + 8;
@@ -792,42 +856,70 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         }
     };
 
-    // (a warp that gave up waiting still walks the units, without waits: the
-    // other warps count on it at the barriers)
-    for (Step q = walk.begin(); !walk.done(q);) {
+    for (Step q = walk.begin(); !walk.done(q) && !timed_out;) {
       const int n = ctl->cnum[q.ch];
-      if (n <= 8)
+      if (SMALL || n <= 8)
         unit(std::integral_constant<int, 1>{}, q);
       else if (n <= 16)
-        unit(std::integral_constant<int, 2>{}, q);
+        unit(std::integral_constant<int, SMALL ? 1 : 2>{}, q);
       else
-        unit(std::integral_constant<int, 4>{}, q);
-      if (PHASE == 2) {
-        // the block's last unit (over all CTAs) sums its pairs into y
+        unit(std::integral_constant<int, SMALL ? 1 : 4>{}, q);
+      if (PHASE == 2 && !timed_out) {
+        // the last unit (over all CTAs) that gets to these 16 columns sums their
+        // pairs into y: each warp for the rows of its own, without its neighbours
         __threadfence();
-        named_barrier_sync(1, kMmaWarps * 32);
-        if (mw == 0 && lane == 0)
-          ctl->last = atomicAdd(p.count + q.blk, 1u) == static_cast<unsigned>(nchunk * walk.segs - 1);
-        named_barrier_sync(1, kMmaWarps * 32);
-        if (ctl->last) {
+        __syncwarp();
+        unsigned int done = 0;
+        if (lane == 0) done = atomicAdd(p.count + q.blk * kMmaWarps + mw, 1u);
+        done = __shfl_sync(0xffffffffu, done, 0);
+        const int d = q.blk * kRows + 16 * mw + 4 * (lane & 3);
+        if (done == static_cast<unsigned>(nchunk * walk.segs - 1) && d < p.N) {
           __threadfence();
-          const int th = mw * 32 + lane, d0 = q.blk * kRows;
-          for (int i = th; i < p.T * kRows; i += kMmaWarps * 32) {
-            const int t = i / kRows, d = d0 + i % kRows;
-            if (d >= p.N) continue;
-            float a = 0.0f;
-            for (int j = 0; j < p.k; ++j) {
-              const int pr = t * p.k + j;
-              if (ctl->pos[pr] == 0xFFFF) continue;
-              const float w = p.topk_w ? __ldg(p.topk_w + pr) : 1.0f;
-              float o = 0.0f;
-              for (int sg = 0; sg < walk.segs; ++sg)
-                o += __ldcg(p.out + (static_cast<int64_t>(sg) * slots + ctl->pos[pr]) * p.N + d);
-              a = __fmaf_rn(w, o, a);
+          const int64_t seg_pitch = static_cast<int64_t>(slots) * p.N;
+          for (int t = lane >> 2; t < p.T; t += 8) {
+            float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j0 = 0; j0 < p.k; j0 += 8) {
+              float4 o[8];
+              bool ok[8];
+              float w[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {  // eight pairs' loads first
+                const int pr = t * p.k + j0 + j;
+                const int slot = j0 + j < p.k ? ctl->pos[pr] : 0xFFFF;
+                ok[j] = slot != 0xFFFF;
+                o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                w[j] = 1.0f;
+                if (ok[j]) {
+                  const float* src = p.out + static_cast<int64_t>(slot) * p.N + d;
+                  o[j] = __ldcg(reinterpret_cast<const float4*>(src));
+                  if (p.topk_w) w[j] = __ldg(p.topk_w + pr);
+                }
+              }
+              for (int sg = 1; sg < walk.segs; ++sg)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (ok[j]) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                        p.out + sg * seg_pitch + static_cast<int64_t>(ctl->pos[t * p.k + j0 + j]) * p.N + d));
+                    o[j].x += v.x;
+                    o[j].y += v.y;
+                    o[j].z += v.z;
+                    o[j].w += v.w;
+                  }
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (ok[j]) {
+                  a[0] = __fmaf_rn(w[j], o[j].x, a[0]);
+                  a[1] = __fmaf_rn(w[j], o[j].y, a[1]);
+                  a[2] = __fmaf_rn(w[j], o[j].z, a[2]);
+                  a[3] = __fmaf_rn(w[j], o[j].w, a[3]);
+                }
             }
-            p.y[static_cast<int64_t>(t) * p.N + d] = static_cast<uint16_t>(pack_bf16x2(a, 0.0f) & 0xFFFFu);
+            *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t) * p.N + d) =
+                make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
           }
         }
+        __syncwarp();
       }
       q.u += gridDim.x;
       if (!walk.done(q)) walk.open(q);
@@ -878,7 +970,7 @@ int max_segs(int64_t R) {
 }
 
 // Workspace: h fp32 [R, F] or partial a [segs][R, 2F] | o fp32 [segs][R, D] |
-// a counter for every block of output columns, each part 256-byte aligned.
+// a counter for every 16 output columns, each part 256-byte aligned.
 int64_t h_bytes(int64_t R, int64_t F) {
   const int64_t s = max_segs(R);
   return align256(R * F * 4 * (s > 1 ? 2 * s : 1));
@@ -890,20 +982,20 @@ bool shape_ok(int64_t T, int k, int64_t D, int64_t F) {
          F % 16 == 0 && D <= 32768 && F <= 32768;
 }
 
-template <int WT, int PHASE>
-moe_status launch(const void* w, Params p, int grid, cudaStream_t st) {
-  using C = Cfg<WT>;
+template <int WT, int PHASE, bool SMALL>
+moe_status launch_size(const void* w, Params p, int grid, cudaStream_t st) {
+  using C = Cfg<WT, PHASE>;
   CUtensorMap tm;
   const uint64_t bytes = WT == kMx4 ? p.K / 2 : p.K;
   if (!make_map(&tm, w, bytes, p.N, static_cast<uint64_t>(p.El) * (PHASE == 1 ? 2 : 1), PHASE == 1 ? kRows / 2 : kRows,
                 PHASE == 1 ? 2 : 1))
     return MOE_ERR_CUDA;
   const size_t stage = kStageW + static_cast<size_t>(p.cap) * (C::PITCH + 4) + C::SCALE_BYTES;
-  const size_t fixed = 1024 + kCtlBytes;
-  p.stages = static_cast<int>((kSmemLimit - fixed) / stage);
+  const size_t fixed = 1024 + ctl_bytes<SMALL>();
+  p.stages = static_cast<int>(((SMALL ? kSmemHalf : kSmemLimit) - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = fixed + p.stages * stage;
-  auto kernel = decode_kernel<WT, PHASE>;
+  auto kernel = decode_kernel<WT, PHASE, SMALL>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
@@ -917,6 +1009,11 @@ moe_status launch(const void* w, Params p, int grid, cudaStream_t st) {
   cfg.numAttrs = PHASE == 2 ? 1 : 0;
   MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tm, p));
   return MOE_OK;
+}
+
+template <int WT, int PHASE>
+moe_status launch(const void* w, const Params& p, int grid, cudaStream_t st) {
+  return p.cap == 8 ? launch_size<WT, PHASE, true>(w, p, grid, st) : launch_size<WT, PHASE, false>(w, p, grid, st);
 }
 
 template <int PHASE>
@@ -952,7 +1049,7 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_take_err
 
 extern "C" size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F) {
   if (!shape_ok(T, k, D, F)) return 0;
-  return static_cast<size_t>(h_bytes(T * k, F) + o_bytes(T * k, D) + align256(blocks(D, kRows) * 4));
+  return static_cast<size_t>(h_bytes(T * k, F) + o_bytes(T * k, D) + align256(blocks(D, kRows) * kMmaWarps * 4));
 }
 
 extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int k,
@@ -993,18 +1090,21 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   p.topk_w = topk_w;
   p.y = y;
   p.count = reinterpret_cast<unsigned int*>(ws + h_bytes(R, F) + o_bytes(R, D));
-  p.ncount = static_cast<int>(blocks(D, kRows));
+  p.ncount = static_cast<int>(blocks(D, kRows)) * kMmaWarps;
   p.T = static_cast<int>(T);
   p.k = k;
   p.E = E;
   p.g0 = group_offset;
   p.El = E_local;
-  p.cap = T <= 8 ? 8 : (T <= 16 ? 16 : 32);
+  // Pairs a chunk: eight is one MMA column group and lets both kernels sit on
+  // an SM together; beyond eight tokens, 16 where the experts hold few of them
+  // (the ring gets two more stages than with 32), else 32.
+  p.cap = T <= 8 ? 8 : (T <= 16 || R <= 6 * static_cast<int64_t>(E_local) ? 16 : 32);
   p.smax = max_segs(R);
   p.nblock1 = static_cast<int>(blocks(F, kRows / 2));
   p.nst1 = static_cast<int>(blocks(D, ke));
   // no more CTAs than units (a chunk a pair, all segments)
-  const int64_t u1 = R * p.nblock1 * p.smax, u2 = R * p.ncount * p.smax;
+  const int64_t u1 = R * p.nblock1 * p.smax, u2 = R * blocks(D, kRows) * p.smax;
   p.grid1 = static_cast<int>(u1 < sms ? u1 : sms);
   p.act = x;
   p.scale = static_cast<const float*>(s_in);
