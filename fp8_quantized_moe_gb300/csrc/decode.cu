@@ -63,14 +63,13 @@ __device__ unsigned int g_err;
 constexpr int kConvWarps = 3, kMmaWarps = 8;
 constexpr int kThreads = 32 * (1 + kConvWarps + kMmaWarps);
 constexpr int kRows = 128;              // weight rows of a unit
-constexpr int kStageW = kRows * 128;    // weight bytes of a stage
+constexpr int kBoxW = kRows * 128;      // weight bytes of a TMA box
 constexpr int kMaxStages = 10;
 constexpr int kMaxSegs = 8;
 constexpr int kMaxPairs = 1024;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 1024;
 constexpr int kSmemLimit = 232448;
-constexpr int kSmemHalf = 115712;  // two CTAs an SM (228 KB, 1 KB of it reserved for each)
 
 enum { kE4M3 = 0, kInt8 = 1, kMx8 = 2, kMx4 = 3 };
 enum { kScaleChannel = 0, kScaleBlock = 1, kScaleTensor = 2, kScaleMx = 3 };
@@ -93,30 +92,35 @@ struct Params {
   int nblock1, nst1;  // row blocks and K stages of kernel 1
 };
 
-// SMALL: T <= 8, so at most 256 pairs and chunks of eight.
-template <bool SMALL>
 struct Ctl {
-  static constexpr int PAIRS = SMALL ? 256 : kMaxPairs;
   uint64_t full[kMaxStages], xraw[kMaxStages], xfull[kMaxStages], empty[kMaxStages];
   int abort_flag, no_abort, err, nchunk;
-  uint16_t pos[PAIRS];     // slot of pair i (pairs sorted by expert), 0xFFFF: not local
-  uint16_t order[PAIRS];   // pair of slot s
-  uint16_t cexp[PAIRS], cstart[PAIRS], cnum[PAIRS];
+  uint16_t pos[kMaxPairs];     // slot of pair i (pairs sorted by expert), 0xFFFF: not local
+  uint16_t order[kMaxPairs];   // pair of slot s
+  uint16_t cexp[kMaxPairs], cstart[kMaxPairs], cnum[kMaxPairs];
   uint16_t num[kMaxExperts];
 };
 
 template <int WT, int PHASE>
 struct Cfg {
-  static constexpr int KE = WT == kMx4 ? 256 : 128;  // values of K in a stage (128 bytes of weights a row)
-  static constexpr int SPANS = KE / 128;             // scale words of a row and stage
   static constexpr bool MX = WT == kMx8 || WT == kMx4;
-  // a row's scales of a stage: one float a span, or (MX) its four blocks' floats a span
+  // Boxes (128 bytes of each weight row) a stage: two, so that a warp has two
+  // boxes' loads in flight and half the hand-offs; one for e2m1, whose box
+  // holds twice the values and whose activations take the space
+  static constexpr int BOXES = WT == kMx4 ? 1 : 2;
+  static constexpr int BOX_K = WT == kMx4 ? 256 : 128;  // values of K in a box: a span of an activation row
+  static constexpr int KE = BOXES * BOX_K;              // and in a stage
+  static constexpr int STAGE_W = BOXES * kBoxW;
+  static constexpr int WORDS = BOX_K / 128;             // scale words of a row and box
+  // a row's scale word as it is used: one float, or (MX) its four blocks' floats
   static constexpr int SCALE_ROW = MX ? 16 : 4;
-  static constexpr int SCALE_BYTES = SPANS * kRows * SCALE_ROW;
-  static constexpr int PER = KE / 32;  // values of a span a lane converts
+  static constexpr int SCALE_BYTES = BOXES * WORDS * kRows * SCALE_ROW;
+  static constexpr int PER = BOX_K / 32;  // values of a span a lane converts
   // bytes of an activation row as it arrives (bf16 x, fp32 h; the f16 form takes
-  // the front of its place), padded so that eight rows' fragments lie in different banks
-  static constexpr int ROW_BYTES = KE * (PHASE == 1 ? 2 : 4);
+  // the front of each span's place), padded so that eight rows' fragments lie
+  // in different banks
+  static constexpr int SPAN_BYTES = BOX_K * (PHASE == 1 ? 2 : 4);
+  static constexpr int ROW_BYTES = BOXES * SPAN_BYTES;
   static constexpr int PITCH = ROW_BYTES + (WT == kMx4 ? 64 : 32);
 };
 
@@ -135,10 +139,7 @@ __device__ __forceinline__ int pick_segs(int units, int nst, int grid, int smax)
   return best;
 }
 
-template <bool SMALL>
-constexpr size_t ctl_bytes() {
-  return (sizeof(Ctl<SMALL>) + 127) / 128 * 128;
-}
+constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
 
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -249,8 +250,7 @@ __device__ __forceinline__ int local_expert(const Params& p, int i) {
 // Up to 32 pairs, one a lane: a pair's slot is the number of pairs before it
 // in (expert, pair) order, its chunk the number of chunks of smaller experts
 // and of earlier pairs of its own.
-template <class C>
-__device__ __forceinline__ void build_chunks_warp(const Params& p, C* c) {
+__device__ __forceinline__ void build_chunks_warp(const Params& p, Ctl* c) {
   const int lane = threadIdx.x & 31;
   const int R = p.T * p.k;
   const int e = lane < R ? local_expert(p, lane) : 0xFFFF;
@@ -285,8 +285,7 @@ __device__ __forceinline__ void build_chunks_warp(const Params& p, C* c) {
 // among its expert's earlier ones from a warp-wide match and a running count.
 // c->order holds the local expert of every pair until the slots are known,
 // c->num is zero.
-template <class C>
-__device__ void build_chunks(const Params& p, C* c) {
+__device__ void build_chunks(const Params& p, Ctl* c) {
   const int lane = threadIdx.x & 31;
   const int R = p.T * p.k;
   for (int i0 = 0; i0 < R; i0 += 32) {
@@ -341,7 +340,7 @@ __device__ void build_chunks(const Params& p, C* c) {
   }
 }
 
-// One stage: 16 rows x 128 bytes of weights at `wt` (row A + lane / 4 and row
+// One box: 16 rows x 128 bytes of weights at `wt` (row A + lane / 4 and row
 // B + lane / 4 of the fragment), activations at `xb` (already this lane's), the
 // scales of this lane's two weight rows at sA, sB and the activations' span
 // scales at `xs`.  Past the end of K both the weights and the activations are
@@ -349,15 +348,16 @@ __device__ void build_chunks(const Params& p, C* c) {
 // the products (all of them at NT <= 2): taken as they were needed, their
 // latencies made a stage 1.7 times as long.
 template <int WT, int PHASE, int NT>
-__device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t wt, uint32_t swz, uint32_t xb, uint32_t sA,
-                                         uint32_t sB, uint32_t xs, bool block_scale) {
+struct Box {
   using C = Cfg<WT, PHASE>;
-  constexpr int DEPTH = WT == kMx4 ? (NT == 1 ? 4 : (NT == 2 ? 2 : 1)) : (NT <= 2 ? 4 : 2);
-  constexpr int BW = WT == kMx4 ? 4 : 2;  // words of a chunk's activation fragment
-  const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
+  static constexpr int DEPTH = WT == kMx4 ? (NT == 1 ? 4 : (NT == 2 ? 2 : 1)) : (NT <= 2 ? 4 : 2);
+  static constexpr int BW = WT == kMx4 ? 4 : 2;  // words of a chunk's activation fragment
   uint32_t r[4][4];
   uint32_t b[DEPTH][2][NT][BW];
-  auto load_b = [&](int c) {
+  float fA[4], fB[4];
+  uint2 xv[NT];
+
+  __device__ __forceinline__ void load_b(uint32_t xb, int c) {
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
@@ -374,13 +374,8 @@ __device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t wt, uint3
           b[c % DEPTH][cc][n][1] = v.y;
         }
       }
-  };
-#pragma unroll
-  for (int c = 0; c < 4; ++c) ldmatrix_x4(wt + (((2 * c + hi) * 16) ^ swz), r[c]);
-#pragma unroll
-  for (int c = 0; c < DEPTH; ++c) load_b(c);
-  float fA[4] = {1.0f, 1.0f, 1.0f, 1.0f}, fB[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-  auto load_f = [&](int v) {
+  }
+  __device__ __forceinline__ void load_f(uint32_t sA, uint32_t sB, int v) {
     const uint4 a = lds128(sA + v * kRows * 16), d = lds128(sB + v * kRows * 16);
     fA[0] = __uint_as_float(a.x);
     fA[1] = __uint_as_float(a.y);
@@ -390,77 +385,87 @@ __device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t wt, uint3
     fB[1] = __uint_as_float(d.y);
     fB[2] = __uint_as_float(d.z);
     fB[3] = __uint_as_float(d.w);
-  };
-  if (C::MX) {
-    load_f(0);
-  } else if (block_scale) {
-    fA[0] = __uint_as_float(lds32(sA));
-    fB[0] = __uint_as_float(lds32(sB));
   }
-  uint2 xv[NT];
+  __device__ __forceinline__ void load(uint32_t wt, uint32_t swz, uint32_t xb, uint32_t sA, uint32_t sB, uint32_t xs,
+                                       bool block_scale) {
+    const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
 #pragma unroll
-  for (int n = 0; n < NT; ++n) xv[n] = lds64(xs + n * 32);
-
-  // two chains of sums (MX: the sum of the scaled 32-wide blocks, and the block at hand)
-  float s0[NT][4], s1[NT][4];
+    for (int c = 0; c < 4; ++c) ldmatrix_x4(wt + (((2 * c + hi) * 16) ^ swz), r[c]);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int c = 0; c < DEPTH; ++c) load_b(xb, c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s0[n][i] = s1[n][i] = 0.0f;
-  auto fold = [&](float fa, float fb) {
+    for (int i = 0; i < 4; ++i) fA[i] = fB[i] = 1.0f;
+    if (C::MX) {
+      load_f(sA, sB, 0);
+    } else if (block_scale) {
+      fA[0] = __uint_as_float(lds32(sA));
+      fB[0] = __uint_as_float(lds32(sB));
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xv[n] = lds64(xs + n * 32);
+  }
+  __device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t xb, uint32_t sA, uint32_t sB) {
+    // two chains of sums (MX: the sum of the scaled 32-wide blocks, and the block at hand)
+    float s0[NT][4], s1[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s0[n][i] = s1[n][i] = 0.0f;
+    auto fold = [&](float fa, float fb) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        s0[n][0] = __fmaf_rn(s1[n][0], fa, s0[n][0]);
+        s0[n][1] = __fmaf_rn(s1[n][1], fa, s0[n][1]);
+        s0[n][2] = __fmaf_rn(s1[n][2], fb, s0[n][2]);
+        s0[n][3] = __fmaf_rn(s1[n][3], fb, s0[n][3]);
+        s1[n][0] = s1[n][1] = s1[n][2] = s1[n][3] = 0.0f;
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (WT == kMx4 && c == 2) load_f(sA, sB, 1);
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        if (WT == kMx4) {
+          uint32_t va[4], vb[4];
+          weights8(r[c][2 * cc], va);
+          weights8(r[c][2 * cc + 1], vb);
+          const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]}, a1[4] = {va[2], vb[2], va[3], vb[3]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(s1[n], a0, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
+            mma_f16(s1[n], a1, b[c % DEPTH][cc][n][BW - 2], b[c % DEPTH][cc][n][BW - 1]);
+          }
+          fold(fA[(2 * c + cc) & 3], fB[(2 * c + cc) & 3]);
+        } else {
+          uint32_t a[4];
+          weights4<WT>(r[c][2 * cc], a[0], a[2]);
+          weights4<WT>(r[c][2 * cc + 1], a[1], a[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma_f16(C::MX || cc == 1 ? s1[n] : s0[n], a, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
+          if (C::MX && cc == 1) fold(fA[c], fB[c]);  // a 32-wide block is done
+        }
+      }
+      if (c + DEPTH < 4) load_b(xb, c + DEPTH);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      s0[n][0] = __fmaf_rn(s1[n][0], fa, s0[n][0]);
-      s0[n][1] = __fmaf_rn(s1[n][1], fa, s0[n][1]);
-      s0[n][2] = __fmaf_rn(s1[n][2], fb, s0[n][2]);
-      s0[n][3] = __fmaf_rn(s1[n][3], fb, s0[n][3]);
-      s1[n][0] = s1[n][1] = s1[n][2] = s1[n][3] = 0.0f;
-    }
-  };
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (WT == kMx4 && c == 2) load_f(1);
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      if (WT == kMx4) {
-        uint32_t va[4], vb[4];
-        weights8(r[c][2 * cc], va);
-        weights8(r[c][2 * cc + 1], vb);
-        const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]}, a1[4] = {va[2], vb[2], va[3], vb[3]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_f16(s1[n], a0, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
-          mma_f16(s1[n], a1, b[c % DEPTH][cc][n][BW - 2], b[c % DEPTH][cc][n][BW - 1]);
-        }
-        fold(fA[(2 * c + cc) & 3], fB[(2 * c + cc) & 3]);
+      const float x0 = __uint_as_float(xv[n].x), x1 = __uint_as_float(xv[n].y);
+      if (C::MX) {
+        acc[n][0] = __fmaf_rn(s0[n][0], x0, acc[n][0]);
+        acc[n][1] = __fmaf_rn(s0[n][1], x1, acc[n][1]);
+        acc[n][2] = __fmaf_rn(s0[n][2], x0, acc[n][2]);
+        acc[n][3] = __fmaf_rn(s0[n][3], x1, acc[n][3]);
       } else {
-        uint32_t a[4];
-        weights4<WT>(r[c][2 * cc], a[0], a[2]);
-        weights4<WT>(r[c][2 * cc + 1], a[1], a[3]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma_f16(C::MX || cc == 1 ? s1[n] : s0[n], a, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
-        if (C::MX && cc == 1) fold(fA[c], fB[c]);  // a 32-wide block is done
+        acc[n][0] = __fmaf_rn(s0[n][0] + s1[n][0], x0 * fA[0], acc[n][0]);
+        acc[n][1] = __fmaf_rn(s0[n][1] + s1[n][1], x1 * fA[0], acc[n][1]);
+        acc[n][2] = __fmaf_rn(s0[n][2] + s1[n][2], x0 * fB[0], acc[n][2]);
+        acc[n][3] = __fmaf_rn(s0[n][3] + s1[n][3], x1 * fB[0], acc[n][3]);
       }
     }
-    if (c + DEPTH < 4) load_b(c + DEPTH);
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const float x0 = __uint_as_float(xv[n].x), x1 = __uint_as_float(xv[n].y);
-    if (C::MX) {
-      acc[n][0] = __fmaf_rn(s0[n][0], x0, acc[n][0]);
-      acc[n][1] = __fmaf_rn(s0[n][1], x1, acc[n][1]);
-      acc[n][2] = __fmaf_rn(s0[n][2], x0, acc[n][2]);
-      acc[n][3] = __fmaf_rn(s0[n][3], x1, acc[n][3]);
-    } else {
-      acc[n][0] = __fmaf_rn(s0[n][0] + s1[n][0], x0 * fA[0], acc[n][0]);
-      acc[n][1] = __fmaf_rn(s0[n][1] + s1[n][1], x1 * fA[0], acc[n][1]);
-      acc[n][2] = __fmaf_rn(s0[n][2] + s1[n][2], x0 * fB[0], acc[n][2]);
-      acc[n][3] = __fmaf_rn(s0[n][3] + s1[n][3], x1 * fB[0], acc[n][3]);
-    }
-  }
-}
+};
 
 // One span of an activation row, PER values a lane: scaled to f16 in shared
 // memory at `at`, the scale to put back at `sc`.
@@ -536,8 +541,8 @@ struct Walk {
   }
 };
 
-template <int WT, int PHASE, bool SMALL>
-__global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
+template <int WT, int PHASE>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
   using C = Cfg<WT, PHASE>;
   constexpr int PER = C::PER;
   extern __shared__ uint8_t smem_raw[];
@@ -546,12 +551,12 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
   // stages of weights | f16 activations | weight scales | activation span scales | control
   const uint32_t S = p.stages;
   const int cap = p.cap;
-  const uint32_t x_ring = base + S * kStageW;
+  const uint32_t x_ring = base + S * C::STAGE_W;
   const uint32_t x_bytes = cap * C::PITCH;
   const uint32_t s_ring = x_ring + S * x_bytes;
   const uint32_t v_ring = s_ring + S * C::SCALE_BYTES;
-  const uint32_t v_bytes = cap * 4;
-  Ctl<SMALL>* ctl = reinterpret_cast<Ctl<SMALL>*>(bp + (v_ring + S * v_bytes - base));
+  const uint32_t v_bytes = C::BOXES * cap * 4;
+  Ctl* ctl = reinterpret_cast<Ctl*>(bp + (v_ring + S * v_bytes - base));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.T * p.k;
 
@@ -603,9 +608,10 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
     return;
   }
 
+  const int nbox = (p.K + C::BOX_K - 1) / C::BOX_K;  // boxes along K
   const bool words = p.mode == kScaleBlock || p.mode == kScaleMx;  // one scale word a row and 128 values of K
   const bool partial = PHASE == 2 && segs1 > 1;                    // kernel 1 left sums of K segments
-  // where the raw scale words of span v of stage s arrive: the end of their place
+  // where the raw scale words v of stage s arrive: the end of their place
   auto raw_words = [&](uint32_t s, int v) {
     return s_ring + s * C::SCALE_BYTES + (v + 1) * kRows * C::SCALE_ROW - kRows * 4;
   };
@@ -618,9 +624,12 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
       if (lane == 0) {
         const uint32_t fb = smem_u32(&ctl->full[s]);
         const int e = ctl->cexp[q.ch];
-        mbar_arrive_expect_tx(fb, kStageW);
+        const int boxes = min(C::BOXES, nbox - q.kst * C::BOXES);
+        mbar_arrive_expect_tx(fb, boxes * kBoxW);
         // rows past the tensor's channels or K arrive as zeros
-        tma_load_3d(base + s * kStageW, &tmW, q.kst * 128, q.blk * kPer, PHASE == 1 ? 2 * e : e, fb);
+        for (int v = 0; v < boxes; ++v)
+          tma_load_3d(base + s * C::STAGE_W + v * kBoxW, &tmW, (q.kst * C::BOXES + v) * 128, q.blk * kPer,
+                      PHASE == 1 ? 2 * e : e, fb);
       }
     };
     auto load_rest = [&](uint32_t s, const Step& q) {
@@ -628,8 +637,8 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
         const int e = ctl->cexp[q.ch];
         const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * p.N : lane * 4);
 #pragma unroll
-        for (int v = 0; v < C::SPANS; ++v) {
-          const int64_t kb = q.kst * C::SPANS + v;
+        for (int v = 0; v < C::BOXES * C::WORDS; ++v) {
+          const int64_t kb = q.kst * C::BOXES * C::WORDS + v;
           const bool ok = kb < nkb;
           const float* src = p.mode == kScaleMx ? p.scale + kb * (p.El * scale_rows) + e * scale_rows + n0
                                                 : p.scale + (e * static_cast<int64_t>(nkb) + kb) * scale_rows + n0;
@@ -742,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
       }
       if (C::MX) {  // a lane: four rows' words of four codes, as floats
 #pragma unroll
-        for (int v = 0; v < C::SPANS; ++v) {
+        for (int v = 0; v < C::BOXES * C::WORDS; ++v) {
           const uint4 u = lds128(raw_words(s, v) + lane * 16);
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
           const uint32_t dst = s_ring + s * C::SCALE_BYTES + (v * kRows + lane * 4) * C::SCALE_ROW;
@@ -755,23 +764,28 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
                                             __float_as_uint(e8m0_value(w[r] >> 24))));
         }
       }
-      const int n = ctl->cnum[q.ch], col = q.kst * C::KE + lane * PER;
+      const int n = ctl->cnum[q.ch];
       const uint32_t at = x_ring + s * x_bytes, av = v_ring + s * v_bytes;
       if (partial) {
         const int st = ctl->cstart[q.ch];
-        for (int i = 0; i < n; ++i) {
-          float v[PER];
-          join(st + i, col, col < p.K, v);
-          store_span<PER>(v, at + i * C::PITCH, av + i * 4, lane);
-        }
+        for (int i = 0; i < n; ++i)
+          for (int b = 0; b < C::BOXES; ++b) {
+            const int col = q.kst * C::KE + b * C::BOX_K + lane * PER;
+            float v[PER];
+            join(st + i, col, col < p.K, v);
+            store_span<PER>(v, at + i * C::PITCH + b * C::SPAN_BYTES, av + (b * cap + i) * 4, lane);
+          }
       } else {
-        for (int i = 0; i < n; i += 2) {  // two rows' latencies together (an odd last row twice)
-          const int i1 = i + 1 < n ? i + 1 : i;
+        // two spans' latencies together: a row's two, or (one a row) two rows' (an odd last one twice)
+        constexpr int kRowsAtOnce = C::BOXES == 2 ? 1 : 2;
+        for (int i = 0; i < n; i += kRowsAtOnce) {
+          const int i1 = C::BOXES == 2 ? i : (i + 1 < n ? i + 1 : i), b1 = C::BOXES - 1;
+          const uint32_t at0 = at + i * C::PITCH, at1 = at + i1 * C::PITCH + b1 * C::SPAN_BYTES;
           float v[PER], w[PER];
-          raw(at + i * C::PITCH, v);
-          raw(at + i1 * C::PITCH, w);
-          store_span<PER>(v, at + i * C::PITCH, av + i * 4, lane);
-          store_span<PER>(w, at + i1 * C::PITCH, av + i1 * 4, lane);
+          raw(at0, v);
+          raw(at1, w);
+          store_span<PER>(v, at0, av + i * 4, lane);
+          store_span<PER>(w, at1, av + (b1 * cap + i1) * 4, lane);
         }
       }
       __syncwarp();
@@ -808,10 +822,33 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
           *abort_flag = 1;
           break;
         }
-        const uint32_t st = s_ring + s * C::SCALE_BYTES;
-        contract<WT, PHASE, NT>(acc, base + s * kStageW + w_off, swz, x_ring + s * x_bytes + x_off,
-                         st + (rowA + g) * C::SCALE_ROW, st + (rowB + g) * C::SCALE_ROW, v_ring + s * v_bytes + t4 * 8,
-                         p.mode == kScaleBlock);
+        const uint32_t wt = base + s * C::STAGE_W + w_off, xb = x_ring + s * x_bytes + x_off;
+        const uint32_t sA = s_ring + s * C::SCALE_BYTES + (rowA + g) * C::SCALE_ROW;
+        const uint32_t sB = s_ring + s * C::SCALE_BYTES + (rowB + g) * C::SCALE_ROW;
+        const uint32_t xs = v_ring + s * v_bytes + t4 * 8;
+        constexpr int kScaleBox = C::WORDS * kRows * C::SCALE_ROW;
+        const bool block_scale = p.mode == kScaleBlock;
+        if (C::BOXES == 2 && kst * 2 + 1 < nbox) {
+          if (NT == 1) {
+            Box<WT, PHASE, NT> b0, b1;
+            b0.load(wt, swz, xb, sA, sB, xs, block_scale);
+            b1.load(wt + kBoxW, swz, xb + C::SPAN_BYTES, sA + kScaleBox, sB + kScaleBox, xs + cap * 4, block_scale);
+            b0.contract(acc, xb, sA, sB);
+            b1.contract(acc, xb + C::SPAN_BYTES, sA + kScaleBox, sB + kScaleBox);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              Box<WT, PHASE, NT> b;
+              b.load(wt + v * kBoxW, swz, xb + v * C::SPAN_BYTES, sA + v * kScaleBox, sB + v * kScaleBox,
+                     xs + v * cap * 4, block_scale);
+              b.contract(acc, xb + v * C::SPAN_BYTES, sA + v * kScaleBox, sB + v * kScaleBox);
+            }
+          }
+        } else {
+          Box<WT, PHASE, NT> b;
+          b.load(wt, swz, xb, sA, sB, xs, block_scale);
+          b.contract(acc, xb, sA, sB);
+        }
         fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
@@ -858,12 +895,12 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) decode_kernel(const _
 
     for (Step q = walk.begin(); !walk.done(q) && !timed_out;) {
       const int n = ctl->cnum[q.ch];
-      if (SMALL || n <= 8)
+      if (n <= 8)
         unit(std::integral_constant<int, 1>{}, q);
       else if (n <= 16)
-        unit(std::integral_constant<int, SMALL ? 1 : 2>{}, q);
+        unit(std::integral_constant<int, 2>{}, q);
       else
-        unit(std::integral_constant<int, SMALL ? 1 : 4>{}, q);
+        unit(std::integral_constant<int, 4>{}, q);
       if (PHASE == 2 && !timed_out) {
         // the last unit (over all CTAs) that gets to these 16 columns sums their
         // pairs into y: each warp for the rows of its own, without its neighbours
@@ -982,20 +1019,20 @@ bool shape_ok(int64_t T, int k, int64_t D, int64_t F) {
          F % 16 == 0 && D <= 32768 && F <= 32768;
 }
 
-template <int WT, int PHASE, bool SMALL>
-moe_status launch_size(const void* w, Params p, int grid, cudaStream_t st) {
+template <int WT, int PHASE>
+moe_status launch(const void* w, Params p, int grid, cudaStream_t st) {
   using C = Cfg<WT, PHASE>;
   CUtensorMap tm;
   const uint64_t bytes = WT == kMx4 ? p.K / 2 : p.K;
   if (!make_map(&tm, w, bytes, p.N, static_cast<uint64_t>(p.El) * (PHASE == 1 ? 2 : 1), PHASE == 1 ? kRows / 2 : kRows,
                 PHASE == 1 ? 2 : 1))
     return MOE_ERR_CUDA;
-  const size_t stage = kStageW + static_cast<size_t>(p.cap) * (C::PITCH + 4) + C::SCALE_BYTES;
-  const size_t fixed = 1024 + ctl_bytes<SMALL>();
-  p.stages = static_cast<int>(((SMALL ? kSmemHalf : kSmemLimit) - fixed) / stage);
+  const size_t stage = C::STAGE_W + static_cast<size_t>(p.cap) * (C::PITCH + 4 * C::BOXES) + C::SCALE_BYTES;
+  const size_t fixed = 1024 + kCtlBytes;
+  p.stages = static_cast<int>((kSmemLimit - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = fixed + p.stages * stage;
-  auto kernel = decode_kernel<WT, PHASE, SMALL>;
+  auto kernel = decode_kernel<WT, PHASE>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
@@ -1009,11 +1046,6 @@ moe_status launch_size(const void* w, Params p, int grid, cudaStream_t st) {
   cfg.numAttrs = PHASE == 2 ? 1 : 0;
   MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tm, p));
   return MOE_OK;
-}
-
-template <int WT, int PHASE>
-moe_status launch(const void* w, const Params& p, int grid, cudaStream_t st) {
-  return p.cap == 8 ? launch_size<WT, PHASE, true>(w, p, grid, st) : launch_size<WT, PHASE, false>(w, p, grid, st);
 }
 
 template <int PHASE>
@@ -1084,7 +1116,7 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   const int64_t R = T * k;
   float* h = reinterpret_cast<float*>(ws);
   float* o = reinterpret_cast<float*>(ws + h_bytes(R, F));
-  const int ke = type == MOE_WEIGHT_MXFP4 ? 256 : 128;
+  const int ke = 256;  // values of K in a stage, of either width
   Params p{};
   p.ids = topk_ids;
   p.topk_w = topk_w;
