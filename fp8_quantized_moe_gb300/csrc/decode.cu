@@ -343,10 +343,14 @@ __device__ void build_chunks(const Params& p, Ctl* c) {
 // One box: 16 rows x 128 bytes of weights at `wt` (row A + lane / 4 and row
 // B + lane / 4 of the fragment), activations at `xb` (already this lane's), the
 // scales of this lane's two weight rows at sA, sB and the activations' span
-// scales at `xs`.  Past the end of K both the weights and the activations are
+// scales at `xs` (shared-memory addresses).  Past the end of K both the weights and the activations are
 // zeros.  The shared-memory loads run DEPTH pairs of 16-byte chunks ahead of
 // the products (all of them at NT <= 2): taken as they were needed, their
 // latencies made a stage 1.7 times as long.
+struct BoxAt {
+  uint32_t wt, xb, sA, sB, xs;
+};
+
 template <int WT, int PHASE, int NT>
 struct Box {
   using C = Cfg<WT, PHASE>;
@@ -375,8 +379,8 @@ struct Box {
         }
       }
   }
-  __device__ __forceinline__ void load_f(uint32_t sA, uint32_t sB, int v) {
-    const uint4 a = lds128(sA + v * kRows * 16), d = lds128(sB + v * kRows * 16);
+  __device__ __forceinline__ void load_f(const BoxAt& at, int v) {
+    const uint4 a = lds128(at.sA + v * kRows * 16), d = lds128(at.sB + v * kRows * 16);
     fA[0] = __uint_as_float(a.x);
     fA[1] = __uint_as_float(a.y);
     fA[2] = __uint_as_float(a.z);
@@ -386,25 +390,24 @@ struct Box {
     fB[2] = __uint_as_float(d.z);
     fB[3] = __uint_as_float(d.w);
   }
-  __device__ __forceinline__ void load(uint32_t wt, uint32_t swz, uint32_t xb, uint32_t sA, uint32_t sB, uint32_t xs,
-                                       bool block_scale) {
+  __device__ __forceinline__ void load(const BoxAt& at, uint32_t swz, bool block_scale) {
     const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
 #pragma unroll
-    for (int c = 0; c < 4; ++c) ldmatrix_x4(wt + (((2 * c + hi) * 16) ^ swz), r[c]);
+    for (int c = 0; c < 4; ++c) ldmatrix_x4(at.wt + (((2 * c + hi) * 16) ^ swz), r[c]);
 #pragma unroll
-    for (int c = 0; c < DEPTH; ++c) load_b(xb, c);
+    for (int c = 0; c < DEPTH; ++c) load_b(at.xb, c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) fA[i] = fB[i] = 1.0f;
     if (C::MX) {
-      load_f(sA, sB, 0);
+      load_f(at, 0);
     } else if (block_scale) {
-      fA[0] = __uint_as_float(lds32(sA));
-      fB[0] = __uint_as_float(lds32(sB));
+      fA[0] = __uint_as_float(lds32(at.sA));
+      fB[0] = __uint_as_float(lds32(at.sB));
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xv[n] = lds64(xs + n * 32);
+    for (int n = 0; n < NT; ++n) xv[n] = lds64(at.xs + n * 32);
   }
-  __device__ __forceinline__ void contract(float (&acc)[NT][4], uint32_t xb, uint32_t sA, uint32_t sB) {
+  __device__ __forceinline__ void contract(float (&acc)[NT][4], const BoxAt& at) {
     // two chains of sums (MX: the sum of the scaled 32-wide blocks, and the block at hand)
     float s0[NT][4], s1[NT][4];
 #pragma unroll
@@ -423,7 +426,7 @@ struct Box {
     };
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (WT == kMx4 && c == 2) load_f(sA, sB, 1);
+      if (WT == kMx4 && c == 2) load_f(at, 1);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         if (WT == kMx4) {
@@ -447,7 +450,7 @@ struct Box {
           if (C::MX && cc == 1) fold(fA[c], fB[c]);  // a 32-wide block is done
         }
       }
-      if (c + DEPTH < 4) load_b(xb, c + DEPTH);
+      if (c + DEPTH < 4) load_b(at.xb, c + DEPTH);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -632,30 +635,59 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                       PHASE == 1 ? 2 * e : e, fb);
       }
     };
+    // This lane's sources at a unit's first stage, kept over the unit: its part
+    // of the scale words, and of the first kKept x 32 chunks of activations.
+    constexpr int kChunks = C::ROW_BYTES / 16, kVals = PHASE == 1 ? 8 : 4;  // 16-byte chunks of a row, values in one
+    constexpr int kKept = 4;
+    constexpr int kWords = C::BOXES * C::WORDS;
+    int unit = -1, n = 0, st = 0;
+    const float* sc = p.scale;
+    const uint8_t* xsrc[kKept];
+    const int64_t kb_pitch = p.mode == kScaleMx ? p.El * scale_rows : scale_rows;  // from one 128-wide block to the next
+    auto row_src = [&](int i) {  // chunk i of the unit's activations at K = 0
+      const int r = i / kChunks, c = i % kChunks;
+      const int64_t row = PHASE == 1 ? ctl->order[st + r] / p.k : st + r;
+      return static_cast<const uint8_t*>(p.act) + (row * p.K + c * kVals) * (PHASE == 1 ? 2 : 4);
+    };
     auto load_rest = [&](uint32_t s, const Step& q) {
-      if (words) {
+      if (q.u != unit) {
+        unit = q.u;
+        n = ctl->cnum[q.ch];
+        st = ctl->cstart[q.ch];
         const int e = ctl->cexp[q.ch];
-        const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * p.N : lane * 4);
+        if (words) {
+          const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * p.N : lane * 4);
+          sc = p.scale + (p.mode == kScaleMx ? e * scale_rows : static_cast<int64_t>(e) * nkb * scale_rows) + n0;
+        }
 #pragma unroll
-        for (int v = 0; v < C::BOXES * C::WORDS; ++v) {
-          const int64_t kb = q.kst * C::BOXES * C::WORDS + v;
+        for (int j = 0; j < kKept; ++j)
+          xsrc[j] = lane + 32 * j < n * kChunks && !partial ? row_src(lane + 32 * j) : static_cast<const uint8_t*>(p.act);
+      }
+      if (words) {
+#pragma unroll
+        for (int v = 0; v < kWords; ++v) {
+          const int64_t kb = q.kst * kWords + v;
           const bool ok = kb < nkb;
-          const float* src = p.mode == kScaleMx ? p.scale + kb * (p.El * scale_rows) + e * scale_rows + n0
-                                                : p.scale + (e * static_cast<int64_t>(nkb) + kb) * scale_rows + n0;
-          cp_async_16(raw_words(s, v) + lane * 16, ok ? src : p.scale, ok ? 16u : 0u);
+          cp_async_16(raw_words(s, v) + lane * 16, ok ? sc + kb * kb_pitch : p.scale, ok ? 16u : 0u);
         }
       }
       if (!partial) {
-        constexpr int kChunks = C::ROW_BYTES / 16, kVals = PHASE == 1 ? 8 : 4;  // 16-byte chunks of a row, values in one
-        const int n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
-        for (int i = lane; i < n * kChunks; i += 32) {
+        const int64_t k0 = static_cast<int64_t>(q.kst) * C::ROW_BYTES;
+        const uint32_t dst = x_ring + s * x_bytes;
+        // K is a multiple of 16: a chunk is all in or out
+#pragma unroll
+        for (int j = 0; j < kKept; ++j) {
+          const int i = lane + 32 * j;
+          if (i < n * kChunks) {
+            const int r = i / kChunks, c = i % kChunks;
+            const bool ok = q.kst * C::KE + c * kVals < p.K;
+            cp_async_16(dst + r * C::PITCH + c * 16, ok ? xsrc[j] + k0 : xsrc[j], ok ? 16u : 0u);
+          }
+        }
+        for (int i = lane + 32 * kKept; i < n * kChunks; i += 32) {
           const int r = i / kChunks, c = i % kChunks;
-          const int64_t row = PHASE == 1 ? ctl->order[st + r] / p.k : st + r;
-          const int col = q.kst * C::KE + c * kVals;
-          const bool ok = col < p.K;  // K is a multiple of 16
-          const uint8_t* src = static_cast<const uint8_t*>(p.act);
-          cp_async_16(x_ring + s * x_bytes + r * C::PITCH + c * 16,
-                      ok ? src + (row * p.K + col) * (PHASE == 1 ? 2 : 4) : src, ok ? 16u : 0u);
+          const bool ok = q.kst * C::KE + c * kVals < p.K;
+          cp_async_16(dst + r * C::PITCH + c * 16, ok ? row_src(i) + k0 : static_cast<const uint8_t*>(p.act), ok ? 16u : 0u);
         }
       }
       cp_async_arrive(smem_u32(&ctl->xraw[s]));
@@ -815,46 +847,98 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-      for (int kst = q.kst; kst < q.end && !timed_out; ++kst) {
-        if (!mbar_wait_bounded_warp(smem_u32(&ctl->xfull[s]), ph, abort_flag, kWaitLimitNs) ||
-            !mbar_wait_bounded_warp(smem_u32(&ctl->full[s]), ph, abort_flag, kWaitLimitNs)) {
+      // Up to eight tokens: boxes alternate between two register sets, one box's
+      // loads in flight while the other's products run.  A stage goes back as
+      // soon as its last box is done; the next is waited for before that only if
+      // it is already there.
+      const int first = q.kst * C::BOXES, last = min(q.end * C::BOXES, nbox);
+      uint32_t ls = s, lph = ph;  // the stage that the next load reads
+      auto ready = [&] {
+        return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&ctl->xfull[ls]), lph) &&
+                                           mbar_try_wait(smem_u32(&ctl->full[ls]), lph));
+      };
+      auto wait = [&] {
+        if (!mbar_wait_bounded_warp(smem_u32(&ctl->xfull[ls]), lph, abort_flag, kWaitLimitNs) ||
+            !mbar_wait_bounded_warp(smem_u32(&ctl->full[ls]), lph, abort_flag, kWaitLimitNs)) {
           timed_out = true;
           *abort_flag = 1;
-          break;
         }
-        const uint32_t wt = base + s * C::STAGE_W + w_off, xb = x_ring + s * x_bytes + x_off;
-        const uint32_t sA = s_ring + s * C::SCALE_BYTES + (rowA + g) * C::SCALE_ROW;
-        const uint32_t sB = s_ring + s * C::SCALE_BYTES + (rowB + g) * C::SCALE_ROW;
-        const uint32_t xs = v_ring + s * v_bytes + t4 * 8;
-        constexpr int kScaleBox = C::WORDS * kRows * C::SCALE_ROW;
-        const bool block_scale = p.mode == kScaleBlock;
-        if (C::BOXES == 2 && kst * 2 + 1 < nbox) {
-          if (NT == 1) {
-            Box<WT, PHASE, NT> b0, b1;
-            b0.load(wt, swz, xb, sA, sB, xs, block_scale);
-            b1.load(wt + kBoxW, swz, xb + C::SPAN_BYTES, sA + kScaleBox, sB + kScaleBox, xs + cap * 4, block_scale);
-            b0.contract(acc, xb, sA, sB);
-            b1.contract(acc, xb + C::SPAN_BYTES, sA + kScaleBox, sB + kScaleBox);
-          } else {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              Box<WT, PHASE, NT> b;
-              b.load(wt + v * kBoxW, swz, xb + v * C::SPAN_BYTES, sA + v * kScaleBox, sB + v * kScaleBox,
-                     xs + v * cap * 4, block_scale);
-              b.contract(acc, xb + v * C::SPAN_BYTES, sA + v * kScaleBox, sB + v * kScaleBox);
-            }
+      };
+      auto box_at = [&](uint32_t st, int v) {
+        BoxAt a;
+        a.wt = base + st * C::STAGE_W + v * kBoxW + w_off;
+        a.xb = x_ring + st * x_bytes + v * C::SPAN_BYTES + x_off;
+        a.sA = s_ring + st * C::SCALE_BYTES + (v * C::WORDS * kRows + rowA + g) * C::SCALE_ROW;
+        a.sB = a.sA + (rowB - rowA) * C::SCALE_ROW;
+        a.xs = v_ring + st * v_bytes + v * cap * 4 + t4 * 8;
+        return a;
+      };
+      // box j of the unit: its loads, and what follows when its products are done
+      auto load = [&](Box<WT, PHASE, NT>& b, int j) {
+        b.load(box_at(ls, C::BOXES == 2 ? j & 1 : 0), swz, p.mode == kScaleBlock);
+        if (C::BOXES == 1 || (j & 1) || j + 1 == last) {
+          if (++ls == S) {
+            ls = 0;
+            lph ^= 1;
           }
-        } else {
-          Box<WT, PHASE, NT> b;
-          b.load(wt, swz, xb, sA, sB, xs, block_scale);
-          b.contract(acc, xb, sA, sB);
         }
-        fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
-        if (++s == S) {
-          s = 0;
-          ph ^= 1;
+      };
+      auto work = [&](Box<WT, PHASE, NT>& b, int j) {
+        b.contract(acc, box_at(s, C::BOXES == 2 ? j & 1 : 0));
+        if (C::BOXES == 1 || (j & 1) || j + 1 == last) {
+          fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      };
+      if constexpr (NT == 1) {
+        Box<WT, PHASE, NT> b0, b1;
+        wait();
+        if (!timed_out) load(b0, first);
+        for (int j = first; j < last && !timed_out; j += 2) {  // first is even (two boxes a stage) or any (one)
+          if (j + 1 < last) {
+            if (C::BOXES == 1) {
+              if (ready()) {
+                load(b1, j + 1);
+                work(b0, j);
+              } else {
+                work(b0, j);
+                wait();
+                if (timed_out) break;
+                load(b1, j + 1);
+              }
+            } else {
+              load(b1, j + 1);
+              work(b0, j);
+            }
+            if (j + 2 < last) {
+              if (ready()) {
+                load(b0, j + 2);
+                work(b1, j + 1);
+              } else {
+                work(b1, j + 1);
+                wait();
+                if (timed_out) break;
+                load(b0, j + 2);
+              }
+            } else {
+              work(b1, j + 1);
+            }
+          } else {
+            work(b0, j);
+          }
+        }
+      } else {  // (two sets of more tokens' fragments do not fit in the registers)
+        for (int j = first; j < last; ++j) {
+          if (C::BOXES == 1 || !(j & 1)) wait();
+          if (timed_out) break;
+          Box<WT, PHASE, NT> b;
+          load(b, j);
+          work(b, j);
         }
       }
       if (timed_out) return;
