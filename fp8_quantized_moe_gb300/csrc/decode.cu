@@ -88,16 +88,18 @@ struct Params {
   int mode;
   int cap, stages;  // pairs a chunk; ring stages
   int smax;         // segments of K at most
-  int grid1;        // CTAs of kernel 1
-  int nblock1, nst1;  // row blocks and K stages of kernel 1
+  int grid1, grid2;      // CTAs of the two kernels,
+  int nblock1, nblock2;  // their row blocks
+  int nst1, nst2;        // and K stages
 };
 
 struct Ctl {
   uint64_t full[kMaxStages], xraw[kMaxStages], xfull[kMaxStages], empty[kMaxStages];
-  int abort_flag, no_abort, err, nchunk;
+  int abort_flag, no_abort, err, nchunk, segs1, segs2;
   uint16_t pos[kMaxPairs];     // slot of pair i (pairs sorted by expert), 0xFFFF: not local
   uint16_t order[kMaxPairs];   // pair of slot s
   uint16_t cexp[kMaxPairs], cstart[kMaxPairs], cnum[kMaxPairs];
+  uint16_t cfirst[kMaxPairs], ccount[kMaxPairs];  // the first chunk of the chunk's expert, and how many it has
   uint16_t num[kMaxExperts];
 };
 
@@ -125,18 +127,13 @@ struct Cfg {
 };
 
 // How many segments of K: the fewest stages on the busiest CTA, a unit's
-// start and end counted as two stages.
+// start and end counted as two stages.  One warp, a lane a choice (at most
+// 2^19 units x 8 segments x 130 stages: 32 bits hold the cost).
 __device__ __forceinline__ int pick_segs(int units, int nst, int grid, int smax) {
-  int best = 1;
-  int64_t cost = INT64_MAX;
-  for (int s = 1; s <= smax && s <= nst; ++s) {
-    const int64_t c = static_cast<int64_t>((static_cast<int64_t>(units) * s + grid - 1) / grid) * ((nst + s - 1) / s + 2);
-    if (c < cost) {
-      cost = c;
-      best = s;
-    }
-  }
-  return best;
+  const int s = (threadIdx.x & 31) + 1;
+  const unsigned int cost = s <= smax && s <= nst ? static_cast<unsigned>((units * s + grid - 1) / grid * ((nst + s - 1) / s + 2))
+                                                  : 0xFFFFFFFFu;
+  return __ffs(__ballot_sync(0xffffffffu, cost == __reduce_min_sync(0xffffffffu, cost)));
 }
 
 constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
@@ -274,6 +271,8 @@ __device__ __forceinline__ void build_chunks_warp(const Params& p, Ctl* c) {
       c->cexp[q] = static_cast<uint16_t>(e);
       c->cstart[q] = static_cast<uint16_t>(start + rank);
       c->cnum[q] = static_cast<uint16_t>(min(p.cap, n - rank));
+      c->cfirst[q] = static_cast<uint16_t>(chunk);
+      c->ccount[q] = static_cast<uint16_t>((n + p.cap - 1) / p.cap);
     }
   } else if (lane < R) {
     c->pos[lane] = 0xFFFF;
@@ -318,6 +317,8 @@ __device__ void build_chunks(const Params& p, Ctl* c) {
       c->cexp[c0 + j] = static_cast<uint16_t>(e);
       c->cstart[c0 + j] = static_cast<uint16_t>(off + j * p.cap);
       c->cnum[c0 + j] = static_cast<uint16_t>(min(p.cap, n - j * p.cap));
+      c->cfirst[c0 + j] = static_cast<uint16_t>(c0);
+      c->ccount[c0 + j] = static_cast<uint16_t>(nc);
     }
     if (e < p.El) c->num[e] = static_cast<uint16_t>(off);
     both = __shfl_sync(0xffffffffu, both, 31);
@@ -504,16 +505,25 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
 }
 
 // Where a CTA is: unit u = (chunk, row block, segment), stages [kst, end) of
-// it left.  Units are numbered expert-major.
+// it left.  Units are numbered by expert, row block, segment and last by the
+// expert's chunks, so that these read the same weights together.
 struct Step {
   int u, ch, blk, seg, kst, end;
 };
 struct Walk {
   int nblock, segs, nst, total;
+  const Ctl* ctl;
   __device__ __forceinline__ void open(Step& q) const {
     const int per = nblock * segs;
-    q.ch = q.u / per;
-    const int r = q.u - q.ch * per;
+    const int any = q.u / per;  // a chunk of the expert
+    const int first = ctl->cfirst[any], count = ctl->ccount[any];
+    int r = q.u - first * per;
+    if (count > 1) {
+      q.ch = first + r % count;
+      r /= count;
+    } else {
+      q.ch = first;
+    }
     q.blk = r / segs;
     q.seg = r - q.blk * segs;
     q.kst = q.seg * nst / segs;
@@ -589,16 +599,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     __syncthreads();
     if (warp == 1) build_chunks(p, ctl);
   }
+  if (warp == 1) {
+    __syncwarp();
+    const int segs1 = pick_segs(ctl->nchunk * p.nblock1, p.nst1, p.grid1, p.smax);
+    const int segs2 = pick_segs(ctl->nchunk * p.nblock2, p.nst2, p.grid2, p.smax);
+    if (lane == 0) {
+      ctl->segs1 = segs1;
+      ctl->segs2 = segs2;
+    }
+  }
   __syncthreads();
 
   const int nchunk = ctl->nchunk;
   constexpr int kPer = PHASE == 1 ? kRows / 2 : kRows;  // channels of a unit
-  const int segs1 = pick_segs(nchunk * p.nblock1, p.nst1, p.grid1, p.smax);  // kernel 1's, in both kernels
+  const int segs1 = ctl->segs1;
   Walk walk;
-  walk.nblock = (p.N + kPer - 1) / kPer;
-  walk.nst = (p.K + C::KE - 1) / C::KE;
-  walk.segs = PHASE == 1 ? segs1 : pick_segs(nchunk * walk.nblock, walk.nst, gridDim.x, p.smax);
+  walk.nblock = PHASE == 1 ? p.nblock1 : p.nblock2;
+  walk.nst = PHASE == 1 ? p.nst1 : p.nst2;
+  walk.segs = PHASE == 1 ? segs1 : ctl->segs2;
   walk.total = nchunk * walk.nblock * walk.segs;
+  walk.ctl = ctl;
   volatile int* abort_flag = &ctl->abort_flag;
   bool timed_out = false;
 
@@ -847,6 +867,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+      // what the unit's end needs, asked for before its products
+      const int e = ctl->cexp[q.ch], n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
+      const int ca = q.blk * kPer + (PHASE == 1 ? 8 * mw : 16 * mw) + g;  // channel of row A
+      const int cb = PHASE == 1 ? ca : ca + 8;
+      float fa = 1.0f, fb = 1.0f;
+      if (p.mode == kScaleChannel) {
+        const float* sc = p.scale + static_cast<int64_t>(e) * (PHASE == 1 ? 2 * p.N : p.N);
+        if (ca < p.N) fa = __ldg(sc + ca);
+        if (cb < p.N) fb = __ldg(sc + (PHASE == 1 ? p.N : 0) + cb);
+      } else if (p.mode == kScaleTensor) {
+        fa = fb = __ldg(p.scale);
+      }
+
       // Up to eight tokens: boxes alternate between two register sets, one box's
       // loads in flight while the other's products run.  A stage goes back as
       // soon as its last box is done; the next is waited for before that only if
@@ -942,17 +975,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         }
       }
       if (timed_out) return;
-      const int e = ctl->cexp[q.ch], n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
-      const int ca = q.blk * kPer + (PHASE == 1 ? 8 * mw : 16 * mw) + g;  // channel of row A
-      const int cb = PHASE == 1 ? ca : ca + 8;
-      float fa = 1.0f, fb = 1.0f;
-      if (p.mode == kScaleChannel) {
-        const float* sc = p.scale + static_cast<int64_t>(e) * (PHASE == 1 ? 2 * p.N : p.N);
-        if (ca < p.N) fa = __ldg(sc + ca);
-        if (cb < p.N) fb = __ldg(sc + (PHASE == 1 ? p.N : 0) + cb);
-      } else if (p.mode == kScaleTensor) {
-        fa = fb = __ldg(p.scale);
-      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1212,16 +1234,21 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   p.E = E;
   p.g0 = group_offset;
   p.El = E_local;
-  // Pairs a chunk: eight is one MMA column group and lets both kernels sit on
-  // an SM together; beyond eight tokens, 16 where the experts hold few of them
-  // (the ring gets two more stages than with 32), else 32.
-  p.cap = T <= 8 ? 8 : (T <= 16 || R <= 6 * static_cast<int64_t>(E_local) ? 16 : 32);
+  // Pairs a chunk.  A narrow one leaves the ring more of shared memory; an
+  // expert with more pairs takes several chunks and is read again (from L2: its
+  // chunks run side by side), so it has to be rare: the mean number of pairs an
+  // expert is at most 2 (for 8; Poisson: 1 expert in 4000 has more) or 6 (for 16).
+  p.cap = T <= 8 || R <= 2 * static_cast<int64_t>(E_local) ? 8
+                                                           : (T <= 16 || R <= 6 * static_cast<int64_t>(E_local) ? 16 : 32);
   p.smax = max_segs(R);
   p.nblock1 = static_cast<int>(blocks(F, kRows / 2));
   p.nst1 = static_cast<int>(blocks(D, ke));
+  p.nblock2 = static_cast<int>(blocks(D, kRows));
+  p.nst2 = static_cast<int>(blocks(F, ke));
   // no more CTAs than units (a chunk a pair, all segments)
-  const int64_t u1 = R * p.nblock1 * p.smax, u2 = R * blocks(D, kRows) * p.smax;
+  const int64_t u1 = R * p.nblock1 * p.smax, u2 = R * p.nblock2 * p.smax;
   p.grid1 = static_cast<int>(u1 < sms ? u1 : sms);
+  p.grid2 = static_cast<int>(u2 < sms ? u2 : sms);
   p.act = x;
   p.scale = static_cast<const float*>(s_in);
   p.out = h;
@@ -1236,5 +1263,5 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   p.K = static_cast<int>(F);
   p.N = static_cast<int>(D);
   p.mode = kout;
-  return launch_type<2>(type, w_out, p, static_cast<int>(u2 < sms ? u2 : sms), st);
+  return launch_type<2>(type, w_out, p, p.grid2, st);
 }
