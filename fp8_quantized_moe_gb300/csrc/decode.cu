@@ -114,8 +114,9 @@ struct Cfg {
   static constexpr int KE = BOXES * BOX_K;              // and in a stage
   static constexpr int STAGE_W = BOXES * kBoxW;
   static constexpr int WORDS = BOX_K / 128;             // scale words of a row and box
-  // a row's scale word as it is used: one float, or (MX) its four blocks' floats
-  static constexpr int SCALE_ROW = MX ? 16 : 4;
+  // a row's scale word as it is used: one float, or (MX) its four blocks' powers
+  // of two as bf16, which holds them all
+  static constexpr int SCALE_ROW = MX ? 8 : 4;
   static constexpr int SCALE_BYTES = BOXES * WORDS * kRows * SCALE_ROW;
   static constexpr int PER = BOX_K / 32;  // values of a span a lane converts
   // bytes of an activation row as it arrives (bf16 x, fp32 h; the f16 form takes
@@ -280,39 +281,49 @@ __device__ __forceinline__ void build_chunks_warp(const Params& p, Ctl* c) {
   if (lane == 0) c->nchunk = total;
 }
 
-// A stable counting sort by one warp: 32 pairs at a time, the rank of a pair
-// among its expert's earlier ones from a warp-wide match and a running count.
-// c->order holds the local expert of every pair until the slots are known,
-// c->num is zero.
-__device__ void build_chunks(const Params& p, Ctl* c) {
-  const int lane = threadIdx.x & 31;
-  const int R = p.T * p.k;
-  for (int i0 = 0; i0 < R; i0 += 32) {
-    const int i = i0 + lane;
-    const int e = i < R ? c->order[i] : 0xFFFF;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    if (e != 0xFFFF) {
-      const int before = c->num[e];
-      c->pos[i] = static_cast<uint16_t>(before + rank);
-    }
-    __syncwarp();
-    if (e != 0xFFFF && (same >> lane) == 1u)  // the last of its expert in this batch
-      c->num[e] = static_cast<uint16_t>(c->pos[i] + 1);
-    __syncwarp();
+// More than 32 pairs, by the whole CTA.  `bits` (shared memory that the ring
+// does not use yet) holds a bit a pair for every local expert: a pair's rank is
+// the number of its expert's bits below its own, so that the order does not
+// depend on when the atomics come.  Behind it, a word an expert: its first
+// chunk and slot.
+__device__ void build_chunks(const Params& p, Ctl* c, uint32_t* bits) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int R = p.T * p.k, W = (R + 31) / 32;
+  uint32_t* first = bits + p.El * W;
+  for (int i = tid; i < p.El * W; i += kThreads) bits[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < R; i += kThreads) {
+    const int e = local_expert(p, i);
+    c->order[i] = static_cast<uint16_t>(e);
+    if (e != 0xFFFF) atomicOr(bits + e * W + i / 32, 1u << (i & 31));
   }
-  int slots = 0, chunks = 0;
-  for (int e0 = 0; e0 < p.El; e0 += 32) {
-    const int e = e0 + lane;
-    const int n = e < p.El ? c->num[e] : 0;
-    const int nc = (n + p.cap - 1) / p.cap;
-    int both = (nc << 16) | n;  // at most 1024 of either
+  __syncthreads();
+  for (int e = tid; e < p.El; e += kThreads) {
+    int n = 0;
+    for (int w = 0; w < W; ++w) n += __popc(bits[e * W + w]);
+    c->num[e] = static_cast<uint16_t>(n);
+  }
+  __syncthreads();
+  if (tid < 32) {  // a lane: a run of consecutive experts
+    const int per = (p.El + 31) / 32, e0 = lane * per, e1 = min(e0 + per, p.El);
+    uint32_t sum = 0;  // chunks above 16 bits of pairs: at most 1024 of either
+    for (int e = e0; e < e1; ++e) sum += c->num[e] | ((c->num[e] + p.cap - 1) / p.cap) << 16;
+    uint32_t at = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, both, o);
-      if (lane >= o) both += a;
+      const uint32_t a = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += a;
     }
-    const int off = slots + (both & 0xFFFF) - n, c0 = chunks + (both >> 16) - nc;
+    if (lane == 31) c->nchunk = at >> 16;
+    at -= sum;
+    for (int e = e0; e < e1; ++e) {
+      first[e] = at;
+      at += c->num[e] | ((c->num[e] + p.cap - 1) / p.cap) << 16;
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < p.El; e += kThreads) {
+    const int n = c->num[e], nc = (n + p.cap - 1) / p.cap, off = first[e] & 0xFFFF, c0 = first[e] >> 16;
     for (int j = 0; j < nc; ++j) {
       c->cexp[c0 + j] = static_cast<uint16_t>(e);
       c->cstart[c0 + j] = static_cast<uint16_t>(off + j * p.cap);
@@ -320,34 +331,21 @@ __device__ void build_chunks(const Params& p, Ctl* c) {
       c->cfirst[c0 + j] = static_cast<uint16_t>(c0);
       c->ccount[c0 + j] = static_cast<uint16_t>(nc);
     }
-    if (e < p.El) c->num[e] = static_cast<uint16_t>(off);
-    both = __shfl_sync(0xffffffffu, both, 31);
-    slots += both & 0xFFFF;
-    chunks += both >> 16;
   }
-  if (lane == 0) c->nchunk = chunks;
-  __syncwarp();
-  for (int i0 = 0; i0 < R; i0 += 32) {
-    const int i = i0 + lane;
-    if (i < R) {
-      const int e = c->order[i];
-      c->pos[i] = e == 0xFFFF ? 0xFFFF : static_cast<uint16_t>(c->num[e] + c->pos[i]);
+  for (int i = tid; i < R; i += kThreads) {
+    const int e = c->order[i];
+    int at = 0xFFFF;
+    if (e != 0xFFFF) {
+      at = (first[e] & 0xFFFF) + __popc(bits[e * W + i / 32] & ((1u << (i & 31)) - 1u));
+      for (int w = 0; w < i / 32; ++w) at += __popc(bits[e * W + w]);
     }
+    c->pos[i] = static_cast<uint16_t>(at);
   }
-  __syncwarp();
-  for (int i0 = 0; i0 < R; i0 += 32) {  // (the experts in `order` are no longer needed)
-    const int i = i0 + lane;
-    if (i < R && c->pos[i] != 0xFFFF) c->order[c->pos[i]] = static_cast<uint16_t>(i);
-  }
+  __syncthreads();
+  for (int i = tid; i < R; i += kThreads)  // (the experts in `order` are no longer needed)
+    if (c->pos[i] != 0xFFFF) c->order[c->pos[i]] = static_cast<uint16_t>(i);
 }
 
-// One box: 16 rows x 128 bytes of weights at `wt` (row A + lane / 4 and row
-// B + lane / 4 of the fragment), activations at `xb` (already this lane's), the
-// scales of this lane's two weight rows at sA, sB and the activations' span
-// scales at `xs` (shared-memory addresses).  Past the end of K both the weights and the activations are
-// zeros.  The shared-memory loads run DEPTH pairs of 16-byte chunks ahead of
-// the products (all of them at NT <= 2): taken as they were needed, their
-// latencies made a stage 1.7 times as long.
 struct BoxAt {
   uint32_t wt, xb, sA, sB, xs;
 };
@@ -362,41 +360,41 @@ struct Box {
   float fA[4], fB[4];
   uint2 xv[NT];
 
-  __device__ __forceinline__ void load_b(uint32_t xb, int c) {
+  __device__ __forceinline__ void load_b(const BoxAt& at, int c) {
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (WT == kMx4) {
-          const uint4 v = lds128(xb + n * 8 * C::PITCH + (2 * c + cc) * 64);
+          const uint4 v = lds128(at.xb + n * 8 * C::PITCH + (2 * c + cc) * 64);
           b[c % DEPTH][cc][n][0] = v.x;
           b[c % DEPTH][cc][n][1] = v.y;
           b[c % DEPTH][cc][n][BW - 2] = v.z;
           b[c % DEPTH][cc][n][BW - 1] = v.w;
         } else {
-          const uint2 v = lds64(xb + n * 8 * C::PITCH + (2 * c + cc) * 32);
+          const uint2 v = lds64(at.xb + n * 8 * C::PITCH + (2 * c + cc) * 32);
           b[c % DEPTH][cc][n][0] = v.x;
           b[c % DEPTH][cc][n][1] = v.y;
         }
       }
   }
   __device__ __forceinline__ void load_f(const BoxAt& at, int v) {
-    const uint4 a = lds128(at.sA + v * kRows * 16), d = lds128(at.sB + v * kRows * 16);
-    fA[0] = __uint_as_float(a.x);
-    fA[1] = __uint_as_float(a.y);
-    fA[2] = __uint_as_float(a.z);
-    fA[3] = __uint_as_float(a.w);
-    fB[0] = __uint_as_float(d.x);
-    fB[1] = __uint_as_float(d.y);
-    fB[2] = __uint_as_float(d.z);
-    fB[3] = __uint_as_float(d.w);
+    const uint2 a = lds64(at.sA + v * kRows * C::SCALE_ROW), d = lds64(at.sB + v * kRows * C::SCALE_ROW);
+    fA[0] = bf16lo(a.x);
+    fA[1] = bf16hi(a.x);
+    fA[2] = bf16lo(a.y);
+    fA[3] = bf16hi(a.y);
+    fB[0] = bf16lo(d.x);
+    fB[1] = bf16hi(d.x);
+    fB[2] = bf16lo(d.y);
+    fB[3] = bf16hi(d.y);
   }
   __device__ __forceinline__ void load(const BoxAt& at, uint32_t swz, bool block_scale) {
     const int hi = (threadIdx.x >> 4) & 1;  // lanes 16..31 address the second chunk of a pair
 #pragma unroll
     for (int c = 0; c < 4; ++c) ldmatrix_x4(at.wt + (((2 * c + hi) * 16) ^ swz), r[c]);
 #pragma unroll
-    for (int c = 0; c < DEPTH; ++c) load_b(at.xb, c);
+    for (int c = 0; c < DEPTH; ++c) load_b(at, c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) fA[i] = fB[i] = 1.0f;
     if (C::MX) {
@@ -451,7 +449,7 @@ struct Box {
           if (C::MX && cc == 1) fold(fA[c], fB[c]);  // a 32-wide block is done
         }
       }
-      if (c + DEPTH < 4) load_b(at.xb, c + DEPTH);
+      if (c + DEPTH < 4) load_b(at, c + DEPTH);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -496,11 +494,19 @@ __device__ __forceinline__ void store_span(float (&v)[PER], uint32_t at, uint32_
   if (lane == 0) sts32f(sc, __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23));
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+// The weights pass through L2 once: marked to leave it first, they do not push
+// out what is needed again soon (activations, h, o, the kernels' own code).
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar,
+                                            uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+      "%3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -555,7 +561,7 @@ struct Walk {
 };
 
 template <int WT, int PHASE>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Params p) {
   using C = Cfg<WT, PHASE>;
   constexpr int PER = C::PER;
   extern __shared__ uint8_t smem_raw[];
@@ -594,10 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   if (R <= 32) {
     if (warp == 1) build_chunks_warp(p, ctl);
   } else {
-    for (int i = threadIdx.x; i < R; i += kThreads) ctl->order[i] = static_cast<uint16_t>(local_expert(p, i));
-    for (int i = threadIdx.x; i < p.El; i += kThreads) ctl->num[i] = 0;
-    __syncthreads();
-    if (warp == 1) build_chunks(p, ctl);
+    build_chunks(p, ctl, reinterpret_cast<uint32_t*>(bp));
+    // the ring is written by asynchronous copies next
+    fence_proxy_async_smem();
   }
   if (warp == 1) {
     __syncwarp();
@@ -643,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     // ------------------------- weights by TMA; activations and scales by cp.async
     const int nkb = p.K / 128;  // (used with scale words: K % 128 == 0)
     const int64_t scale_rows = static_cast<int64_t>(PHASE == 1 ? 2 * p.N : p.N);
+    const uint64_t policy = evict_first_policy();
     auto load_weights = [&](uint32_t s, const Step& q) {
       if (lane == 0) {
         const uint32_t fb = smem_u32(&ctl->full[s]);
@@ -652,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         // rows past the tensor's channels or K arrive as zeros
         for (int v = 0; v < boxes; ++v)
           tma_load_3d(base + s * C::STAGE_W + v * kBoxW, &tmW, (q.kst * C::BOXES + v) * 128, q.blk * kPer,
-                      PHASE == 1 ? 2 * e : e, fb);
+                      PHASE == 1 ? 2 * e : e, fb, policy);
       }
     };
     // This lane's sources at a unit's first stage, kept over the unit: its part
@@ -745,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
     __syncwarp();
   } else if (warp <= kConvWarps) {
-    // ---------------------- activations to f16 and MX scale codes to floats, in place
+    // ---------------------- activations to f16 and MX scale codes to bf16, in place
     const int slots = PHASE == 2 ? ctl->cstart[nchunk - 1] + ctl->cnum[nchunk - 1] : 0;
     // h of kernel 1's segments: their sums in ascending order, then SwiGLU
     auto join = [&](int slot, int col, bool ok, float (&v)[PER]) {
@@ -801,19 +807,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         timed_out = true;
         break;
       }
-      if (C::MX) {  // a lane: four rows' words of four codes, as floats
+      if (C::MX) {  // a lane: four rows' words of four codes, as bf16
+        auto pair = [](uint32_t w) {  // the low two codes of w
+          return pack_bf16x2(e8m0_value(w & 0xFFu), e8m0_value((w >> 8) & 0xFFu));
+        };
 #pragma unroll
         for (int v = 0; v < C::BOXES * C::WORDS; ++v) {
           const uint4 u = lds128(raw_words(s, v) + lane * 16);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
           const uint32_t dst = s_ring + s * C::SCALE_BYTES + (v * kRows + lane * 4) * C::SCALE_ROW;
-          __syncwarp();  // the floats go over the words
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            sts128(dst + r * 16, make_uint4(__float_as_uint(e8m0_value(w[r] & 0xFFu)),
-                                            __float_as_uint(e8m0_value((w[r] >> 8) & 0xFFu)),
-                                            __float_as_uint(e8m0_value((w[r] >> 16) & 0xFFu)),
-                                            __float_as_uint(e8m0_value(w[r] >> 24))));
+          __syncwarp();  // the bf16 go over the words
+          sts128(dst, make_uint4(pair(u.x), pair(u.x >> 16), pair(u.y), pair(u.y >> 16)));
+          sts128(dst + 16, make_uint4(pair(u.z), pair(u.z >> 16), pair(u.w), pair(u.w >> 16)));
         }
       }
       const int n = ctl->cnum[q.ch];
@@ -897,13 +901,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           *abort_flag = 1;
         }
       };
-      auto box_at = [&](uint32_t st, int v) {
+      auto box_at = [&](uint32_t sg, int v) {
         BoxAt a;
-        a.wt = base + st * C::STAGE_W + v * kBoxW + w_off;
-        a.xb = x_ring + st * x_bytes + v * C::SPAN_BYTES + x_off;
-        a.sA = s_ring + st * C::SCALE_BYTES + (v * C::WORDS * kRows + rowA + g) * C::SCALE_ROW;
+        a.wt = base + sg * C::STAGE_W + v * kBoxW + w_off;
+        a.xb = x_ring + sg * x_bytes + v * C::SPAN_BYTES + x_off;
+        a.sA = s_ring + sg * C::SCALE_BYTES + (v * C::WORDS * kRows + rowA + g) * C::SCALE_ROW;
         a.sB = a.sA + (rowB - rowA) * C::SCALE_ROW;
-        a.xs = v_ring + st * v_bytes + v * cap * 4 + t4 * 8;
+        a.xs = v_ring + sg * v_bytes + v * cap * 4 + t4 * 8;
         return a;
       };
       // box j of the unit: its loads, and what follows when its products are done
