@@ -67,18 +67,35 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _s():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # (the raw handle: building a torch.cuda.Stream object takes longer than a launch)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _arg(what: str, t: Optional[torch.Tensor], dtype, shape) -> Optional[torch.Tensor]:
-    """`t`, checked against the type and shape that the call `what` takes (None in `shape`: any size)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise MoEError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise MoEError(f"{what}: a tensor on {t.device}, but the current device is {torch.cuda.current_device()}")
+def _arg(what: str, t, dtype, ndim: int):
+    """`t`, checked to be a tensor of this type and number of dimensions (its
+    shape is then read off it)."""
+    if t.dtype is not dtype or t.dim() != ndim:
+        raise MoEError(f"{what}: expected {dtype} of {ndim} dimensions, got {t.dtype} {list(t.shape)}")
     return t
+
+
+def _ptr(what: str, t: torch.Tensor, dtype, shape: tuple, dev: int) -> int:
+    """The address of `t`, checked against the type, shape and device that the call `what` takes."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise MoEError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev:
+        raise MoEError(f"{what}: expected a tensor on the current CUDA device {dev}, got one on {t.device}")
+    if not t.is_contiguous():
+        raise MoEError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _dev(what: str, t: torch.Tensor) -> int:
+    """The device of `t`, which has to be the current CUDA device (its stream is the one launched on)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise MoEError(f"{what}: expected a tensor on the current CUDA device, got one on {t.device}")
+    return dev
 
 
 def _nb(cols: int) -> int:
@@ -284,64 +301,71 @@ def swiglu_quant_mx(a: torch.Tensor, h_q=None, h_sf=None):
 
 def quantize_rows_mx4(x: torch.Tensor, q=None, sf=None):
     """MXFP4: bf16 [rows, cols] -> (packed e2m1 codes uint8 [rows, cols/2], E8M0 codes uint8 [cols/128, rows, 4])."""
-    rows, cols = _arg("quantize_rows_mx4", x, torch.bfloat16, (None, None)).shape
+    rows, cols = _arg("quantize_rows_mx4", x, torch.bfloat16, 2).shape
+    dev = _dev("quantize_rows_mx4", x)
+    px = _ptr("quantize_rows_mx4", x, torch.bfloat16, (rows, cols), dev)
     q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device) if q is None else q
     sf = _scale_buf(MX4, rows, cols, x.device, sf)
-    _arg("quantize_rows_mx4 q", q, torch.uint8, (rows, cols // 2))
-    _arg("quantize_rows_mx4 sf", sf, torch.uint8, (cols // 128, rows, 4))
-    if x.numel():
-        check(lib().moe_quantize_rows_mx4(_p(x), rows, cols, _p(q), _p(sf), _s()), "moe_quantize_rows_mx4")
+    pq = _ptr("quantize_rows_mx4 q", q, torch.uint8, (rows, cols // 2), dev)
+    ps = _ptr("quantize_rows_mx4 sf", sf, torch.uint8, (cols // 128, rows, 4), dev)
+    if rows:
+        check(lib().moe_quantize_rows_mx4(px, rows, cols, pq, ps, _s()), "moe_quantize_rows_mx4")
     return q, sf
 
 
 def quantize_weights_mx4(w: torch.Tensor):
     """MXFP4 weights: bf16 [E, N, K] -> (codes [E, N, K/2], E8M0 codes [K/128, E*N, 4])."""
-    E, N, K = _arg("quantize_weights_mx4", w, torch.bfloat16, (None, None, None)).shape
-    q, sf = quantize_rows_mx4(w.reshape(E * N, K))
+    E, N, K = _arg("quantize_weights_mx4", w, torch.bfloat16, 3).shape
+    if not w.is_contiguous():
+        raise MoEError("quantize_weights_mx4: expected a contiguous tensor")
+    q, sf = quantize_rows_mx4(w.view(E * N, K))
     return q.view(E, N, K // 2), sf
 
 
 def dequantize_rows_mx4(q: torch.Tensor, sf: torch.Tensor, out=None) -> torch.Tensor:
     """MXFP4 codes [rows, cols/2] and scale codes [cols/128, rows, 4] -> their bf16 values [rows, cols]."""
-    rows, half = _arg("dequantize_rows_mx4", q, torch.uint8, (None, None)).shape
-    cols = 2 * half
-    _arg("dequantize_rows_mx4 sf", sf, torch.uint8, (cols // 128, rows, 4))
+    rows, half = _arg("dequantize_rows_mx4", q, torch.uint8, 2).shape
+    cols, dev = 2 * half, _dev("dequantize_rows_mx4", q)
+    pq = _ptr("dequantize_rows_mx4", q, torch.uint8, (rows, half), dev)
+    ps = _ptr("dequantize_rows_mx4 sf", sf, torch.uint8, (cols // 128, rows, 4), dev)
     out = torch.empty(rows, cols, dtype=torch.bfloat16, device=q.device) if out is None else out
-    _arg("dequantize_rows_mx4 out", out, torch.bfloat16, (rows, cols))
-    if q.numel():
-        check(lib().moe_dequantize_rows_mx4(_p(q), _p(sf), rows, cols, _p(out), _s()), "moe_dequantize_rows_mx4")
+    po = _ptr("dequantize_rows_mx4 out", out, torch.bfloat16, (rows, cols), dev)
+    if rows:
+        check(lib().moe_dequantize_rows_mx4(pq, ps, rows, cols, po, _s()), "moe_dequantize_rows_mx4")
     return out
 
 
 def quantize_sort_mx4(x: torch.Tensor, topk_ids: torch.Tensor, E: int, out: Optional[dict] = None):
     """MXFP4 steps 1 + 2: the dict of quantize_sort with xs_q = packed codes [T*k, D/2] and
     xs_scale = E8M0 codes [D/128, T*k, 4]."""
-    T, k = _arg("quantize_sort_mx4 topk_ids", topk_ids, torch.int32, (None, None)).shape
-    D = _arg("quantize_sort_mx4 x", x, torch.bfloat16, (T, None)).shape[1]
-    R = T * k
-    dev = x.device
+    T, k = _arg("quantize_sort_mx4 topk_ids", topk_ids, torch.int32, 2).shape
+    D = _arg("quantize_sort_mx4 x", x, torch.bfloat16, 2).shape[1]
+    R, dev, at = T * k, _dev("quantize_sort_mx4", x), x.device
+    px = _ptr("quantize_sort_mx4 x", x, torch.bfloat16, (T, D), dev)
+    pi = _ptr("quantize_sort_mx4 topk_ids", topk_ids, torch.int32, (T, k), dev)
     o = out if out is not None else {}
     if "sorted_src" not in o:
-        o["sorted_src"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["pos"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["group_sizes"] = torch.empty(E, dtype=torch.int32, device=dev)
-        o["group_offsets"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        o["xs_q"] = torch.empty(R, D // 2, dtype=torch.uint8, device=dev)
-        o["xs_scale"] = _scale_buf(MX4, R, D, dev)
-    for key, n in (("sorted_src", R), ("pos", R), ("group_sizes", E), ("group_offsets", E + 1)):
-        _arg(f"quantize_sort_mx4 {key}", o[key], torch.int32, (n,))
-    _arg("quantize_sort_mx4 xs_q", o["xs_q"], torch.uint8, (R, D // 2))
-    _arg("quantize_sort_mx4 xs_scale", o["xs_scale"], torch.uint8, (D // 128, R, 4))
+        o["sorted_src"] = torch.empty(R, dtype=torch.int32, device=at)
+        o["pos"] = torch.empty(R, dtype=torch.int32, device=at)
+        o["group_sizes"] = torch.empty(E, dtype=torch.int32, device=at)
+        o["group_offsets"] = torch.empty(E + 1, dtype=torch.int32, device=at)
+        o["xs_q"] = torch.empty(R, D // 2, dtype=torch.uint8, device=at)
+        o["xs_scale"] = _scale_buf(MX4, R, D, at)
+    p = [_ptr(f"quantize_sort_mx4 {key}", o[key], torch.int32, (n,), dev)
+         for key, n in (("sorted_src", R), ("pos", R), ("group_sizes", E), ("group_offsets", E + 1))]
+    pq = _ptr("quantize_sort_mx4 xs_q", o["xs_q"], torch.uint8, (R, D // 2), dev)
+    ps = _ptr("quantize_sort_mx4 xs_scale", o["xs_scale"], torch.uint8, (D // 128, R, 4), dev)
     if not R:
         o["group_sizes"].zero_()
         o["group_offsets"].zero_()
         return o
-    nws = lib().moe_ragged_sort_workspace_bytes(T, k, E)
-    if "sort_ws" not in o or o["sort_ws"].numel() < nws:
-        o["sort_ws"] = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
-    check(lib().moe_quantize_sort_mx4(_p(x), _p(topk_ids), T, k, E, D, _p(o["sorted_src"]), _p(o["pos"]),
-                                      _p(o["group_sizes"]), _p(o["group_offsets"]), _p(o["xs_q"]), _p(o["xs_scale"]),
-                                      _p(o["sort_ws"]), o["sort_ws"].numel(), _s()), "moe_quantize_sort_mx4")
+    L = lib()
+    nws = L.moe_ragged_sort_workspace_bytes(T, k, E)
+    ws = o.get("sort_ws")
+    if ws is None or ws.numel() < nws:
+        ws = o["sort_ws"] = torch.empty(max(nws, 16), dtype=torch.uint8, device=at)
+    check(L.moe_quantize_sort_mx4(px, pi, T, k, E, D, *p, pq, ps, ws.data_ptr(), ws.numel(), _s()),
+          "moe_quantize_sort_mx4")
     return o
 
 
@@ -349,33 +373,35 @@ def gmm_mx4(lhs_q, lhs_sf, rhs_q, rhs_sf, group_sizes, group_offset: int = 0, E_
             out=None):
     """MXFP4 grouped matmul of packed codes lhs_q [M, K/2] and rhs_q [E_local, N, K/2] -> bf16 [M, N];
     lhs_sf [K/128, M, 4], rhs_sf [K/128, E_local*N, 4]."""
-    M, half = _arg("gmm_mx4 lhs_q", lhs_q, torch.uint8, (None, None)).shape
-    El, N, _ = _arg("gmm_mx4 rhs_q", rhs_q, torch.uint8, (None, None, half)).shape
-    K = 2 * half
-    E = _arg("gmm_mx4 group_sizes", group_sizes, torch.int32, (None,)).numel()
-    E_local = El if E_local is None else E_local
-    if E_local != El:
+    M, half = _arg("gmm_mx4 lhs_q", lhs_q, torch.uint8, 2).shape
+    El, N, _ = _arg("gmm_mx4 rhs_q", rhs_q, torch.uint8, 3).shape
+    E = _arg("gmm_mx4 group_sizes", group_sizes, torch.int32, 1).shape[0]
+    K, dev = 2 * half, _dev("gmm_mx4", lhs_q)
+    if E_local is not None and E_local != El:
         raise MoEError(f"gmm_mx4: E_local is {E_local}, but rhs_q holds {El} experts")
-    _arg("gmm_mx4 lhs_sf", lhs_sf, torch.uint8, (K // 128, M, 4))
-    _arg("gmm_mx4 rhs_sf", rhs_sf, torch.uint8, (K // 128, El * N, 4))
+    pl = _ptr("gmm_mx4 lhs_q", lhs_q, torch.uint8, (M, half), dev)
+    pls = _ptr("gmm_mx4 lhs_sf", lhs_sf, torch.uint8, (K // 128, M, 4), dev)
+    pr = _ptr("gmm_mx4 rhs_q", rhs_q, torch.uint8, (El, N, half), dev)
+    prs = _ptr("gmm_mx4 rhs_sf", rhs_sf, torch.uint8, (K // 128, El * N, 4), dev)
+    pg = _ptr("gmm_mx4 group_sizes", group_sizes, torch.int32, (E,), dev)
     out = torch.empty(M, N, dtype=torch.bfloat16, device=lhs_q.device) if out is None else out
-    _arg("gmm_mx4 out", out, torch.bfloat16, (M, N))
+    po = _ptr("gmm_mx4 out", out, torch.bfloat16, (M, N), dev)
     if M:
-        check(lib().gmm_fp4_mx(_p(lhs_q), _p(lhs_sf), _p(rhs_q), _p(rhs_sf), _p(group_sizes), E, group_offset,
-                               E_local, M, K, N, _p(out), _s()), "gmm_fp4_mx")
+        check(lib().gmm_fp4_mx(pl, pls, pr, prs, pg, E, group_offset, El, M, K, N, po, _s()), "gmm_fp4_mx")
     return out
 
 
 def swiglu_quant_mx4(a: torch.Tensor, h_q=None, h_sf=None):
     """MXFP4 step 4: a = [a0 | a1] bf16 [R, 2F] -> (h codes [R, F/2], h E8M0 codes [F/128, R, 4])."""
-    R, F2 = _arg("swiglu_quant_mx4", a, torch.bfloat16, (None, None)).shape
-    F = F2 // 2
+    R, F2 = _arg("swiglu_quant_mx4", a, torch.bfloat16, 2).shape
+    F, dev = F2 // 2, _dev("swiglu_quant_mx4", a)
+    pa = _ptr("swiglu_quant_mx4", a, torch.bfloat16, (R, 2 * F), dev)
     h_q = torch.empty(R, F // 2, dtype=torch.uint8, device=a.device) if h_q is None else h_q
     h_sf = _scale_buf(MX4, R, F, a.device, h_sf)
-    _arg("swiglu_quant_mx4 h_q", h_q, torch.uint8, (R, F // 2))
-    _arg("swiglu_quant_mx4 h_sf", h_sf, torch.uint8, (F // 128, R, 4))
-    if a.numel():
-        check(lib().moe_swiglu_quant_mx4(_p(a), R, F, _p(h_q), _p(h_sf), _s()), "moe_swiglu_quant_mx4")
+    pq = _ptr("swiglu_quant_mx4 h_q", h_q, torch.uint8, (R, F // 2), dev)
+    ps = _ptr("swiglu_quant_mx4 h_sf", h_sf, torch.uint8, (F // 128, R, 4), dev)
+    if R:
+        check(lib().moe_swiglu_quant_mx4(pa, R, F, pq, ps, _s()), "moe_swiglu_quant_mx4")
     return h_q, h_sf
 
 
@@ -804,6 +830,7 @@ class DecodeBuffers:
             raise MoEError(f"ffn_decode does not take T = {T}, k = {k}, D = {D}, F = {F}")
         self.y = torch.empty(T, D, dtype=torch.bfloat16, device=device)
         self.ws = torch.empty(n, dtype=torch.uint8, device=device)
+        self.ws_bytes = n
 
 
 def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.Tensor], W: ExpertWeights,
@@ -817,38 +844,48 @@ def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.T
     + W.w_in.shape[0]) of E; the others add nothing.  With `buf` (made for T
     tokens or more) the result is a part of buf.y and nothing is allocated; calls
     that may overlap on the GPU need buffers of their own."""
-    T, k = _arg("ffn_decode topk_ids", topk_ids, torch.int32, (None, None)).shape
-    D = _arg("ffn_decode x", x, torch.bfloat16, (T, None)).shape[1]
-    _arg("ffn_decode topk_w", topk_w, torch.float32, (T, k))
+    T, k = _arg("ffn_decode topk_ids", topk_ids, torch.int32, 2).shape
+    D = _arg("ffn_decode x", x, torch.bfloat16, 2).shape[1]
     El, F2 = W.w_in.shape[:2]
     F = F2 // 2
     E = group_offset + El if E is None else E
-    kind = {MX32: 2, MX4: 3}.get(W.in_mode, 1 if W.w_in.dtype == torch.int8 else 0)
-    if (W.out_mode in (MX32, MX4) or kind > 1) and W.out_mode != W.in_mode:
-        raise MoEError("ffn_decode: w_in and w_out hold different weight types")
-    code = torch.int8 if kind == 1 else torch.uint8
-    half = 2 if kind == 3 else 1
-    _arg("ffn_decode w_in", W.w_in, code, (El, 2 * F, D // half))
-    _arg("ffn_decode w_out", W.w_out, code, (El, D, F // half))
-    for what, s, mode, N, K in (("s_in", W.s_in, W.in_mode, 2 * F, D), ("s_out", W.s_out, W.out_mode, D, F)):
-        if kind > 1:
-            _arg(f"ffn_decode {what}", s, torch.uint8, (K // 128, El * N, 4))
-        elif mode in (PER_ROW, PER_ROW_BLOCK128, PER_TENSOR):
-            shape = {PER_ROW: (El, N), PER_ROW_BLOCK128: (El, _nb(K), N), PER_TENSOR: (1,)}[mode]
-            _arg(f"ffn_decode {what}", s, torch.float32, shape)
-        else:
-            raise MoEError(f"ffn_decode: scale mode {mode} of {what}")
+    in_mode, out_mode, dev = W.in_mode, W.out_mode, _dev("ffn_decode", x)
+    if in_mode in (MX32, MX4) or out_mode in (MX32, MX4):
+        kind, code, half = 2 + (in_mode == MX4), torch.uint8, 1 + (in_mode == MX4)
+        if in_mode != out_mode:
+            raise MoEError("ffn_decode: w_in and w_out hold different weight types")
+        s_type, s_in, s_out, m_in, m_out = torch.uint8, (D // 128, El * 2 * F, 4), (F // 128, El * D, 4), 0, 0
+    else:
+        kind, code, half = (1, torch.int8, 1) if W.w_in.dtype is torch.int8 else (0, torch.uint8, 1)
+        s_type, s_in, s_out = torch.float32, _decode_scale(in_mode, El, 2 * F, D), _decode_scale(out_mode, El, D, F)
+        m_in, m_out = in_mode, out_mode
+    px = _ptr("ffn_decode x", x, torch.bfloat16, (T, D), dev)
+    pi = _ptr("ffn_decode topk_ids", topk_ids, torch.int32, (T, k), dev)
+    pw = None if topk_w is None else _ptr("ffn_decode topk_w", topk_w, torch.float32, (T, k), dev)
+    p_in = _ptr("ffn_decode w_in", W.w_in, code, (El, 2 * F, D // half), dev)
+    p_out = _ptr("ffn_decode w_out", W.w_out, code, (El, D, F // half), dev)
+    ps_in = _ptr("ffn_decode s_in", W.s_in, s_type, s_in, dev)
+    ps_out = _ptr("ffn_decode s_out", W.s_out, s_type, s_out, dev)
     if buf is None:
         buf = DecodeBuffers(max(T, 1), D, E, k, F, x.device)
-    elif buf.T < T or buf.k != k or buf.D != D or buf.F != F:
-        raise MoEError("ffn_decode: the buffers were made for another shape")
-    y = buf.y[:T]
+    elif buf.T < T or buf.k != k or buf.D != D or buf.F != F or buf.y.get_device() != dev:
+        raise MoEError("ffn_decode: the buffers were made for another shape or device")
+    y = buf.y if T == buf.T else buf.y[:T]
     if T:
-        check(lib().moe_ffn_decode(_p(x), _p(topk_ids), _p(topk_w), T, k, E, group_offset, El, D, F, kind, _p(W.w_in),
-                                   _p(W.s_in), 0 if kind > 1 else W.in_mode, _p(W.w_out), _p(W.s_out),
-                                   0 if kind > 1 else W.out_mode, _p(y), _p(buf.ws), buf.ws.numel(), _s()),
-              "moe_ffn_decode")
+        check(lib().moe_ffn_decode(px, pi, pw, T, k, E, group_offset, El, D, F, kind, p_in, ps_in, m_in, p_out, ps_out,
+                                   m_out, y.data_ptr(), buf.ws.data_ptr(), buf.ws_bytes, _s()), "moe_ffn_decode")
     return y
+
+
+def _decode_scale(mode: int, El: int, N: int, K: int) -> tuple:
+    """Shape of the fp32 scales of weights [El, N, K]."""
+    if mode == PER_ROW:
+        return (El, N)
+    if mode == PER_ROW_BLOCK128:
+        return (El, _nb(K), N)
+    if mode == PER_TENSOR:
+        return (1,)
+    raise MoEError(f"ffn_decode: scale mode {mode}")
 
 
 def ffn_backward(dY: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, buf: FFNBuffers,
