@@ -157,6 +157,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum: c = a b.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -407,22 +415,24 @@ struct Box {
     for (int n = 0; n < NT; ++n) xv[n] = lds64(at.xs + n * 32);
   }
   __device__ __forceinline__ void contract(float (&acc)[NT][4], const BoxAt& at) {
-    // two chains of sums (MX: the sum of the scaled 32-wide blocks, and the block at hand)
-    float s0[NT][4], s1[NT][4];
+    // Without block scales, two chains of sums, s0 and blk[0].  MX: s0 sums the
+    // scaled 32-wide blocks; a block is scaled into it one block late, while the
+    // next one's products run.
+    float s0[NT][4], blk[2][NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s0[n][i] = s1[n][i] = 0.0f;
-    auto fold = [&](float fa, float fb) {
+      for (int i = 0; i < 4; ++i) s0[n][i] = 0.0f;
+    auto fold = [&](int k, float fa, float fb) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        s0[n][0] = __fmaf_rn(s1[n][0], fa, s0[n][0]);
-        s0[n][1] = __fmaf_rn(s1[n][1], fa, s0[n][1]);
-        s0[n][2] = __fmaf_rn(s1[n][2], fb, s0[n][2]);
-        s0[n][3] = __fmaf_rn(s1[n][3], fb, s0[n][3]);
-        s1[n][0] = s1[n][1] = s1[n][2] = s1[n][3] = 0.0f;
+        s0[n][0] = __fmaf_rn(blk[k][n][0], fa, s0[n][0]);
+        s0[n][1] = __fmaf_rn(blk[k][n][1], fa, s0[n][1]);
+        s0[n][2] = __fmaf_rn(blk[k][n][2], fb, s0[n][2]);
+        s0[n][3] = __fmaf_rn(blk[k][n][3], fb, s0[n][3]);
       }
     };
+    float pa = 0.0f, pb = 0.0f;  // the scales of the block before
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (WT == kMx4 && c == 2) load_f(at, 1);
@@ -435,22 +445,46 @@ struct Box {
           const uint32_t a0[4] = {va[0], vb[0], va[1], vb[1]}, a1[4] = {va[2], vb[2], va[3], vb[3]};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_f16(s1[n], a0, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
-            mma_f16(s1[n], a1, b[c % DEPTH][cc][n][BW - 2], b[c % DEPTH][cc][n][BW - 1]);
+            mma_f16_first(blk[cc][n], a0, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
+            mma_f16(blk[cc][n], a1, b[c % DEPTH][cc][n][BW - 2], b[c % DEPTH][cc][n][BW - 1]);
           }
-          fold(fA[(2 * c + cc) & 3], fB[(2 * c + cc) & 3]);
+          if (c > 0 || cc > 0) fold(cc ^ 1, pa, pb);
+          pa = fA[(2 * c + cc) & 3];
+          pb = fB[(2 * c + cc) & 3];
         } else {
           uint32_t a[4];
           weights4<WT>(r[c][2 * cc], a[0], a[2]);
           weights4<WT>(r[c][2 * cc + 1], a[1], a[3]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma_f16(C::MX || cc == 1 ? s1[n] : s0[n], a, b[c % DEPTH][cc][n][0], b[c % DEPTH][cc][n][1]);
-          if (C::MX && cc == 1) fold(fA[c], fB[c]);  // a 32-wide block is done
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t b0 = b[c % DEPTH][cc][n][0], b1 = b[c % DEPTH][cc][n][1];
+            if (C::MX) {
+              if (cc == 0)
+                mma_f16_first(blk[c & 1][n], a, b0, b1);
+              else
+                mma_f16(blk[c & 1][n], a, b0, b1);
+            } else if (cc == 0) {
+              if (c == 0)
+                mma_f16_first(s0[n], a, b0, b1);
+              else
+                mma_f16(s0[n], a, b0, b1);
+            } else {
+              if (c == 0)
+                mma_f16_first(blk[0][n], a, b0, b1);
+              else
+                mma_f16(blk[0][n], a, b0, b1);
+            }
+          }
+          if (C::MX && cc == 1) {
+            if (c > 0) fold((c & 1) ^ 1, pa, pb);
+            pa = fA[c];
+            pb = fB[c];
+          }
         }
       }
       if (c + DEPTH < 4) load_b(at, c + DEPTH);
     }
+    if (C::MX) fold(1, pa, pb);  // the last block
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float x0 = __uint_as_float(xv[n].x), x1 = __uint_as_float(xv[n].y);
@@ -460,10 +494,10 @@ struct Box {
         acc[n][2] = __fmaf_rn(s0[n][2], x0, acc[n][2]);
         acc[n][3] = __fmaf_rn(s0[n][3], x1, acc[n][3]);
       } else {
-        acc[n][0] = __fmaf_rn(s0[n][0] + s1[n][0], x0 * fA[0], acc[n][0]);
-        acc[n][1] = __fmaf_rn(s0[n][1] + s1[n][1], x1 * fA[0], acc[n][1]);
-        acc[n][2] = __fmaf_rn(s0[n][2] + s1[n][2], x0 * fB[0], acc[n][2]);
-        acc[n][3] = __fmaf_rn(s0[n][3] + s1[n][3], x1 * fB[0], acc[n][3]);
+        acc[n][0] = __fmaf_rn(s0[n][0] + blk[0][n][0], x0 * fA[0], acc[n][0]);
+        acc[n][1] = __fmaf_rn(s0[n][1] + blk[0][n][1], x1 * fA[0], acc[n][1]);
+        acc[n][2] = __fmaf_rn(s0[n][2] + blk[0][n][2], x0 * fB[0], acc[n][2]);
+        acc[n][3] = __fmaf_rn(s0[n][3] + blk[0][n][3], x1 * fB[0], acc[n][3]);
       }
     }
   }
