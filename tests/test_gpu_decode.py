@@ -112,3 +112,210 @@ def test_sizes_that_fill_no_tile(kind, T, D, F):
     rng, x, ids, w = case(T + D, T, 2, 3, D)
     W = make_weights(kind, 3, D, F, rng)
     check(moe.ffn_decode(x, dev(ids), dev(w), W), x, ids, w, W)
+
+
+@pytest.mark.parametrize("kind", ["e4m3-block", "int8-channel", "mx4"])
+@pytest.mark.parametrize("T,k,E", [(8, 4, 2), (64, 4, 3), (20, 32, 40), (40, 3, 200), (64, 16, 9)])
+def test_routing_that_repeats_crowds_and_scatters(kind, T, k, E):
+    """The same expert twice for a token, every pair on one expert (several
+    chunks of it), more than 32 pairs and more than 32 chunks."""
+    rng = np.random.default_rng(T * k + E)
+    D, F = 128, 256
+    x = dev(bf16(rng.standard_normal((T, D)).astype(np.float32)))
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    if E == 3:
+        ids[:] = 1
+    w = rng.random((T, k)).astype(np.float32)
+    W = make_weights(kind, E, D, F, rng)
+    check(moe.ffn_decode(x, dev(ids), dev(w), W), x, ids, w, W)
+
+
+@pytest.mark.parametrize("kind", ["e4m3-channel", "mx8", "mx4"])
+@pytest.mark.parametrize("T,k,D,F", [(1, 1, 4096, 128), (2, 1, 128, 4096), (1, 3, 2048, 2176), (17, 2, 640, 1408)])
+def test_long_contractions(kind, T, k, D, F):
+    """K in several segments (one or a few pairs), an odd number of boxes, the
+    ring going round."""
+    rng, x, ids, w = case(D + F, T, k, 4, D)
+    W = make_weights(kind, 4, D, F, rng)
+    check(moe.ffn_decode(x, dev(ids), dev(w), W), x, ids, w, W)
+
+
+def test_without_weights_of_the_choices():
+    rng, x, ids, w = case(3, 5, 2, 4, 256)
+    W = make_weights("e4m3-block", 4, 256, 128, rng)
+    check(moe.ffn_decode(x, dev(ids), None, W), x, ids, None, W)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("kind", ["e4m3-block", "mx4"])
+def test_shards(kind, T):
+    """Experts of other shards add nothing; a token with none of its experts here
+    gets zeros; the sum over the shards is the whole."""
+    rng, x, ids, w = case(T, T, 2, 6, 256)
+    ids[0] = [4, 5]
+    W = make_weights(kind, 6, 256, 128, rng)
+    wi, wo = values(W.w_in, W.s_in, W.in_mode), values(W.w_out, W.s_out, W.out_mode)
+    for g0, El in ((0, 2), (2, 3), (0, 1)):
+        part = lambda t, n: t[n * g0:n * (g0 + El)].contiguous()  # noqa: E731
+        if kind == "mx4":
+            sl = lambda s, n: s[:, n * g0:n * (g0 + El)].contiguous()  # noqa: E731
+            Ws = moe.ExpertWeights(part(W.w_in, 1), sl(W.s_in, 256), W.in_mode, part(W.w_out, 1), sl(W.s_out, 256), W.out_mode)
+        else:
+            Ws = moe.ExpertWeights(part(W.w_in, 1), part(W.s_in, 1), W.in_mode, part(W.w_out, 1), part(W.s_out, 1), W.out_mode)
+        y = moe.ffn_decode(x, dev(ids), dev(w), Ws, E=6, group_offset=g0)
+        check(y, x, ids, w, Ws, g0)
+        if g0 + El <= 4:
+            assert (y[0] == 0).all()
+    assert wi.shape[0] == wo.shape[0] == 6
+
+
+def test_no_expert_here_at_all():
+    rng, x, _, w = case(4, 7, 2, 2, 128)
+    W = make_weights("int8-channel", 2, 128, 256, rng)
+    buf = moe.DecodeBuffers(7, 128, 9, 2, 256, "cuda")
+    buf.y.fill_(3.0)
+    y = moe.ffn_decode(x, dev(np.full((7, 2), 8, np.int32)), dev(w), W, buf, E=9, group_offset=3)
+    assert (y == 0).all() and moe.device_error() == 0
+
+
+def test_bad_ids_add_nothing_and_are_reported():
+    rng, x, ids, w = case(5, 9, 3, 4, 128)
+    W = make_weights("e4m3-channel", 4, 128, 128, rng)
+    bad = ids.copy()
+    bad[0, 1], bad[4, 0], bad[8, 2] = -1, 4, 2147483647
+    y = moe.ffn_decode(x, dev(bad), dev(w), W)
+    assert moe.device_error() == 0x1
+    check(y, x, bad, w, W)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_infinities_and_nan_stay_in_their_token(kind):
+    rng, x, ids, w = case(6, 11, 2, 3, 256)
+    W = make_weights(kind, 3, 256, 128, rng)
+    clean = moe.ffn_decode(x, dev(ids), dev(w), W).clone()
+    x2 = x.clone()
+    x2[3, 17], x2[7, 200] = float("nan"), float("inf")
+    y = moe.ffn_decode(x2, dev(ids), dev(w), W)
+    assert not torch.isfinite(y[3]).any() and not torch.isfinite(y[7]).any()
+    keep = [t for t in range(11) if t not in (3, 7)]
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("kind", ["mx8", "mx4", "e4m3-channel"])
+def test_nan_weights_reach_the_outputs_they_feed(kind):
+    rng, x, ids, w = case(7, 5, 1, 3, 256)
+    ids[:] = [[0], [1], [2], [1], [0]]
+    W = make_weights(kind, 3, 256, 128, rng)
+    clean = moe.ffn_decode(x, dev(ids), dev(w), W).clone()
+    if kind == "e4m3-channel":
+        W.w_out[1, 9, 100] = 0x7F
+    else:
+        W.s_out[0, 256 + 9, 3] = 255  # expert 1, channel 9, values 96..127
+    y = moe.ffn_decode(x, dev(ids), dev(w), W)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[1, 9] = bad[3, 9] = True
+    assert y[bad].isnan().all() and torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -45, 2.0 ** 60])
+@pytest.mark.parametrize("kind", ["e4m3-block", "mx4"])
+def test_far_magnitudes(kind, scale):
+    """Rows far outside f16's range, beside ordinary ones, and spans of one row
+    2^20 apart: the span scales carry them."""
+    rng, x, ids, w = case(8, 6, 2, 3, 512)
+    x[1] *= scale
+    x[4, 128:256] *= 2.0 ** -20
+    W = make_weights(kind, 3, 512, 128, rng)
+    check(moe.ffn_decode(x, dev(ids), dev(w), W), x, ids, w, W)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_repeats_bit_for_bit(kind):
+    rng, x, ids, w = case(9, 33, 4, 8, 512)
+    W = make_weights(kind, 8, 512, 256, rng)
+    ids_d, w_d = dev(ids), dev(w)
+    first = moe.ffn_decode(x, ids_d, w_d, W)
+    buf = moe.DecodeBuffers(64, 512, 8, 4, 256, "cuda")
+    for _ in range(20):
+        assert torch.equal(moe.ffn_decode(x, ids_d, w_d, W, buf), first)
+
+
+def test_the_batch_around_a_token_does_not_change_it():
+    """A token alone and in a batch: the same sums up to the K segments that few
+    pairs are split into, so within both bounds of the oracle."""
+    rng, x, ids, w = case(10, 40, 2, 4, 256)
+    W = make_weights("e4m3-block", 4, 256, 256, rng)
+    for t in (0, 39):
+        check(moe.ffn_decode(x[t:t + 1].contiguous(), dev(ids[t:t + 1]), dev(w[t:t + 1]), W), x[t:t + 1], ids[t:t + 1],
+              w[t:t + 1], W)
+
+
+def test_empty_and_shorter_batches():
+    rng, x, ids, w = case(11, 16, 2, 4, 256)
+    W = make_weights("mx8", 4, 256, 128, rng)
+    buf = moe.DecodeBuffers(16, 256, 4, 2, 128, "cuda")
+    assert moe.ffn_decode(x[:0], dev(ids[:0]), dev(w[:0]), W, buf).shape == (0, 256)
+    moe.ffn_decode(x, dev(ids), dev(w), W, buf)
+    rest = buf.y[5:].clone()
+    y = moe.ffn_decode(x[:5], dev(ids[:5]), dev(w[:5]), W, buf)
+    check(y, x[:5], ids[:5], w[:5], W)
+    assert torch.equal(buf.y[5:], rest)  # rows behind the batch stay as they were
+
+
+def test_captured_and_replayed():
+    """Two graphs on the same buffers, replayed in turn with new inputs."""
+    rng, x, ids, w = case(12, 6, 2, 4, 256)
+    W = make_weights("e4m3-block", 4, 256, 128, rng)
+    W4 = make_weights("mx4", 4, 256, 128, rng)
+    buf = moe.DecodeBuffers(6, 256, 4, 2, 128, "cuda")
+    xd, idd, wd = x.clone(), dev(ids), dev(w)
+    graphs = []
+    for weights in (W, W4):
+        moe.ffn_decode(xd, idd, wd, weights, buf)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.ffn_decode(xd, idd, wd, weights, buf)
+        graphs.append((g, weights))
+    for seed in (20, 21, 22):
+        _, x2, ids2, w2 = case(seed, 6, 2, 4, 256)
+        xd.copy_(x2), idd.copy_(dev(ids2)), wd.copy_(dev(w2))
+        for g, weights in graphs:
+            g.replay()
+            check(buf.y.clone(), x2, ids2, w2, weights)
+
+
+def test_on_two_streams_at_once():
+    rng, x, ids, w = case(13, 8, 2, 4, 1024)
+    W = make_weights("e4m3-channel", 4, 1024, 1024, rng)
+    idd, wd = dev(ids), dev(w)
+    want = moe.ffn_decode(x, idd, wd, W).clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    bufs = [moe.DecodeBuffers(8, 1024, 4, 2, 1024, "cuda") for _ in streams]
+    for _ in range(10):
+        for s, b in zip(streams, bufs):
+            with torch.cuda.stream(s):
+                moe.ffn_decode(x, idd, wd, W, b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(b.y, want) for b in bufs) and moe.device_error() == 0
+
+
+def test_a_prompt_and_its_decoding_steps():
+    """As a server uses them: weights quantised once to MXFP4, the prompt through
+    ffn_forward, then steps routed by router_topk through ffn_decode."""
+    rng = np.random.default_rng(14)
+    T, D, E, k, F = 96, 256, 8, 2, 256
+    W = make_weights("mx4", E, D, F, rng)
+    gate = dev(bf16(rng.standard_normal((E, D)).astype(np.float32) * 0.1))
+    x = dev(bf16(rng.standard_normal((T, D)).astype(np.float32)))
+    _, ids, w = moe.router_topk(x, gate, k)
+    prompt = moe.ffn_forward(x, ids, w, W, moe.MX4, moe.FFNBuffers(T, D, E, k, F, moe.MX4, "cuda"))
+    assert torch.isfinite(prompt).all() and moe.device_error() == 0
+    buf = moe.DecodeBuffers(4, D, E, k, F, "cuda")
+    step = x[:4].contiguous()
+    for _ in range(3):
+        _, ids, w = moe.router_topk(step, gate, k)
+        y = moe.ffn_decode(step, ids, w, W, buf)
+        check(y, step, ids.cpu().numpy(), w.cpu().numpy(), W)
+        step = (step + y).contiguous()

@@ -84,3 +84,38 @@ def test_product_binding():
         moe.gmm_mx4(*good, E_local=1)
     with pytest.raises(moe.MoEError):
         moe.gmm_mx4(*good)  # not on the GPU
+
+
+def test_decode(lib):
+    def call(x=P, ids=P, w=P, T=4, k=2, E=8, g0=0, El=8, D=256, F=128, kind=0, wi=P, si=P, mi=0, wo=P, so=P, mo=0, y=P,
+             ws=P, nws=1 << 30):
+        return lib.moe_ffn_decode(x, ids, w, T, k, E, g0, El, D, F, kind, wi, si, mi, wo, so, mo, y, ws, nws, None)
+
+    need = lib.moe_ffn_decode_workspace_bytes(4, 2, 256, 128)
+    assert need >= 4 * 8 * (256 + 128)
+    for bad in (dict(x=None), dict(ids=None), dict(wi=None), dict(si=None), dict(wo=None), dict(so=None), dict(y=None),
+                dict(ws=None), dict(T=-1), dict(T=65), dict(k=0), dict(k=33), dict(T=64, k=17), dict(D=0), dict(D=24),
+                dict(F=24), dict(D=32784), dict(F=32784), dict(E=0), dict(E=1025), dict(g0=-1), dict(g0=1), dict(El=0),
+                dict(El=9), dict(kind=4), dict(kind=-1), dict(mi=3), dict(mi=4), dict(mo=7), dict(nws=need - 1),
+                dict(mi=1, D=144), dict(mo=1, D=144), dict(mi=1, F=144), dict(kind=2, D=144), dict(kind=3, F=144),
+                dict(x=ODD), dict(wi=ODD), dict(wo=ODD), dict(si=ODD), dict(so=ODD), dict(y=ODD), dict(ws=ODD),
+                dict(E=1024, El=1024, F=32768, D=32768, T=1, nws=1 << 40, g0=1)):
+        assert call(**bad) == 1, bad
+    for shape in ((65, 2, 256, 128), (4, 0, 256, 128), (4, 2, 250, 128), (64, 17, 256, 128), (-1, 2, 256, 128)):
+        assert lib.moe_ffn_decode_workspace_bytes(*shape) == 0
+
+
+def test_decode_binding():
+    u8, f32 = (lambda *s: torch.zeros(*s, dtype=torch.uint8)), torch.zeros
+    x, ids, w = torch.zeros(2, 256, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32), f32(2, 2)
+    W = moe.ExpertWeights(u8(4, 256, 256), f32(4, 256), moe.PER_ROW, u8(4, 256, 128), f32(4, 256), moe.PER_ROW)
+    with pytest.raises(moe.MoEError):
+        moe.ffn_decode(x, ids, w, W)  # not on the GPU
+    with pytest.raises(moe.MoEError):
+        moe.ffn_decode(x.float(), ids, w, W)
+    with pytest.raises(moe.MoEError):
+        moe.ffn_decode(x, ids.long(), w, W)
+    with pytest.raises(moe.MoEError):
+        moe.DecodeBuffers(65, 256, 4, 2, 128, "cpu")
+    with pytest.raises(moe.MoEError):
+        moe.DecodeBuffers(4, 250, 4, 2, 128, "cpu")
