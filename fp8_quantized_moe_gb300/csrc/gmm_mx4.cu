@@ -7,13 +7,22 @@
 // One persistent CTA per SM, 128 x 256 tiles:
 //   warp 0      TMA producer: per stage 256 values of K (128 packed bytes a
 //               row, 128-byte swizzle), 128 A rows and 256 B rows: 48 KB,
-//               four stages.
+//               four stages; and B's scale words.
 //   warp 1      MMA issuer: copies the stage's scale atoms into tensor memory
 //               (tcgen05.cp), then four M = 128, N = 256, K = 64 MMAs.
-//   warp 2      scale gatherer: the stage's scale words by 4-byte cp.async into
-//               the 32 x 16-byte atoms that tcgen05.cp copies.
+//   warp 2      gatherer of A's scale words, by 4-byte cp.async, into a ring
+//               of its own that runs further ahead than the stages.
 //   warps 4..11 epilogue: accumulator -> bf16 in registers, accumulator
 //               released, then row segments to memory.
+// The tensor core takes the scales of 128 rows as an atom of 32 x 16 bytes, whose
+// 16 bytes l are the words of rows l, 32 + l, 64 + l and 96 + l.  In memory the
+// words of consecutive rows are adjacent.  B's rows can come in any order, since
+// its rows are output columns: TMA brings channel 4 l + c of each 128 to row 32 c
+// + l of the tile, so that B's scale words are an atom as they lie, one 512-byte
+// bulk copy, and the epilogue undoes the order when it packs columns.  A's rows
+// start anywhere (a group's first row), so its words are gathered.  (With all
+// scale words gathered the stage's 24 copies an element of the warp held the MMAs
+// up: 980 us at 16384 x 28672 x 4096 over 8 groups.)
 // The 256-column accumulator and the scale slots share the 512 columns, so
 // there is one accumulator; the epilogue hands it back as soon as its 128
 // columns a warp sit packed in 64 registers, before any of them is stored.
@@ -39,15 +48,18 @@ constexpr int kRowBytes = 128;       // a stage's bytes of one operand row: 256 
 constexpr int kABytes = kBM * kRowBytes, kBBytes = kBN * kRowBytes;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kAtom = 512;           // scale words of 128 rows and 128 values of K: 32 rows of 16 bytes
-constexpr int kSfBytes = 6 * kAtom;  // a stage: A and two halves of B, each for two 128-wide K blocks
+constexpr int kSfBBytes = 4 * kAtom; // a stage's: two halves of B, each for two 128-wide K blocks
+constexpr int kSfABytes = 2 * kAtom; // a slot of A's ring
+constexpr int kSfSlots = 8;
 constexpr int kSfCols = 24;          // tensor-memory columns of a stage's scales: 4 an atom
 constexpr int kSfCol0 = kBN;
-constexpr int kLag = 2;              // stages of scale copies in flight
+constexpr int kLag = 4;              // stages of A's scale copies in flight
 constexpr int kCtrlWarps = 4, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kCtrlWarps + kEpiWarps);
 constexpr int kMaxGroups = 1024;
 constexpr int kStgPitch = 80, kStgBytes = 8 * kStgPitch;
 static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
+static_assert(kLag < kSfSlots, "the gatherer announces a slot before it needs the last one back");
 
 struct Params {
   const int32_t* group_sizes;
@@ -61,14 +73,14 @@ struct Params {
 };
 
 struct Ctl {
-  uint64_t full[kStages], empty[kStages], sffull[kStages];
+  uint64_t full[kStages], empty[kStages], sffull[kSfSlots], sfempty[kSfSlots];
   uint64_t tfull, tempty, drain;
   uint32_t tmem_base;
   int abort_flag, no_abort, err, total;
-  int start[kMaxGroups + 1], prefix[kMaxGroups + 1], size[kMaxGroups];
+  int start[kMaxGroups + 1], prefix[kMaxGroups + 1];  // local groups' first rows and tiles; the last: their ends
 };
 constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
-constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kStageBytes + kSfBytes) + kCtlBytes +
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kStageBytes + kSfBBytes) + kSfSlots * kSfABytes + kCtlBytes +
                          static_cast<size_t>(kEpiWarps) * kStgBytes;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
@@ -90,7 +102,15 @@ __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
-// Local groups' first rows, sizes and first tiles, by warp 0 (any size
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Local groups' first rows and first tiles, by warp 0 (any size
 // negative or a sum other than M: err).
 __device__ void build_tables(const Params& p, Ctl* c) {
   const int lane = threadIdx.x & 31;
@@ -115,8 +135,8 @@ __device__ void build_tables(const Params& p, Ctl* c) {
       }
     }
     if (mine) {
-      c->size[local] = sz;
       c->start[local] = static_cast<int>(rows + ir - sz);
+      if (local == p.El - 1) c->start[p.El] = static_cast<int>(rows + ir);
       c->prefix[local] = tiles + it - nt;
     }
     rows += __shfl_sync(0xffffffffu, ir, 31);
@@ -142,7 +162,7 @@ __device__ __forceinline__ Tile get_tile(const Params& p, const Ctl* c, int t) {
   }
   Tile tl;
   tl.el = lo;
-  const int sz = c->size[lo], mt = (sz + kBM - 1) / kBM, local = t - c->prefix[lo];
+  const int sz = c->start[lo + 1] - c->start[lo], mt = (sz + kBM - 1) / kBM, local = t - c->prefix[lo];
   const int nt = local / mt, mi = local - nt * mt;
   tl.row0 = c->start[lo] + mi * kBM;
   tl.rows = min(kBM, sz - mi * kBM);
@@ -155,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* bp = smem_raw + (base - raw);
-  const uint32_t sf_ring = base + kStages * kStageBytes;
-  Ctl* ctl = reinterpret_cast<Ctl*>(bp + kStages * (kStageBytes + kSfBytes));
+  const uint32_t sfb_ring = base + kStages * kStageBytes, sfa_ring = sfb_ring + kStages * kSfBBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(bp + kStages * (kStageBytes + kSfBBytes) + kSfSlots * kSfABytes);
   uint8_t* stg_base = reinterpret_cast<uint8_t*>(ctl) + kCtlBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -165,7 +185,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
-      mbar_init(smem_u32(&ctl->sffull[s]), 32);
+    }
+    for (int q = 0; q < kSfSlots; ++q) {
+      mbar_init(smem_u32(&ctl->sffull[q]), 32);
+      mbar_init(smem_u32(&ctl->sfempty[q]), 1);
     }
     mbar_init(smem_u32(&ctl->tfull), 1);
     mbar_init(smem_u32(&ctl->tempty), kEpiWarps);
@@ -198,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
+      const int64_t brows = static_cast<int64_t>(p.El) * p.N;
       for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
         const Tile tl = get_tile(p, ctl, t);
         const int brow = tl.el * p.N + tl.n0;
@@ -208,9 +232,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t fb = smem_u32(&ctl->full[s]), sa = base + s * kStageBytes;
-          mbar_arrive_expect_tx(fb, kStageBytes);
+          const int nh = min(2, p.nkb - 2 * kb);                // 128-wide K blocks of this stage
+          const int words = min(kBN, p.N - tl.n0);              // channels of the tile (a multiple of 16)
+          mbar_arrive_expect_tx(fb, kStageBytes + nh * words * 4);
           tma_load_2d(sa, &tmA, kb * kRowBytes, tl.row0, fb);
-          tma_load_2d(sa + kABytes, &tmB, kb * kRowBytes, brow, fb);
+          tma_load_3d(sa + kABytes, &tmB, kb * kRowBytes, brow / 4, 0, fb);
+          tma_load_3d(sa + kABytes + kBBytes / 2, &tmB, kb * kRowBytes, brow / 4 + 32, 0, fb);
+          // channels past N keep what lay there: their columns are not stored
+          for (int h = 0; h < nh; ++h)
+            bulk_load(sfb_ring + s * kSfBBytes + 2 * kAtom * h, p.rhs_sf + (2 * kb + h) * brows + brow, words * 4, fb);
         }
       }
       if (timed_out) {
@@ -233,27 +263,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         for (int kb = 0; kb < nstep; ++kb, ++it) {
           const int s = it % kStages;
-          const uint32_t ph = (it / kStages) & 1;
+          const uint32_t ph = (it / kStages) & 1, q = it % kSfSlots;
           if (!mbar_wait_bounded(smem_u32(&ctl->full[s]), ph, abort_flag, kWaitLimitNs) ||
-              !mbar_wait_bounded(smem_u32(&ctl->sffull[s]), ph, abort_flag, kWaitLimitNs)) {
+              !mbar_wait_bounded(smem_u32(&ctl->sffull[q]), (it / kSfSlots) & 1, abort_flag, kWaitLimitNs)) {
             timed_out = true;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + s * kStageBytes, sf = sf_ring + s * kSfBytes;
+          const uint32_t sa = base + s * kStageBytes, sfa_sm = sfa_ring + q * kSfABytes, sfb_sm = sfb_ring + s * kSfBBytes;
           const uint32_t sft = tmem + kSfCol0 + s * kSfCols;  // per K block: A's 4 columns, then B's 8
           const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kABytes);
-#pragma unroll
-          for (int a = 0; a < 6; ++a) tmem_cp_32x128b_warpx4(sft + 4 * a, smem_desc_plain(sf + kAtom * a));
           const int nh = min(2, p.nkb - 2 * kb);  // 128-wide K blocks of this stage
           for (int h = 0; h < nh; ++h) {
             const uint32_t sfa = sft + 12 * h, sfb = sfa + 4;
+            tmem_cp_32x128b_warpx4(sfa, smem_desc_plain(sfa_sm + kAtom * h));
+            tmem_cp_32x128b_warpx4(sfb, smem_desc_plain(sfb_sm + 2 * kAtom * h));
+            tmem_cp_32x128b_warpx4(sfb + 4, smem_desc_plain(sfb_sm + 2 * kAtom * h + kAtom));
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              mma_mx4(tmem, da + 4 * h + 2 * q, db + 4 * h + 2 * q, idesc_mx4(kBM, kBN, 2 * q), sfa, sfb,
-                      kb > 0 || h > 0 || q > 0);
+            for (int half = 0; half < 2; ++half)
+              mma_mx4(tmem, da + 4 * h + 2 * half, db + 4 * h + 2 * half, idesc_mx4(kBM, kBN, 2 * half), sfa, sfb,
+                      kb > 0 || h > 0 || half > 0);
           }
           mma_commit(smem_u32(&ctl->empty[s]));
+          mma_commit(smem_u32(&ctl->sfempty[q]));
         }
         if (timed_out) break;
         mma_commit(smem_u32(&ctl->tfull));
@@ -267,51 +299,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    // Lane l copies the words of tile rows 32 c + l.  The words of a tile's
-    // rows for one K block are adjacent, so an instruction reads one 128-byte
-    // line.  A stage is announced kLag stages later, once its copies have
-    // landed and are visible to the tensor core's (async-proxy) reads.
+    // Lane l copies the words of tile rows 32 c + l: the words of a tile's rows
+    // for one K block are adjacent, so an instruction reads one 128-byte line.  A
+    // slot is announced kLag stages later, once its copies have landed and are
+    // visible to the tensor core's (async-proxy) reads.
     uint32_t it = 0;
-    const int64_t brows = static_cast<int64_t>(p.El) * p.N;
     for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
       const Tile tl = get_tile(p, ctl, t);
       for (int kb = 0; kb < nstep; ++kb, ++it) {
-        const int s = it % kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag,
+        const int q = it % kSfSlots;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&ctl->sfempty[q]), ((it / kSfSlots) & 1) ^ 1, abort_flag,
                                                        kWaitLimitNs))) {
           timed_out = true;
           break;
         }
-        const uint32_t dst = sf_ring + s * kSfBytes + lane * 16;
+        const uint32_t dst = sfa_ring + q * kSfABytes + lane * 16;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int64_t k = 2 * kb + h;
-          const bool kok = k < p.nkb;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {  // rows past M read as zeros
             const int64_t row = static_cast<int64_t>(tl.row0) + 32 * c + lane;
-            const bool ok = kok && row < p.M;
-            cp_async_4(dst + 3 * kAtom * h + 4 * c, ok ? p.lhs_sf + k * p.M + row : p.lhs_sf, ok ? 4u : 0u);
-          }
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {  // channels past N read as zeros
-            const int n = tl.n0 + 32 * c + lane;
-            const bool ok = kok && n < p.N;
-            cp_async_4(dst + 3 * kAtom * h + kAtom * (1 + (c >> 2)) + 4 * (c & 3),
-                       ok ? p.rhs_sf + k * brows + static_cast<int64_t>(tl.el) * p.N + n : p.rhs_sf, ok ? 4u : 0u);
+            const bool ok = k < p.nkb && row < p.M;
+            cp_async_4(dst + kAtom * h + 4 * c, ok ? p.lhs_sf + k * p.M + row : p.lhs_sf, ok ? 4u : 0u);
           }
         }
         cp_async_commit();
         if (it >= kLag) {
           cp_async_wait<kLag>();
           fence_proxy_async_smem();
-          mbar_arrive(smem_u32(&ctl->sffull[(it - kLag) % kStages]));
+          mbar_arrive(smem_u32(&ctl->sffull[(it - kLag) % kSfSlots]));
         }
       }
     }
     cp_async_wait<0>();
     fence_proxy_async_smem();
-    for (uint32_t j = it > kLag ? it - kLag : 0; j < it; ++j) mbar_arrive(smem_u32(&ctl->sffull[j % kStages]));
+    for (uint32_t j = it > kLag ? it - kLag : 0; j < it; ++j) mbar_arrive(smem_u32(&ctl->sffull[j % kSfSlots]));
     if (timed_out) {
       *abort_flag = 1;
       ctl->err = 2;
@@ -328,15 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      // column 32 c + l of the warp's 128 holds channel 4 l + c
       uint32_t w[4][16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(taddr + 32 * i, v);
+      for (int i = 0; i < 2; ++i) {
+        uint32_t u[32], v[32];
+        tmem_ld_32x32b_x32(taddr + 64 * i, u);
+        tmem_ld_32x32b_x32(taddr + 64 * i + 32, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          w[i][j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        for (int l = 0; l < 32; ++l)
+          w[l / 8][2 * (l % 8) + i] = pack_bf16x2(__uint_as_float(u[l]), __uint_as_float(v[l]));
       }
       tc_fence_before();
       __syncwarp();
@@ -424,14 +449,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Packed codes as bytes: `rows` rows of `bytes`, boxes of box_rows x 128
-// bytes with the 128-byte swizzle; reads past the extents return zeros.
-bool make_map(CUtensorMap* m, const void* ptr, uint64_t bytes, uint64_t rows, uint32_t box_rows) {
+// Packed codes as bytes, 128-byte swizzle; reads past the extents return
+// zeros.  A: boxes of 128 rows x 128 bytes.  B: row 4 l + c of the matrix is
+// (l, c), and a box of 32 l x 4 c puts it at row 32 c + l of the tile.
+bool make_map(CUtensorMap* m, const void* ptr, uint64_t bytes, uint64_t rows, bool b) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {bytes, rows}, strides[1] = {bytes};
-  cuuint32_t box[2] = {kRowBytes, box_rows}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  cuuint64_t dims[3] = {bytes, b ? rows / 4 : rows, 4}, strides[2] = {b ? 4 * bytes : bytes, bytes};
+  cuuint32_t box[3] = {kRowBytes, b ? 32u : static_cast<cuuint32_t>(kBM), 4}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, b ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -459,7 +485,7 @@ extern "C" moe_status gmm_fp4_mx(const uint8_t* lhs_q, const uint8_t* lhs_sf, co
                      N <= ((1ll << 31) - kBN) / E_local,
                  MOE_ERR_INVALID_ARG);
   MOE_HOST_CHECK(aligned16(lhs_q) && aligned16(rhs_q) && aligned16(out) &&
-                     ((reinterpret_cast<uintptr_t>(lhs_sf) | reinterpret_cast<uintptr_t>(rhs_sf)) & 3) == 0,
+                     (reinterpret_cast<uintptr_t>(lhs_sf) & 3) == 0 && aligned16(rhs_sf),
                  MOE_ERR_INVALID_ARG);
   const int64_t ntiles = (N + kBN - 1) / kBN;
   const int64_t units = ((M + kBM - 1) / kBM + E_local) * ntiles;
@@ -477,8 +503,8 @@ extern "C" moe_status gmm_fp4_mx(const uint8_t* lhs_q, const uint8_t* lhs_sf, co
     MOE_CUDA_TRY(cudaGetLastError());
   }
   CUtensorMap A, B;
-  if (!make_map(&A, lhs_q, K / 2, M, kBM)) return MOE_ERR_CUDA;
-  if (!make_map(&B, rhs_q, K / 2, static_cast<uint64_t>(E_local) * N, kBN)) return MOE_ERR_CUDA;
+  if (!make_map(&A, lhs_q, K / 2, M, false)) return MOE_ERR_CUDA;
+  if (!make_map(&B, rhs_q, K / 2, static_cast<uint64_t>(E_local) * N, true)) return MOE_ERR_CUDA;
   Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(N), static_cast<int>(K / 128),
            static_cast<int>(ntiles), reinterpret_cast<const uint32_t*>(lhs_sf),
            reinterpret_cast<const uint32_t*>(rhs_sf), out};

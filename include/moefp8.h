@@ -515,8 +515,8 @@ moe_status moe_quantize_sort_mx4(const uint16_t* x, const int32_t* topk_ids, int
  *   lhs_q [M, K/2], lhs_sf [K/128][M][4]; rhs_q [E_local, N, K/2], rhs_sf
  *   [K/128][E_local * N][4] (row e * N + n); out bf16 [M, N].
  * Groups, group_offset and E_local are as in gmm_fp8: rows outside the local
- * groups are zero.  K % 128 == 0, N % 16 == 0, E <= 1024; lhs_q, rhs_q and
- * out 16-byte aligned, the scale codes 4-byte.  MOE_ERR_UNSUPPORTED off
+ * groups are zero.  K % 128 == 0, N % 16 == 0, E <= 1024; every pointer but
+ * lhs_sf (4-byte) and group_sizes 16-byte aligned.  MOE_ERR_UNSUPPORTED off
  * sm_103. */
 moe_status gmm_fp4_mx(const uint8_t* lhs_q, const uint8_t* lhs_sf, const uint8_t* rhs_q, const uint8_t* rhs_sf,
                       const int32_t* group_sizes, int E, int group_offset, int E_local, int64_t M, int64_t K,

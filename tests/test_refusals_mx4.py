@@ -67,7 +67,7 @@ def test_product(lib):
     for bad in (dict(lq=None), dict(ls=None), dict(rq=None), dict(rs=None), dict(sz=None), dict(out=None), dict(E=0),
                 dict(E=1025), dict(g0=-1), dict(El=0), dict(g0=1), dict(E=2, g0=1, El=2), dict(M=-1), dict(M=1 << 31),
                 dict(K=0), dict(K=192), dict(K=1 << 30), dict(N=0), dict(N=24), dict(N=1 << 30), dict(lq=ODD),
-                dict(rq=ODD), dict(out=ODD), dict(ls=ctypes.c_void_p(258)), dict(rs=ctypes.c_void_p(258)),
+                dict(rq=ODD), dict(out=ODD), dict(ls=ctypes.c_void_p(258)), dict(rs=ctypes.c_void_p(260)),
                 dict(El=2147483647, E=1024)):
         assert call(**bad) == 1, bad
 
