@@ -829,7 +829,7 @@ class DecodeBuffers:
         if not n:
             raise MoEError(f"ffn_decode does not take T = {T}, k = {k}, D = {D}, F = {F}")
         self.y = torch.empty(T, D, dtype=torch.bfloat16, device=device)
-        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=device)  # (its counters have to start at zero)
         self.ws_bytes = n
 
 

@@ -74,23 +74,25 @@ constexpr int kSmemLimit = 232448;
 enum { kE4M3 = 0, kInt8 = 1, kMx8 = 2, kMx4 = 3 };
 enum { kScaleChannel = 0, kScaleBlock = 1, kScaleTensor = 2, kScaleMx = 3 };
 
+struct PhaseParams {
+  const void* act;     // phase 1: x bf16 [T, K]; phase 2: h fp32 [slots, K], or partial a [segs][slots, 2K]
+  const float* scale;  // fp32 scales, or the MX scale words
+  float* out;          // phase 1: h [slots, N], or partial a [segs][slots, 2N]; phase 2: o [segs][slots, N]
+  int K, N;            // N: channels (phase 1: F, phase 2: D)
+  int mode;
+  int nblock, nst;     // row blocks, K stages
+};
+
 struct Params {
-  const void* act;  // PHASE 1: x bf16 [T, K]; PHASE 2: h fp32 [slots, K], or partial a [segs][slots, 2K]
+  PhaseParams f[2];
   const int32_t* ids;
   const float* topk_w;
-  const float* scale;  // fp32 scales, or the MX scale words
-  float* out;          // PHASE 1: h [slots, N], or partial a [segs][slots, 2N]; PHASE 2: o [segs][slots, N]
   uint16_t* y;
-  unsigned int* count;  // finished units of every 16 output columns (PHASE 1 clears them)
-  int ncount;
+  unsigned int* sync;   // [0] warps done with phase 1, [1] CTAs that have seen all of them; zero between calls
+  unsigned int* count;  // finished units of every 16 output columns; zero between calls
   int T, k, E, g0, El;
-  int K, N;  // N: channels (PHASE 1: F, PHASE 2: D)
-  int mode;
   int cap, stages;  // pairs a chunk; ring stages
   int smax;         // segments of K at most
-  int grid1, grid2;      // CTAs of the two kernels,
-  int nblock1, nblock2;  // their row blocks
-  int nst1, nst2;        // and K stages
 };
 
 struct Ctl {
@@ -139,8 +141,11 @@ __device__ __forceinline__ int pick_segs(int units, int nst, int grid, int smax)
 
 constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
 
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ unsigned int load_acquire(const unsigned int* p) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -245,11 +250,12 @@ __device__ __forceinline__ void weights8(uint32_t w, uint32_t (&v)[4]) {
 // Every CTA of both kernels sorts for itself, to the same tables.
 
 __device__ __forceinline__ int local_expert(const Params& p, int i) {
-  const int id = __ldg(p.ids + i), e = id - p.g0;
+  const int id = __ldg(p.ids + i);
   if (id < 0 || id >= p.E) {
     raise_error(&g_err, MOE_DEVERR_BAD_EXPERT_ID);
     return 0xFFFF;
   }
+  const int e = id - p.g0;
   return e >= 0 && e < p.El ? e : 0xFFFF;
 }
 
@@ -581,43 +587,40 @@ struct Walk {
       if (q.u < total) open(q);
     }
   }
-  __device__ __forceinline__ void skip(Step& q, int n) const {  // n stages on
+  __device__ __forceinline__ int skip(Step& q, int n) const {  // n stages on; returns how many lie past the end
     while (n > 0 && q.u < total) {
       if (q.kst + n < q.end) {
         q.kst += n;
-        return;
+        return 0;
       }
       n -= q.end - q.kst;
       q.u += gridDim.x;
       if (q.u < total) open(q);
     }
+    return n;
   }
 };
 
-template <int WT, int PHASE>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Params p) {
-  using C = Cfg<WT, PHASE>;
-  constexpr int PER = C::PER;
+template <int WT>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
+                  const __grid_constant__ Params p) {
+  using G = Cfg<WT, 2>;  // the ring's geometry: phase 2's, whose activations are the wider
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* bp = smem_raw + (base - raw);
   // stages of weights | f16 activations | weight scales | activation span scales | control
   const uint32_t S = p.stages;
   const int cap = p.cap;
-  const uint32_t x_ring = base + S * C::STAGE_W;
-  const uint32_t x_bytes = cap * C::PITCH;
+  const uint32_t x_ring = base + S * G::STAGE_W;
+  const uint32_t x_bytes = cap * G::PITCH;
   const uint32_t s_ring = x_ring + S * x_bytes;
-  const uint32_t v_ring = s_ring + S * C::SCALE_BYTES;
-  const uint32_t v_bytes = C::BOXES * cap * 4;
+  const uint32_t v_ring = s_ring + S * G::SCALE_BYTES;
+  const uint32_t v_bytes = G::BOXES * cap * 4;
   Ctl* ctl = reinterpret_cast<Ctl*>(bp + (v_ring + S * v_bytes - base));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.T * p.k;
 
-  if (PHASE == 1) {
-    grid_dep_launch();
-    if (blockIdx.x == 0)
-      for (int i = threadIdx.x; i < p.ncount; i += kThreads) p.count[i] = 0;
-  }
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
@@ -629,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     ctl->no_abort = 0;
     ctl->err = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tm1);
+    tma_prefetch_desc(&tm2);
   }
   if (R <= 32) {
     if (warp == 1) build_chunks_warp(p, ctl);
@@ -640,8 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   }
   if (warp == 1) {
     __syncwarp();
-    const int segs1 = pick_segs(ctl->nchunk * p.nblock1, p.nst1, p.grid1, p.smax);
-    const int segs2 = pick_segs(ctl->nchunk * p.nblock2, p.nst2, p.grid2, p.smax);
+    const int segs1 = pick_segs(ctl->nchunk * p.f[0].nblock, p.f[0].nst, gridDim.x, p.smax);
+    const int segs2 = pick_segs(ctl->nchunk * p.f[1].nblock, p.f[1].nst, gridDim.x, p.smax);
     if (lane == 0) {
       ctl->segs1 = segs1;
       ctl->segs2 = segs2;
@@ -650,130 +654,180 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   __syncthreads();
 
   const int nchunk = ctl->nchunk;
-  constexpr int kPer = PHASE == 1 ? kRows / 2 : kRows;  // channels of a unit
   const int segs1 = ctl->segs1;
-  Walk walk;
-  walk.nblock = PHASE == 1 ? p.nblock1 : p.nblock2;
-  walk.nst = PHASE == 1 ? p.nst1 : p.nst2;
-  walk.segs = PHASE == 1 ? segs1 : ctl->segs2;
-  walk.total = nchunk * walk.nblock * walk.segs;
-  walk.ctl = ctl;
+  const int slots = nchunk > 0 ? ctl->cstart[nchunk - 1] + ctl->cnum[nchunk - 1] : 0;  // local pairs
   volatile int* abort_flag = &ctl->abort_flag;
   bool timed_out = false;
 
-  if (PHASE == 2 && nchunk == 0) {  // no local expert was chosen at all
-    grid_dep_wait();
-    const int64_t n = static_cast<int64_t>(p.T) * p.N;
+  if (nchunk == 0) {  // no local expert was chosen at all
+    const int64_t n = static_cast<int64_t>(p.T) * p.f[1].N;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
       p.y[i] = 0;
     return;
   }
 
-  const int nbox = (p.K + C::BOX_K - 1) / C::BOX_K;  // boxes along K
-  const bool words = p.mode == kScaleBlock || p.mode == kScaleMx;  // one scale word a row and 128 values of K
-  const bool partial = PHASE == 2 && segs1 > 1;                    // kernel 1 left sums of K segments
+  auto walk_of = [&](int phase) {
+    Walk w;
+    w.nblock = p.f[phase - 1].nblock;
+    w.nst = p.f[phase - 1].nst;
+    w.segs = phase == 1 ? segs1 : ctl->segs2;
+    w.total = nchunk * w.nblock * w.segs;
+    w.ctl = ctl;
+    return w;
+  };
+  auto has_words = [](const PhaseParams& f) {  // one scale word a row and 128 values of K
+    return f.mode == kScaleBlock || f.mode == kScaleMx;
+  };
+  const bool partial = segs1 > 1;  // phase 1 leaves sums of K segments
   // where the raw scale words v of stage s arrive: the end of their place
   auto raw_words = [&](uint32_t s, int v) {
-    return s_ring + s * C::SCALE_BYTES + (v + 1) * kRows * C::SCALE_ROW - kRows * 4;
+    return s_ring + s * G::SCALE_BYTES + (v + 1) * kRows * G::SCALE_ROW - kRows * 4;
   };
 
   if (warp == 0) {
     // ------------------------- weights by TMA; activations and scales by cp.async
-    const int nkb = p.K / 128;  // (used with scale words: K % 128 == 0)
-    const int64_t scale_rows = static_cast<int64_t>(PHASE == 1 ? 2 * p.N : p.N);
     const uint64_t policy = evict_first_policy();
-    auto load_weights = [&](uint32_t s, const Step& q) {
-      if (lane == 0) {
-        const uint32_t fb = smem_u32(&ctl->full[s]);
-        const int e = ctl->cexp[q.ch];
-        const int boxes = min(C::BOXES, nbox - q.kst * C::BOXES);
-        mbar_arrive_expect_tx(fb, boxes * kBoxW);
-        // rows past the tensor's channels or K arrive as zeros
-        for (int v = 0; v < boxes; ++v)
-          tma_load_3d(base + s * C::STAGE_W + v * kBoxW, &tmW, (q.kst * C::BOXES + v) * 128, q.blk * kPer,
-                      PHASE == 1 ? 2 * e : e, fb, policy);
-      }
-    };
-    // This lane's sources at a unit's first stage, kept over the unit: its part
-    // of the scale words, and of the first kKept x 32 chunks of activations.
-    constexpr int kChunks = C::ROW_BYTES / 16, kVals = PHASE == 1 ? 8 : 4;  // 16-byte chunks of a row, values in one
-    constexpr int kKept = 4;
-    constexpr int kWords = C::BOXES * C::WORDS;
-    int unit = -1, n = 0, st = 0;
-    const float* sc = p.scale;
-    const uint8_t* xsrc[kKept];
-    const int64_t kb_pitch = p.mode == kScaleMx ? p.El * scale_rows : scale_rows;  // from one 128-wide block to the next
-    auto row_src = [&](int i) {  // chunk i of the unit's activations at K = 0
-      const int r = i / kChunks, c = i % kChunks;
-      const int64_t row = PHASE == 1 ? ctl->order[st + r] / p.k : st + r;
-      return static_cast<const uint8_t*>(p.act) + (row * p.K + c * kVals) * (PHASE == 1 ? 2 : 4);
-    };
-    auto load_rest = [&](uint32_t s, const Step& q) {
-      if (q.u != unit) {
-        unit = q.u;
-        n = ctl->cnum[q.ch];
-        st = ctl->cstart[q.ch];
-        const int e = ctl->cexp[q.ch];
-        if (words) {
-          const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * p.N : lane * 4);
-          sc = p.scale + (p.mode == kScaleMx ? e * scale_rows : static_cast<int64_t>(e) * nkb * scale_rows) + n0;
-        }
-#pragma unroll
-        for (int j = 0; j < kKept; ++j)
-          xsrc[j] = lane + 32 * j < n * kChunks && !partial ? row_src(lane + 32 * j) : static_cast<const uint8_t*>(p.act);
-      }
-      if (words) {
-#pragma unroll
-        for (int v = 0; v < kWords; ++v) {
-          const int64_t kb = q.kst * kWords + v;
-          const bool ok = kb < nkb;
-          cp_async_16(raw_words(s, v) + lane * 16, ok ? sc + kb * kb_pitch : p.scale, ok ? 16u : 0u);
-        }
-      }
-      if (!partial) {
-        const int64_t k0 = static_cast<int64_t>(q.kst) * C::ROW_BYTES;
-        const uint32_t dst = x_ring + s * x_bytes;
-        // K is a multiple of 16: a chunk is all in or out
-#pragma unroll
-        for (int j = 0; j < kKept; ++j) {
-          const int i = lane + 32 * j;
-          if (i < n * kChunks) {
-            const int r = i / kChunks, c = i % kChunks;
-            const bool ok = q.kst * C::KE + c * kVals < p.K;
-            cp_async_16(dst + r * C::PITCH + c * 16, ok ? xsrc[j] + k0 : xsrc[j], ok ? 16u : 0u);
-          }
-        }
-        for (int i = lane + 32 * kKept; i < n * kChunks; i += 32) {
-          const int r = i / kChunks, c = i % kChunks;
-          const bool ok = q.kst * C::KE + c * kVals < p.K;
-          cp_async_16(dst + r * C::PITCH + c * 16, ok ? row_src(i) + k0 : static_cast<const uint8_t*>(p.act), ok ? 16u : 0u);
-        }
-      }
-      cp_async_arrive(smem_u32(&ctl->xraw[s]));
-    };
-    uint32_t s = 0, ph = 0, issued = 0;
-    Step q = walk.begin();
-    if (PHASE == 2) {
-      // the ring's first weights do not depend on kernel 1; its h does
-      Step w = q;
-      for (uint32_t i = 0; i < S && !walk.done(w); ++i, walk.next(w)) load_weights(i, w);
-      grid_dep_wait();
-      for (; issued < S && !walk.done(q); ++issued, walk.next(q)) load_rest(issued, q);
-      ph = 1;  // a full ring is out; where it is not full, no stage is left
-    }
-    for (; !walk.done(q); walk.next(q), ++issued) {
-      if (!mbar_wait_bounded_warp(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs)) {
-        timed_out = true;
-        break;
-      }
-      load_weights(s, q);
-      load_rest(s, q);
+    uint32_t s = 0, ph = 0, issued = 0;  // the ring goes on from phase 1 to phase 2
+    auto advance = [&] {
       if (++s == S) {
         s = 0;
         ph ^= 1;
       }
-    }
+    };
+    auto wait_empty = [&] {
+      if (!mbar_wait_bounded_warp(smem_u32(&ctl->empty[s]), ph ^ 1, abort_flag, kWaitLimitNs)) timed_out = true;
+      return !timed_out;
+    };
+    // All of phase 1, from every CTA: its warps count themselves.  The last CTA to
+    // have seen it sets the counters back for the next call.
+    auto wait_phase1 = [&] {
+      int ok = 1;
+      if (lane == 0) {
+        const unsigned int all = gridDim.x * kMmaWarps;
+        const uint64_t t0 = globaltimer_ns();
+        while (load_acquire(p.sync) != all) {
+          if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) {
+            ok = 0;
+            break;
+          }
+        }
+        if (ok && atomicAdd(p.sync + 1, 1u) == gridDim.x - 1) {
+          p.sync[0] = 0;
+          p.sync[1] = 0;
+        }
+      }
+      return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
+    auto run = [&](auto phase_tag) {
+      constexpr int PHASE = decltype(phase_tag)::value;
+      using C = Cfg<WT, PHASE>;
+      constexpr int kPer = PHASE == 1 ? kRows / 2 : kRows;  // channels of a unit
+      const PhaseParams& f = p.f[PHASE - 1];
+      const Walk walk = walk_of(PHASE);
+      const int nbox = (f.K + C::BOX_K - 1) / C::BOX_K;  // boxes along K
+      const bool words = has_words(f), joined = PHASE == 2 && partial;
+      const int nkb = f.K / 128;  // (used with scale words: K % 128 == 0)
+      const int64_t scale_rows = static_cast<int64_t>(PHASE == 1 ? 2 * f.N : f.N);
+      auto load_weights = [&](uint32_t s, const Step& q) {
+        if (lane == 0) {
+          const uint32_t fb = smem_u32(&ctl->full[s]);
+          const int e = ctl->cexp[q.ch];
+          const int boxes = min(C::BOXES, nbox - q.kst * C::BOXES);
+          mbar_arrive_expect_tx(fb, boxes * kBoxW);
+          // rows past the tensor's channels or K arrive as zeros
+          for (int v = 0; v < boxes; ++v)
+            tma_load_3d(base + s * C::STAGE_W + v * kBoxW, PHASE == 1 ? &tm1 : &tm2, (q.kst * C::BOXES + v) * 128, q.blk * kPer,
+                        PHASE == 1 ? 2 * e : e, fb, policy);
+        }
+      };
+      // This lane's sources at a unit's first stage, kept over the unit: its part
+      // of the scale words, and of the first kKept x 32 chunks of activations.
+      constexpr int kChunks = C::ROW_BYTES / 16, kVals = PHASE == 1 ? 8 : 4;  // 16-byte chunks of a row, values in one
+      constexpr int kKept = 4;
+      constexpr int kWords = C::BOXES * C::WORDS;
+      int unit = -1, n = 0, st = 0;
+      const float* sc = f.scale;
+      const uint8_t* xsrc[kKept];
+      const int64_t kb_pitch = f.mode == kScaleMx ? p.El * scale_rows : scale_rows;  // from one 128-wide block to the next
+      auto row_src = [&](int i) {  // chunk i of the unit's activations at K = 0
+        const int r = i / kChunks, c = i % kChunks;
+        const int64_t row = PHASE == 1 ? ctl->order[st + r] / p.k : st + r;
+        return static_cast<const uint8_t*>(f.act) + (row * f.K + c * kVals) * (PHASE == 1 ? 2 : 4);
+      };
+      auto load_rest = [&](uint32_t s, const Step& q) {
+        if (q.u != unit) {
+          unit = q.u;
+          n = ctl->cnum[q.ch];
+          st = ctl->cstart[q.ch];
+          const int e = ctl->cexp[q.ch];
+          if (words) {
+            const int64_t n0 = q.blk * kPer + (PHASE == 1 ? (lane & 15) * 4 + (lane >> 4) * f.N : lane * 4);
+            sc = f.scale + (f.mode == kScaleMx ? e * scale_rows : static_cast<int64_t>(e) * nkb * scale_rows) + n0;
+          }
+#pragma unroll
+          for (int j = 0; j < kKept; ++j)
+            xsrc[j] = lane + 32 * j < n * kChunks && !joined ? row_src(lane + 32 * j) : static_cast<const uint8_t*>(f.act);
+        }
+        if (words) {
+#pragma unroll
+          for (int v = 0; v < kWords; ++v) {
+            const int64_t kb = q.kst * kWords + v;
+            const bool ok = kb < nkb;
+            cp_async_16(raw_words(s, v) + lane * 16, ok ? sc + kb * kb_pitch : f.scale, ok ? 16u : 0u);
+          }
+        }
+        if (!joined) {
+          const int64_t k0 = static_cast<int64_t>(q.kst) * C::ROW_BYTES;
+          const uint32_t dst = x_ring + s * x_bytes;
+          // K is a multiple of 16: a chunk is all in or out
+#pragma unroll
+          for (int j = 0; j < kKept; ++j) {
+            const int i = lane + 32 * j;
+            if (i < n * kChunks) {
+              const int r = i / kChunks, c = i % kChunks;
+              const bool ok = q.kst * C::KE + c * kVals < f.K;
+              cp_async_16(dst + r * C::PITCH + c * 16, ok ? xsrc[j] + k0 : xsrc[j], ok ? 16u : 0u);
+            }
+          }
+          for (int i = lane + 32 * kKept; i < n * kChunks; i += 32) {
+            const int r = i / kChunks, c = i % kChunks;
+            const bool ok = q.kst * C::KE + c * kVals < f.K;
+            cp_async_16(dst + r * C::PITCH + c * 16, ok ? row_src(i) + k0 : static_cast<const uint8_t*>(f.act), ok ? 16u : 0u);
+          }
+        }
+        cp_async_arrive(smem_u32(&ctl->xraw[s]));
+      };
+
+      Step q = walk.begin();
+      if (PHASE == 2) {
+        // weights do not depend on phase 1: a ring of them goes out as its stages
+        // come back, then every CTA's h has to be there
+        const uint32_t s0 = s, ph0 = ph;
+        uint32_t ahead = 0;
+        for (Step w = q; ahead < S && !walk.done(w) && wait_empty(); walk.next(w), ++ahead) {
+          load_weights(s, w);
+          ++issued;
+          advance();
+        }
+        if (!timed_out) timed_out = !wait_phase1();
+        if (timed_out) return;
+        s = s0;
+        ph = ph0;
+        for (; ahead > 0; --ahead, walk.next(q)) {
+          load_rest(s, q);
+          advance();
+        }
+      }
+      for (; !walk.done(q) && wait_empty(); walk.next(q)) {
+        load_weights(s, q);
+        ++issued;
+        load_rest(s, q);
+        advance();
+      }
+    };
+    run(std::integral_constant<int, 1>{});
+    if (!timed_out) run(std::integral_constant<int, 2>{});
     if (timed_out) {
       *abort_flag = 1;
       ctl->err = 2;
@@ -786,101 +840,110 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     __syncwarp();
   } else if (warp <= kConvWarps) {
     // ---------------------- activations to f16 and MX scale codes to bf16, in place
-    const int slots = PHASE == 2 ? ctl->cstart[nchunk - 1] + ctl->cnum[nchunk - 1] : 0;
-    // h of kernel 1's segments: their sums in ascending order, then SwiGLU
-    auto join = [&](int slot, int col, bool ok, float (&v)[PER]) {
-      float a0[PER], a1[PER];
+    uint32_t step = warp - 1;  // this warp's next stage of the CTA's,
+    int left = warp - 1;       // and how many stages of the phase lie before it
+    auto run = [&](auto phase_tag) {
+      constexpr int PHASE = decltype(phase_tag)::value;
+      using C = Cfg<WT, PHASE>;
+      constexpr int PER = C::PER;
+      const PhaseParams& f = p.f[PHASE - 1];
+      const Walk walk = walk_of(PHASE);
+      // h of phase 1's segments: their sums in ascending order, then SwiGLU
+      auto join = [&](int slot, int col, bool ok, float (&v)[PER]) {
+        float a0[PER], a1[PER];
 #pragma unroll
-      for (int j = 0; j < PER; ++j) a0[j] = a1[j] = 0.0f;
-      if (ok)
-        for (int g = 0; g < segs1; ++g) {
-          const float* src = static_cast<const float*>(p.act) + (static_cast<int64_t>(g) * slots + slot) * 2 * p.K + col;
+        for (int j = 0; j < PER; ++j) a0[j] = a1[j] = 0.0f;
+        if (ok)
+          for (int g = 0; g < segs1; ++g) {
+            const float* src = static_cast<const float*>(f.act) + (static_cast<int64_t>(g) * slots + slot) * 2 * f.K + col;
 #pragma unroll
-          for (int j = 0; j < PER; j += 4) {
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(src + j));
-            const float4 w = __ldcg(reinterpret_cast<const float4*>(src + p.K + j));
-            a0[j] += u.x;
-            a0[j + 1] += u.y;
-            a0[j + 2] += u.z;
-            a0[j + 3] += u.w;
-            a1[j] += w.x;
-            a1[j + 1] += w.y;
-            a1[j + 2] += w.z;
-            a1[j + 3] += w.w;
+            for (int j = 0; j < PER; j += 4) {
+              const float4 u = __ldcg(reinterpret_cast<const float4*>(src + j));
+              const float4 w = __ldcg(reinterpret_cast<const float4*>(src + f.K + j));
+              a0[j] += u.x;
+              a0[j + 1] += u.y;
+              a0[j + 2] += u.z;
+              a0[j + 3] += u.w;
+              a1[j] += w.x;
+              a1[j + 1] += w.y;
+              a1[j + 2] += w.z;
+              a1[j + 3] += w.w;
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[j] = ok ? __fmul_rn(silu_f32(a0[j]), a1[j]) : 0.0f;
+      };
+      // a lane's PER values of the raw row at `at`
+      auto raw = [&](uint32_t at, float (&v)[PER]) {
+#pragma unroll
+        for (int j = 0; j < PER; j += 4) {
+          if (PHASE == 1) {
+            const uint2 d = lds64(at + (lane * PER + j) * 2);
+            v[j] = bf16lo(d.x);
+            v[j + 1] = bf16hi(d.x);
+            v[j + 2] = bf16lo(d.y);
+            v[j + 3] = bf16hi(d.y);
+          } else {
+            const uint4 d = lds128(at + (lane * PER + j) * 4);
+            v[j] = __uint_as_float(d.x);
+            v[j + 1] = __uint_as_float(d.y);
+            v[j + 2] = __uint_as_float(d.z);
+            v[j + 3] = __uint_as_float(d.w);
           }
         }
-#pragma unroll
-      for (int j = 0; j < PER; ++j) v[j] = ok ? __fmul_rn(silu_f32(a0[j]), a1[j]) : 0.0f;
-    };
-    // a lane's PER values of the raw row at `at`
-    auto raw = [&](uint32_t at, float (&v)[PER]) {
-#pragma unroll
-      for (int j = 0; j < PER; j += 4) {
-        if (PHASE == 1) {
-          const uint2 d = lds64(at + (lane * PER + j) * 2);
-          v[j] = bf16lo(d.x);
-          v[j + 1] = bf16hi(d.x);
-          v[j + 2] = bf16lo(d.y);
-          v[j + 3] = bf16hi(d.y);
-        } else {
-          const uint4 d = lds128(at + (lane * PER + j) * 4);
-          v[j] = __uint_as_float(d.x);
-          v[j + 1] = __uint_as_float(d.y);
-          v[j + 2] = __uint_as_float(d.z);
-          v[j + 3] = __uint_as_float(d.w);
-        }
-      }
-    };
+      };
 
-    if (PHASE == 2) grid_dep_wait();  // h is kernel 1's
-    Step q = walk.begin();
-    walk.skip(q, warp - 1);
-    for (uint32_t step = warp - 1; !walk.done(q); step += kConvWarps, walk.skip(q, kConvWarps)) {
-      const uint32_t s = step % S, ph = (step / S) & 1;
-      if (!mbar_wait_bounded_warp(smem_u32(&ctl->xraw[s]), ph, abort_flag, kWaitLimitNs)) {
-        timed_out = true;
-        break;
-      }
-      if (C::MX) {  // a lane: four rows' words of four codes, as bf16
-        auto pair = [](uint32_t w) {  // the low two codes of w
-          return pack_bf16x2(e8m0_value(w & 0xFFu), e8m0_value((w >> 8) & 0xFFu));
-        };
+      Step q = walk.begin();
+      left = walk.skip(q, left);
+      for (; !walk.done(q); step += kConvWarps, left = walk.skip(q, kConvWarps)) {
+        const uint32_t s = step % S, ph = (step / S) & 1;
+        if (!mbar_wait_bounded_warp(smem_u32(&ctl->xraw[s]), ph, abort_flag, kWaitLimitNs)) {
+          timed_out = true;
+          break;
+        }
+        if (C::MX) {  // a lane: four rows' words of four codes, as bf16
+          auto pair = [](uint32_t w) {  // the low two codes of w
+            return pack_bf16x2(e8m0_value(w & 0xFFu), e8m0_value((w >> 8) & 0xFFu));
+          };
 #pragma unroll
-        for (int v = 0; v < C::BOXES * C::WORDS; ++v) {
-          const uint4 u = lds128(raw_words(s, v) + lane * 16);
-          const uint32_t dst = s_ring + s * C::SCALE_BYTES + (v * kRows + lane * 4) * C::SCALE_ROW;
-          __syncwarp();  // the bf16 go over the words
-          sts128(dst, make_uint4(pair(u.x), pair(u.x >> 16), pair(u.y), pair(u.y >> 16)));
-          sts128(dst + 16, make_uint4(pair(u.z), pair(u.z >> 16), pair(u.w), pair(u.w >> 16)));
-        }
-      }
-      const int n = ctl->cnum[q.ch];
-      const uint32_t at = x_ring + s * x_bytes, av = v_ring + s * v_bytes;
-      if (partial) {
-        const int st = ctl->cstart[q.ch];
-        for (int i = 0; i < n; ++i)
-          for (int b = 0; b < C::BOXES; ++b) {
-            const int col = q.kst * C::KE + b * C::BOX_K + lane * PER;
-            float v[PER];
-            join(st + i, col, col < p.K, v);
-            store_span<PER>(v, at + i * C::PITCH + b * C::SPAN_BYTES, av + (b * cap + i) * 4, lane);
+          for (int v = 0; v < C::BOXES * C::WORDS; ++v) {
+            const uint4 u = lds128(raw_words(s, v) + lane * 16);
+            const uint32_t dst = s_ring + s * C::SCALE_BYTES + (v * kRows + lane * 4) * C::SCALE_ROW;
+            __syncwarp();  // the bf16 go over the words
+            sts128(dst, make_uint4(pair(u.x), pair(u.x >> 16), pair(u.y), pair(u.y >> 16)));
+            sts128(dst + 16, make_uint4(pair(u.z), pair(u.z >> 16), pair(u.w), pair(u.w >> 16)));
           }
-      } else {
-        // two spans' latencies together: a row's two, or (one a row) two rows' (an odd last one twice)
-        constexpr int kRowsAtOnce = C::BOXES == 2 ? 1 : 2;
-        for (int i = 0; i < n; i += kRowsAtOnce) {
-          const int i1 = C::BOXES == 2 ? i : (i + 1 < n ? i + 1 : i), b1 = C::BOXES - 1;
-          const uint32_t at0 = at + i * C::PITCH, at1 = at + i1 * C::PITCH + b1 * C::SPAN_BYTES;
-          float v[PER], w[PER];
-          raw(at0, v);
-          raw(at1, w);
-          store_span<PER>(v, at0, av + i * 4, lane);
-          store_span<PER>(w, at1, av + (b1 * cap + i1) * 4, lane);
         }
+        const int n = ctl->cnum[q.ch];
+        const uint32_t at = x_ring + s * x_bytes, av = v_ring + s * v_bytes;
+        if (PHASE == 2 && partial) {
+          const int st = ctl->cstart[q.ch];
+          for (int i = 0; i < n; ++i)
+            for (int b = 0; b < C::BOXES; ++b) {
+              const int col = q.kst * C::KE + b * C::BOX_K + lane * PER;
+              float v[PER];
+              join(st + i, col, col < f.K, v);
+              store_span<PER>(v, at + i * C::PITCH + b * C::SPAN_BYTES, av + (b * cap + i) * 4, lane);
+            }
+        } else {
+          // two spans' latencies together: a row's two, or (one a row) two rows' (an odd last one twice)
+          constexpr int kRowsAtOnce = C::BOXES == 2 ? 1 : 2;
+          for (int i = 0; i < n; i += kRowsAtOnce) {
+            const int i1 = C::BOXES == 2 ? i : (i + 1 < n ? i + 1 : i), b1 = C::BOXES - 1;
+            const uint32_t at0 = at + i * C::PITCH, at1 = at + i1 * C::PITCH + b1 * C::SPAN_BYTES;
+            float v[PER], w[PER];
+            raw(at0, v);
+            raw(at1, w);
+            store_span<PER>(v, at0, av + i * 4, lane);
+            store_span<PER>(w, at1, av + (b1 * cap + i1) * 4, lane);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->xfull[s]));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->xfull[s]));
-    }
+    };
+    run(std::integral_constant<int, 1>{});
+    if (!timed_out) run(std::integral_constant<int, 2>{});
     if (timed_out) {
       *abort_flag = 1;
       ctl->err = 2;
@@ -889,221 +952,235 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     // ----------------------------------------------------------- contraction
     const int mw = warp - 1 - kConvWarps;
     const int g = lane >> 2, t4 = lane & 3;
-    // rows of the fragment: 0..7 from row A, 8..15 from row B
-    const int rowA = PHASE == 1 ? 8 * mw : 16 * mw, rowB = PHASE == 1 ? kRows / 2 + 8 * mw : 16 * mw + 8;
-    const int lrow = ((lane >> 3) & 1 ? rowB : rowA) + (lane & 7);  // the row this lane addresses for ldmatrix
-    const uint32_t w_off = lrow * 128, swz = (lrow & 7) * 16;
-    const uint32_t x_off = g * C::PITCH + t4 * (WT == kMx4 ? 16 : 8);
-    const int slots = ctl->cstart[nchunk > 0 ? nchunk - 1 : 0] + ctl->cnum[nchunk > 0 ? nchunk - 1 : 0];
     uint32_t s = 0, ph = 0;
-    if (PHASE == 2) grid_dep_wait();  // before o and the counters are touched
-
-    auto unit = [&](auto nt_tag, const Step& q) {
-      constexpr int NT = decltype(nt_tag)::value;
-      float acc[NT][4];
+    auto run = [&](auto phase_tag) {
+      constexpr int PHASE = decltype(phase_tag)::value;
+      using C = Cfg<WT, PHASE>;
+      constexpr int kPer = PHASE == 1 ? kRows / 2 : kRows;  // channels of a unit
+      const PhaseParams& f = p.f[PHASE - 1];
+      const Walk walk = walk_of(PHASE);
+      const int nbox = (f.K + C::BOX_K - 1) / C::BOX_K;  // boxes along K
+      // rows of the fragment: 0..7 from row A, 8..15 from row B
+      const int rowA = PHASE == 1 ? 8 * mw : 16 * mw, rowB = PHASE == 1 ? kRows / 2 + 8 * mw : 16 * mw + 8;
+      const int lrow = ((lane >> 3) & 1 ? rowB : rowA) + (lane & 7);  // the row this lane addresses for ldmatrix
+      const uint32_t w_off = lrow * 128, swz = (lrow & 7) * 16;
+      const uint32_t x_off = g * C::PITCH + t4 * (WT == kMx4 ? 16 : 8);
+      auto unit = [&](auto nt_tag, const Step& q) {
+        constexpr int NT = decltype(nt_tag)::value;
+        float acc[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-      // what the unit's end needs, asked for before its products
-      const int e = ctl->cexp[q.ch], n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
-      const int ca = q.blk * kPer + (PHASE == 1 ? 8 * mw : 16 * mw) + g;  // channel of row A
-      const int cb = PHASE == 1 ? ca : ca + 8;
-      float fa = 1.0f, fb = 1.0f;
-      if (p.mode == kScaleChannel) {
-        const float* sc = p.scale + static_cast<int64_t>(e) * (PHASE == 1 ? 2 * p.N : p.N);
-        if (ca < p.N) fa = __ldg(sc + ca);
-        if (cb < p.N) fb = __ldg(sc + (PHASE == 1 ? p.N : 0) + cb);
-      } else if (p.mode == kScaleTensor) {
-        fa = fb = __ldg(p.scale);
-      }
+          for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+        // what the unit's end needs, asked for before its products
+        const int e = ctl->cexp[q.ch], n = ctl->cnum[q.ch], st = ctl->cstart[q.ch];
+        const int ca = q.blk * kPer + (PHASE == 1 ? 8 * mw : 16 * mw) + g;  // channel of row A
+        const int cb = PHASE == 1 ? ca : ca + 8;
+        float fa = 1.0f, fb = 1.0f;
+        if (f.mode == kScaleChannel) {
+          const float* sc = f.scale + static_cast<int64_t>(e) * (PHASE == 1 ? 2 * f.N : f.N);
+          if (ca < f.N) fa = __ldg(sc + ca);
+          if (cb < f.N) fb = __ldg(sc + (PHASE == 1 ? f.N : 0) + cb);
+        } else if (f.mode == kScaleTensor) {
+          fa = fb = __ldg(f.scale);
+        }
 
-      // Up to eight tokens: boxes alternate between two register sets, one box's
-      // loads in flight while the other's products run.  A stage goes back as
-      // soon as its last box is done; the next is waited for before that only if
-      // it is already there.
-      const int first = q.kst * C::BOXES, last = min(q.end * C::BOXES, nbox);
-      uint32_t ls = s, lph = ph;  // the stage that the next load reads
-      auto ready = [&] {
-        return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&ctl->xfull[ls]), lph) &&
-                                           mbar_try_wait(smem_u32(&ctl->full[ls]), lph));
-      };
-      auto wait = [&] {
-        if (!mbar_wait_bounded_warp(smem_u32(&ctl->xfull[ls]), lph, abort_flag, kWaitLimitNs) ||
-            !mbar_wait_bounded_warp(smem_u32(&ctl->full[ls]), lph, abort_flag, kWaitLimitNs)) {
-          timed_out = true;
-          *abort_flag = 1;
-        }
-      };
-      auto box_at = [&](uint32_t sg, int v) {
-        BoxAt a;
-        a.wt = base + sg * C::STAGE_W + v * kBoxW + w_off;
-        a.xb = x_ring + sg * x_bytes + v * C::SPAN_BYTES + x_off;
-        a.sA = s_ring + sg * C::SCALE_BYTES + (v * C::WORDS * kRows + rowA + g) * C::SCALE_ROW;
-        a.sB = a.sA + (rowB - rowA) * C::SCALE_ROW;
-        a.xs = v_ring + sg * v_bytes + v * cap * 4 + t4 * 8;
-        return a;
-      };
-      // box j of the unit: its loads, and what follows when its products are done
-      auto load = [&](Box<WT, PHASE, NT>& b, int j) {
-        b.load(box_at(ls, C::BOXES == 2 ? j & 1 : 0), swz, p.mode == kScaleBlock);
-        if (C::BOXES == 1 || (j & 1) || j + 1 == last) {
-          if (++ls == S) {
-            ls = 0;
-            lph ^= 1;
+        // Up to eight tokens: boxes alternate between two register sets, one box's
+        // loads in flight while the other's products run.  A stage goes back as
+        // soon as its last box is done; the next is waited for before that only if
+        // it is already there.
+        const int first = q.kst * C::BOXES, last = min(q.end * C::BOXES, nbox);
+        uint32_t ls = s, lph = ph;  // the stage that the next load reads
+        auto ready = [&] {
+          return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&ctl->xfull[ls]), lph) &&
+                                             mbar_try_wait(smem_u32(&ctl->full[ls]), lph));
+        };
+        auto wait = [&] {
+          if (!mbar_wait_bounded_warp(smem_u32(&ctl->xfull[ls]), lph, abort_flag, kWaitLimitNs) ||
+              !mbar_wait_bounded_warp(smem_u32(&ctl->full[ls]), lph, abort_flag, kWaitLimitNs)) {
+            timed_out = true;
+            *abort_flag = 1;
           }
-        }
-      };
-      auto work = [&](Box<WT, PHASE, NT>& b, int j) {
-        b.contract(acc, box_at(s, C::BOXES == 2 ? j & 1 : 0));
-        if (C::BOXES == 1 || (j & 1) || j + 1 == last) {
-          fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
-          if (++s == S) {
-            s = 0;
-            ph ^= 1;
+        };
+        auto box_at = [&](uint32_t sg, int v) {
+          BoxAt a;
+          a.wt = base + sg * C::STAGE_W + v * kBoxW + w_off;
+          a.xb = x_ring + sg * x_bytes + v * C::SPAN_BYTES + x_off;
+          a.sA = s_ring + sg * C::SCALE_BYTES + (v * C::WORDS * kRows + rowA + g) * C::SCALE_ROW;
+          a.sB = a.sA + (rowB - rowA) * C::SCALE_ROW;
+          a.xs = v_ring + sg * v_bytes + v * cap * 4 + t4 * 8;
+          return a;
+        };
+        // box j of the unit: its loads, and what follows when its products are done
+        auto load = [&](Box<WT, PHASE, NT>& b, int j) {
+          b.load(box_at(ls, C::BOXES == 2 ? j & 1 : 0), swz, f.mode == kScaleBlock);
+          if (C::BOXES == 1 || (j & 1) || j + 1 == last) {
+            if (++ls == S) {
+              ls = 0;
+              lph ^= 1;
+            }
           }
-        }
-      };
-      if constexpr (NT == 1) {
-        Box<WT, PHASE, NT> b0, b1;
-        wait();
-        if (!timed_out) load(b0, first);
-        for (int j = first; j < last && !timed_out; j += 2) {  // first is even (two boxes a stage) or any (one)
-          if (j + 1 < last) {
-            if (C::BOXES == 1) {
-              if (ready()) {
-                load(b1, j + 1);
-                work(b0, j);
+        };
+        auto work = [&](Box<WT, PHASE, NT>& b, int j) {
+          b.contract(acc, box_at(s, C::BOXES == 2 ? j & 1 : 0));
+          if (C::BOXES == 1 || (j & 1) || j + 1 == last) {
+            fence_proxy_async_smem();  // this warp's reads of the stage before the next copy into it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
+            if (++s == S) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+        };
+        if constexpr (NT == 1) {
+          Box<WT, PHASE, NT> b0, b1;
+          wait();
+          if (!timed_out) load(b0, first);
+          for (int j = first; j < last && !timed_out; j += 2) {  // first is even (two boxes a stage) or any (one)
+            if (j + 1 < last) {
+              if (C::BOXES == 1) {
+                if (ready()) {
+                  load(b1, j + 1);
+                  work(b0, j);
+                } else {
+                  work(b0, j);
+                  wait();
+                  if (timed_out) break;
+                  load(b1, j + 1);
+                }
               } else {
-                work(b0, j);
-                wait();
-                if (timed_out) break;
                 load(b1, j + 1);
+                work(b0, j);
+              }
+              if (j + 2 < last) {
+                if (ready()) {
+                  load(b0, j + 2);
+                  work(b1, j + 1);
+                } else {
+                  work(b1, j + 1);
+                  wait();
+                  if (timed_out) break;
+                  load(b0, j + 2);
+                }
+              } else {
+                work(b1, j + 1);
               }
             } else {
-              load(b1, j + 1);
               work(b0, j);
             }
-            if (j + 2 < last) {
-              if (ready()) {
-                load(b0, j + 2);
-                work(b1, j + 1);
+          }
+        } else {  // (two sets of more tokens' fragments do not fit in the registers)
+          for (int j = first; j < last; ++j) {
+            if (C::BOXES == 1 || !(j & 1)) wait();
+            if (timed_out) break;
+            Box<WT, PHASE, NT> b;
+            load(b, j);
+            work(b, j);
+          }
+        }
+        if (timed_out) return;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int col = nt * 8 + 2 * t4 + j;
+            if (col >= n) continue;
+            const float va = acc[nt][j] * fa, vb = acc[nt][2 + j] * fb;
+            if (PHASE == 1) {
+              if (ca >= f.N) continue;
+              if (walk.segs == 1) {
+                f.out[static_cast<int64_t>(st + col) * f.N + ca] = __fmul_rn(silu_f32(va), vb);
               } else {
-                work(b1, j + 1);
-                wait();
-                if (timed_out) break;
-                load(b0, j + 2);
+                float* o = f.out + (static_cast<int64_t>(q.seg) * slots + st + col) * 2 * f.N;
+                o[ca] = va;
+                o[f.N + ca] = vb;
               }
             } else {
-              work(b1, j + 1);
+              float* o = f.out + (static_cast<int64_t>(q.seg) * slots + st + col) * f.N;
+              if (ca < f.N) o[ca] = va;
+              if (cb < f.N) o[cb] = vb;
             }
-          } else {
-            work(b0, j);
           }
-        }
-      } else {  // (two sets of more tokens' fragments do not fit in the registers)
-        for (int j = first; j < last; ++j) {
-          if (C::BOXES == 1 || !(j & 1)) wait();
-          if (timed_out) break;
-          Box<WT, PHASE, NT> b;
-          load(b, j);
-          work(b, j);
-        }
-      }
-      if (timed_out) return;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = nt * 8 + 2 * t4 + j;
-          if (col >= n) continue;
-          const float va = acc[nt][j] * fa, vb = acc[nt][2 + j] * fb;
-          if (PHASE == 1) {
-            if (ca >= p.N) continue;
-            if (walk.segs == 1) {
-              p.out[static_cast<int64_t>(st + col) * p.N + ca] = __fmul_rn(silu_f32(va), vb);
-            } else {
-              float* o = p.out + (static_cast<int64_t>(q.seg) * slots + st + col) * 2 * p.N;
-              o[ca] = va;
-              o[p.N + ca] = vb;
-            }
-          } else {
-            float* o = p.out + (static_cast<int64_t>(q.seg) * slots + st + col) * p.N;
-            if (ca < p.N) o[ca] = va;
-            if (cb < p.N) o[cb] = vb;
-          }
-        }
-    };
+      };
 
-    for (Step q = walk.begin(); !walk.done(q) && !timed_out;) {
-      const int n = ctl->cnum[q.ch];
-      if (n <= 8)
-        unit(std::integral_constant<int, 1>{}, q);
-      else if (n <= 16)
-        unit(std::integral_constant<int, 2>{}, q);
-      else
-        unit(std::integral_constant<int, 4>{}, q);
-      if (PHASE == 2 && !timed_out) {
-        // the last unit (over all CTAs) that gets to these 16 columns sums their
-        // pairs into y: each warp for the rows of its own, without its neighbours
-        __threadfence();
-        __syncwarp();
-        unsigned int done = 0;
-        if (lane == 0) done = atomicAdd(p.count + q.blk * kMmaWarps + mw, 1u);
-        done = __shfl_sync(0xffffffffu, done, 0);
-        const int d = q.blk * kRows + 16 * mw + 4 * (lane & 3);
-        if (done == static_cast<unsigned>(nchunk * walk.segs - 1) && d < p.N) {
+      for (Step q = walk.begin(); !walk.done(q) && !timed_out;) {
+        const int n = ctl->cnum[q.ch];
+        if (n <= 8)
+          unit(std::integral_constant<int, 1>{}, q);
+        else if (n <= 16)
+          unit(std::integral_constant<int, 2>{}, q);
+        else
+          unit(std::integral_constant<int, 4>{}, q);
+        if (PHASE == 2 && !timed_out) {
+          // the last unit (over all CTAs) that gets to these 16 columns sums their
+          // pairs into y: each warp for the rows of its own, without its neighbours
           __threadfence();
-          const int64_t seg_pitch = static_cast<int64_t>(slots) * p.N;
-          for (int t = lane >> 2; t < p.T; t += 8) {
-            float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int j0 = 0; j0 < p.k; j0 += 8) {
-              float4 o[8];
-              bool ok[8];
-              float w[8];
+          __syncwarp();
+          unsigned int done = 0;
+          if (lane == 0) done = atomicAdd(p.count + q.blk * kMmaWarps + mw, 1u);
+          done = __shfl_sync(0xffffffffu, done, 0);
+          const int d = q.blk * kRows + 16 * mw + 4 * (lane & 3);
+          const bool all = done == static_cast<unsigned>(nchunk * walk.segs - 1);
+          if (all && lane == 0) p.count[q.blk * kMmaWarps + mw] = 0;  // for the next call
+          if (all && d < f.N) {
+            __threadfence();
+            const int64_t seg_pitch = static_cast<int64_t>(slots) * f.N;
+            for (int t = lane >> 2; t < p.T; t += 8) {
+              float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              for (int j0 = 0; j0 < p.k; j0 += 8) {
+                float4 o[8];
+                bool ok[8];
+                float w[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {  // eight pairs' loads first
-                const int pr = t * p.k + j0 + j;
-                const int slot = j0 + j < p.k ? ctl->pos[pr] : 0xFFFF;
-                ok[j] = slot != 0xFFFF;
-                o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                w[j] = 1.0f;
-                if (ok[j]) {
-                  const float* src = p.out + static_cast<int64_t>(slot) * p.N + d;
-                  o[j] = __ldcg(reinterpret_cast<const float4*>(src));
-                  if (p.topk_w) w[j] = __ldg(p.topk_w + pr);
+                for (int j = 0; j < 8; ++j) {  // eight pairs' loads first
+                  const int pr = t * p.k + j0 + j;
+                  const int slot = j0 + j < p.k ? ctl->pos[pr] : 0xFFFF;
+                  ok[j] = slot != 0xFFFF;
+                  o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                  w[j] = 1.0f;
+                  if (ok[j]) {
+                    const float* src = f.out + static_cast<int64_t>(slot) * f.N + d;
+                    o[j] = __ldcg(reinterpret_cast<const float4*>(src));
+                    if (p.topk_w) w[j] = __ldg(p.topk_w + pr);
+                  }
                 }
-              }
-              for (int sg = 1; sg < walk.segs; ++sg)
+                for (int sg = 1; sg < walk.segs; ++sg)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    if (ok[j]) {
+                      const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                          f.out + sg * seg_pitch + static_cast<int64_t>(ctl->pos[t * p.k + j0 + j]) * f.N + d));
+                      o[j].x += v.x;
+                      o[j].y += v.y;
+                      o[j].z += v.z;
+                      o[j].w += v.w;
+                    }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                   if (ok[j]) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                        p.out + sg * seg_pitch + static_cast<int64_t>(ctl->pos[t * p.k + j0 + j]) * p.N + d));
-                    o[j].x += v.x;
-                    o[j].y += v.y;
-                    o[j].z += v.z;
-                    o[j].w += v.w;
+                    a[0] = __fmaf_rn(w[j], o[j].x, a[0]);
+                    a[1] = __fmaf_rn(w[j], o[j].y, a[1]);
+                    a[2] = __fmaf_rn(w[j], o[j].z, a[2]);
+                    a[3] = __fmaf_rn(w[j], o[j].w, a[3]);
                   }
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (ok[j]) {
-                  a[0] = __fmaf_rn(w[j], o[j].x, a[0]);
-                  a[1] = __fmaf_rn(w[j], o[j].y, a[1]);
-                  a[2] = __fmaf_rn(w[j], o[j].z, a[2]);
-                  a[3] = __fmaf_rn(w[j], o[j].w, a[3]);
-                }
+              }
+              *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t) * f.N + d) =
+                  make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
             }
-            *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t) * p.N + d) =
-                make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
           }
+          __syncwarp();
         }
-        __syncwarp();
+        q.u += gridDim.x;
+        if (!walk.done(q)) walk.open(q);
       }
-      q.u += gridDim.x;
-      if (!walk.done(q)) walk.open(q);
+    };
+    run(std::integral_constant<int, 1>{});
+    if (!timed_out) {
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) atomicAdd(p.sync, 1u);
+      run(std::integral_constant<int, 2>{});
     }
     if (timed_out) {
       *abort_flag = 1;
@@ -1141,6 +1218,7 @@ bool make_map(CUtensorMap* m, const void* ptr, uint64_t bytes, uint64_t rows, ui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int64_t kSyncWords = 64;
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t blocks(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
@@ -1150,8 +1228,10 @@ int max_segs(int64_t R) {
   return static_cast<int>(s < 1 ? 1 : (s > kMaxSegs ? kMaxSegs : s));
 }
 
-// Workspace: h fp32 [R, F] or partial a [segs][R, 2F] | o fp32 [segs][R, D] |
-// a counter for every 16 output columns, each part 256-byte aligned.
+// Workspace: the sync words and a counter for every 16 output columns (zero
+// between calls) | h fp32 [R, F] or partial a [segs][R, 2F] | o fp32
+// [segs][R, D], each part 256-byte aligned.
+int64_t count_bytes(int64_t D) { return align256((kSyncWords + blocks(D, kRows) * kMmaWarps) * 4); }
 int64_t h_bytes(int64_t R, int64_t F) {
   const int64_t s = max_segs(R);
   return align256(R * F * 4 * (s > 1 ? 2 * s : 1));
@@ -1163,43 +1243,39 @@ bool shape_ok(int64_t T, int k, int64_t D, int64_t F) {
          F % 16 == 0 && D <= 32768 && F <= 32768;
 }
 
-template <int WT, int PHASE>
-moe_status launch(const void* w, Params p, int grid, cudaStream_t st) {
-  using C = Cfg<WT, PHASE>;
-  CUtensorMap tm;
-  const uint64_t bytes = WT == kMx4 ? p.K / 2 : p.K;
-  if (!make_map(&tm, w, bytes, p.N, static_cast<uint64_t>(p.El) * (PHASE == 1 ? 2 : 1), PHASE == 1 ? kRows / 2 : kRows,
-                PHASE == 1 ? 2 : 1))
+template <int WT>
+moe_status launch(const void* w_in, const void* w_out, Params p, int sms, cudaStream_t st) {
+  using C = Cfg<WT, 2>;
+  const PhaseParams &f1 = p.f[0], &f2 = p.f[1];
+  CUtensorMap tm1, tm2;
+  const int half = WT == kMx4 ? 2 : 1;
+  if (!make_map(&tm1, w_in, f1.K / half, f1.N, 2ull * p.El, kRows / 2, 2) ||
+      !make_map(&tm2, w_out, f2.K / half, f2.N, p.El, kRows, 1))
     return MOE_ERR_CUDA;
   const size_t stage = C::STAGE_W + static_cast<size_t>(p.cap) * (C::PITCH + 4 * C::BOXES) + C::SCALE_BYTES;
   const size_t fixed = 1024 + kCtlBytes;
   p.stages = static_cast<int>((kSmemLimit - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
+  // the ring holds the pair sort's bits and words first (at most 136 KB; the smallest ring has 160)
+  const size_t sort = (static_cast<size_t>((p.T * p.k + 31) / 32) + 1) * p.El * 4;
+  MOE_HOST_CHECK(p.stages >= 2 && p.stages * stage >= sort, MOE_ERR_UNSUPPORTED);
   const size_t smem = fixed + p.stages * stage;
-  auto kernel = decode_kernel<WT, PHASE>;
+  // no more CTAs than units (a chunk a pair, all segments)
+  const int64_t u = static_cast<int64_t>(p.T) * p.k * p.smax * (f1.nblock > f2.nblock ? f1.nblock : f2.nblock);
+  auto kernel = decode_kernel<WT>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs at once: they wait for one another between the phases
+  attr[0].val.cooperative = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(u < sms ? u : sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = PHASE == 2 ? 1 : 0;
-  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tm, p));
+  cfg.numAttrs = 1;
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tm1, tm2, p));
   return MOE_OK;
-}
-
-template <int PHASE>
-moe_status launch_type(int wt, const void* w, const Params& p, int grid, cudaStream_t st) {
-  switch (wt) {
-    case kE4M3: return launch<kE4M3, PHASE>(w, p, grid, st);
-    case kInt8: return launch<kInt8, PHASE>(w, p, grid, st);
-    case kMx8: return launch<kMx8, PHASE>(w, p, grid, st);
-    default: return launch<kMx4, PHASE>(w, p, grid, st);
-  }
 }
 
 // Scale mode of one weight tensor in the kernel's terms, -1 if it is not taken.
@@ -1225,7 +1301,7 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_take_err
 
 extern "C" size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F) {
   if (!shape_ok(T, k, D, F)) return 0;
-  return static_cast<size_t>(h_bytes(T * k, F) + o_bytes(T * k, D) + align256(blocks(D, kRows) * kMmaWarps * 4));
+  return static_cast<size_t>(count_bytes(D) + h_bytes(T * k, F) + o_bytes(T * k, D));
 }
 
 extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int k,
@@ -1258,15 +1334,20 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   cudaStream_t st = as_stream(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int64_t R = T * k;
-  float* h = reinterpret_cast<float*>(ws);
-  float* o = reinterpret_cast<float*>(ws + h_bytes(R, F));
+  float* h = reinterpret_cast<float*>(ws + count_bytes(D));
+  float* o = reinterpret_cast<float*>(ws + count_bytes(D) + h_bytes(R, F));
   const int ke = 256;  // values of K in a stage, of either width
+  const int d = static_cast<int>(D), f = static_cast<int>(F);
   Params p{};
+  p.f[0] = {x, static_cast<const float*>(s_in), h, d, f, kin, static_cast<int>(blocks(F, kRows / 2)),
+            static_cast<int>(blocks(D, ke))};
+  p.f[1] = {h, static_cast<const float*>(s_out), o, f, d, kout, static_cast<int>(blocks(D, kRows)),
+            static_cast<int>(blocks(F, ke))};
   p.ids = topk_ids;
   p.topk_w = topk_w;
   p.y = y;
-  p.count = reinterpret_cast<unsigned int*>(ws + h_bytes(R, F) + o_bytes(R, D));
-  p.ncount = static_cast<int>(blocks(D, kRows)) * kMmaWarps;
+  p.sync = reinterpret_cast<unsigned int*>(ws);
+  p.count = p.sync + kSyncWords;
   p.T = static_cast<int>(T);
   p.k = k;
   p.E = E;
@@ -1279,27 +1360,10 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   p.cap = T <= 8 || R <= 2 * static_cast<int64_t>(E_local) ? 8
                                                            : (T <= 16 || R <= 6 * static_cast<int64_t>(E_local) ? 16 : 32);
   p.smax = max_segs(R);
-  p.nblock1 = static_cast<int>(blocks(F, kRows / 2));
-  p.nst1 = static_cast<int>(blocks(D, ke));
-  p.nblock2 = static_cast<int>(blocks(D, kRows));
-  p.nst2 = static_cast<int>(blocks(F, ke));
-  // no more CTAs than units (a chunk a pair, all segments)
-  const int64_t u1 = R * p.nblock1 * p.smax, u2 = R * p.nblock2 * p.smax;
-  p.grid1 = static_cast<int>(u1 < sms ? u1 : sms);
-  p.grid2 = static_cast<int>(u2 < sms ? u2 : sms);
-  p.act = x;
-  p.scale = static_cast<const float*>(s_in);
-  p.out = h;
-  p.K = static_cast<int>(D);
-  p.N = static_cast<int>(F);
-  p.mode = kin;
-  moe_status s = launch_type<1>(type, w_in, p, p.grid1, st);
-  if (s != MOE_OK) return s;
-  p.act = h;
-  p.scale = static_cast<const float*>(s_out);
-  p.out = o;
-  p.K = static_cast<int>(F);
-  p.N = static_cast<int>(D);
-  p.mode = kout;
-  return launch_type<2>(type, w_out, p, p.grid2, st);
+  switch (type) {
+    case MOE_WEIGHT_E4M3: return launch<kE4M3>(w_in, w_out, p, sms, st);
+    case MOE_WEIGHT_INT8: return launch<kInt8>(w_in, w_out, p, sms, st);
+    case MOE_WEIGHT_MXFP8: return launch<kMx8>(w_in, w_out, p, sms, st);
+    default: return launch<kMx4>(w_in, w_out, p, sms, st);
+  }
 }

@@ -581,7 +581,7 @@ moe_status gmm_fp8_w8(const uint8_t* lhs_q, const float* lhs_scale, moe_scale_mo
 size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
 
 /* ------------------------------------------------------------------------
- * The expert FFN of a decoding step (a few tokens), in two kernels:
+ * The expert FFN of a decoding step (a few tokens), in one cooperative kernel:
  *   y[t] = bf16( sum_j topk_w[t, j] * Wo[e] (silu(W0[e] x[t]) * (W1[e] x[t])) ),
  *   e = topk_ids[t, j], in ascending j.
  * With a few tokens the bytes of the chosen experts' weights are the cost, so
@@ -605,8 +605,10 @@ size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
  *   Experts outside [group_offset, group_offset + E_local) add nothing.
  *   y         bf16 [T, D]
  *   workspace moe_ffn_decode_workspace_bytes(T, k, D, F) bytes of device
- *             memory, not initialised, 16-byte aligned.  Calls that may overlap
- *             on the GPU need workspaces of their own.
+ *             memory, 16-byte aligned, ZERO before its first use: it holds
+ *             counters, which every call leaves at zero (after a call that set
+ *             MOE_DEVERR_TIMEOUT it has to be zeroed again).  Calls that may
+ *             overlap on the GPU need workspaces of their own.
  * D % 16 == 0, F % 16 == 0 (both % 128 with blockwise or MX scales), D and
  * F <= 32768, E <= 1024; every pointer but topk_ids and topk_w 16-byte
  * aligned.  MOE_ERR_UNSUPPORTED off sm_103.  The call can be captured into a
