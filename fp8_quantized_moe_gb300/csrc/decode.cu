@@ -60,8 +60,15 @@ namespace {
 
 __device__ unsigned int g_err;
 
-constexpr int kConvWarps = 3, kMmaWarps = 8;
-constexpr int kThreads = 32 * (1 + kConvWarps + kMmaWarps);
+constexpr int kMmaWarps = 8;  // contracting warps of a group
+constexpr int kMaxNT = 2;     // two groups: eight tokens times this a chunk (registers)
+// e2m1's stage holds twice the values of the other types' bytes and takes longer
+// to convert and to multiply than to arrive: two groups of contracting warps, on
+// alternate stages, and five warps that convert (16 tokens over 256 experts: 703 us
+// with one group and three warps, 689 with two groups, 651 with five warps, too).
+__host__ __device__ constexpr int groups_of(int wt) { return wt == 3 ? 2 : 1; }
+__host__ __device__ constexpr int conv_of(int wt) { return wt == 3 ? 5 : 3; }
+__host__ __device__ constexpr int threads_of(int wt) { return 32 * (1 + conv_of(wt) + kMmaWarps * groups_of(wt)); }
 constexpr int kRows = 128;              // weight rows of a unit
 constexpr int kBoxW = kRows * 128;      // weight bytes of a TMA box
 constexpr int kMaxStages = 10;
@@ -97,6 +104,7 @@ struct Params {
 
 struct Ctl {
   uint64_t full[kMaxStages], xraw[kMaxStages], xfull[kMaxStages], empty[kMaxStages];
+  uint64_t rfull[kMmaWarps], rempty[kMmaWarps];  // a warp's sums have been left for its partner, and taken
   int abort_flag, no_abort, err, nchunk, segs1, segs2;
   uint16_t pos[kMaxPairs];     // slot of pair i (pairs sorted by expert), 0xFFFF: not local
   uint16_t order[kMaxPairs];   // pair of slot s
@@ -111,6 +119,7 @@ struct Cfg {
   // Boxes (128 bytes of each weight row) a stage: two, so that a warp has two
   // boxes' loads in flight and half the hand-offs; one for e2m1, whose box
   // holds twice the values and whose activations take the space
+  static constexpr int GROUPS = groups_of(WT), CONV = conv_of(WT);
   static constexpr int BOXES = WT == kMx4 ? 1 : 2;
   static constexpr int BOX_K = WT == kMx4 ? 256 : 128;  // values of K in a box: a span of an activation row
   static constexpr int KE = BOXES * BOX_K;              // and in a stage
@@ -304,15 +313,15 @@ __device__ void build_chunks(const Params& p, Ctl* c, uint32_t* bits) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int R = p.T * p.k, W = (R + 31) / 32;
   uint32_t* first = bits + p.El * W;
-  for (int i = tid; i < p.El * W; i += kThreads) bits[i] = 0;
+  for (int i = tid; i < p.El * W; i += blockDim.x) bits[i] = 0;
   __syncthreads();
-  for (int i = tid; i < R; i += kThreads) {
+  for (int i = tid; i < R; i += blockDim.x) {
     const int e = local_expert(p, i);
     c->order[i] = static_cast<uint16_t>(e);
     if (e != 0xFFFF) atomicOr(bits + e * W + i / 32, 1u << (i & 31));
   }
   __syncthreads();
-  for (int e = tid; e < p.El; e += kThreads) {
+  for (int e = tid; e < p.El; e += blockDim.x) {
     int n = 0;
     for (int w = 0; w < W; ++w) n += __popc(bits[e * W + w]);
     c->num[e] = static_cast<uint16_t>(n);
@@ -336,7 +345,7 @@ __device__ void build_chunks(const Params& p, Ctl* c, uint32_t* bits) {
     }
   }
   __syncthreads();
-  for (int e = tid; e < p.El; e += kThreads) {
+  for (int e = tid; e < p.El; e += blockDim.x) {
     const int n = c->num[e], nc = (n + p.cap - 1) / p.cap, off = first[e] & 0xFFFF, c0 = first[e] >> 16;
     for (int j = 0; j < nc; ++j) {
       c->cexp[c0 + j] = static_cast<uint16_t>(e);
@@ -346,7 +355,7 @@ __device__ void build_chunks(const Params& p, Ctl* c, uint32_t* bits) {
       c->ccount[c0 + j] = static_cast<uint16_t>(nc);
     }
   }
-  for (int i = tid; i < R; i += kThreads) {
+  for (int i = tid; i < R; i += blockDim.x) {
     const int e = c->order[i];
     int at = 0xFFFF;
     if (e != 0xFFFF) {
@@ -356,7 +365,7 @@ __device__ void build_chunks(const Params& p, Ctl* c, uint32_t* bits) {
     c->pos[i] = static_cast<uint16_t>(at);
   }
   __syncthreads();
-  for (int i = tid; i < R; i += kThreads)  // (the experts in `order` are no longer needed)
+  for (int i = tid; i < R; i += blockDim.x)  // (the experts in `order` are no longer needed)
     if (c->pos[i] != 0xFFFF) c->order[c->pos[i]] = static_cast<uint16_t>(i);
 }
 
@@ -367,7 +376,7 @@ struct BoxAt {
 template <int WT, int PHASE, int NT>
 struct Box {
   using C = Cfg<WT, PHASE>;
-  static constexpr int DEPTH = WT == kMx4 ? (NT == 1 ? 4 : (NT == 2 ? 2 : 1)) : (NT <= 2 ? 4 : 2);
+  static constexpr int DEPTH = WT == kMx4 ? (NT == 1 ? 4 : 1) : (NT <= 2 ? 4 : 2);
   static constexpr int BW = WT == kMx4 ? 4 : 2;  // words of a chunk's activation fragment
   uint32_t r[4][4];
   uint32_t b[DEPTH][2][NT][BW];
@@ -602,7 +611,7 @@ struct Walk {
 };
 
 template <int WT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(WT), 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
                   const __grid_constant__ Params p) {
   using G = Cfg<WT, 2>;  // the ring's geometry: phase 2's, whose activations are the wider
@@ -618,10 +627,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t v_ring = s_ring + S * G::SCALE_BYTES;
   const uint32_t v_bytes = G::BOXES * cap * 4;
   Ctl* ctl = reinterpret_cast<Ctl*>(bp + (v_ring + S * v_bytes - base));
+  float* red = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ctl) + kCtlBytes);  // two groups: sums on their way
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.T * p.k;
 
   if (threadIdx.x == 0) {
+    for (int w = 0; w < kMmaWarps; ++w) {
+      mbar_init(smem_u32(&ctl->rfull[w]), 32);
+      mbar_init(smem_u32(&ctl->rempty[w]), 32);
+    }
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->xraw[s]), 32);
@@ -661,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (nchunk == 0) {  // no local expert was chosen at all
     const int64_t n = static_cast<int64_t>(p.T) * p.f[1].N;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * kThreads)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
       p.y[i] = 0;
     return;
   }
@@ -838,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_bounded(smem_u32(&ctl->full[j % S]), (j / S) & 1, &ctl->no_abort, kWaitLimitNs);
     }
     __syncwarp();
-  } else if (warp <= kConvWarps) {
+  } else if (warp <= G::CONV) {
     // ---------------------- activations to f16 and MX scale codes to bf16, in place
     uint32_t step = warp - 1;  // this warp's next stage of the CTA's,
     int left = warp - 1;       // and how many stages of the phase lie before it
@@ -895,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       Step q = walk.begin();
       left = walk.skip(q, left);
-      for (; !walk.done(q); step += kConvWarps, left = walk.skip(q, kConvWarps)) {
+      for (; !walk.done(q); step += G::CONV, left = walk.skip(q, G::CONV)) {
         const uint32_t s = step % S, ph = (step / S) & 1;
         if (!mbar_wait_bounded_warp(smem_u32(&ctl->xraw[s]), ph, abort_flag, kWaitLimitNs)) {
           timed_out = true;
@@ -950,7 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------- contraction
-    const int mw = warp - 1 - kConvWarps;
+    const int mw = (warp - 1 - G::CONV) % kMmaWarps, group = (warp - 1 - G::CONV) / kMmaWarps;
+    uint32_t handed = 0;  // two groups: units whose sums went from the second to the first
     const int g = lane >> 2, t4 = lane & 3;
     uint32_t s = 0, ph = 0;
     auto run = [&](auto phase_tag) {
@@ -1033,7 +1048,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        if constexpr (NT == 1) {
+        if constexpr (G::GROUPS == 2) {
+          // every other stage; the ring position moves on over the partner's, too
+          auto step_on = [&](uint32_t& a, uint32_t& b) {
+            if (++a == S) {
+              a = 0;
+              b ^= 1;
+            }
+          };
+          for (int j = first; j < last; ++j) {
+            if (((j - first) & 1) == group) {
+              wait();
+              if (timed_out) break;
+              Box<WT, PHASE, NT> b;
+              load(b, j);
+              work(b, j);
+            } else {
+              step_on(ls, lph);
+              step_on(s, ph);
+            }
+          }
+          if (!timed_out) {
+            float* r = red + mw * 32 * 4 * kMaxNT + lane;
+            if (group == 1) {
+              if (!mbar_wait_bounded_warp(smem_u32(&ctl->rempty[mw]), (handed & 1) ^ 1, abort_flag, kWaitLimitNs)) timed_out = true;
+              if (!timed_out) {
+#pragma unroll
+                for (int i = 0; i < 4 * NT; ++i) r[32 * i] = acc[i / 4][i % 4];
+                mbar_arrive(smem_u32(&ctl->rfull[mw]));
+              }
+            } else {
+              if (!mbar_wait_bounded_warp(smem_u32(&ctl->rfull[mw]), handed & 1, abort_flag, kWaitLimitNs)) timed_out = true;
+              if (!timed_out) {
+#pragma unroll
+                for (int i = 0; i < 4 * NT; ++i) acc[i / 4][i % 4] += r[32 * i];
+                mbar_arrive(smem_u32(&ctl->rempty[mw]));
+              }
+            }
+            if (timed_out) *abort_flag = 1;
+            ++handed;
+          }
+        } else if constexpr (NT == 1) {
           Box<WT, PHASE, NT> b0, b1;
           wait();
           if (!timed_out) load(b0, first);
@@ -1079,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             work(b, j);
           }
         }
-        if (timed_out) return;
+        if (timed_out || group > 0) return;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1111,8 +1166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (n <= 16)
           unit(std::integral_constant<int, 2>{}, q);
         else
-          unit(std::integral_constant<int, 4>{}, q);
-        if (PHASE == 2 && !timed_out) {
+          unit(std::integral_constant<int, G::GROUPS == 2 ? 2 : 4>{}, q);
+        if (PHASE == 2 && !timed_out && group == 0) {
           // the last unit (over all CTAs) that gets to these 16 columns sums their
           // pairs into y: each warp for the rows of its own, without its neighbours
           __threadfence();
@@ -1179,7 +1234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!timed_out) {
       __threadfence();
       __syncwarp();
-      if (lane == 0) atomicAdd(p.sync, 1u);
+      if (lane == 0 && group == 0) atomicAdd(p.sync, 1u);
       run(std::integral_constant<int, 2>{});
     }
     if (timed_out) {
@@ -1252,13 +1307,17 @@ moe_status launch(const void* w_in, const void* w_out, Params p, int sms, cudaSt
   if (!make_map(&tm1, w_in, f1.K / half, f1.N, 2ull * p.El, kRows / 2, 2) ||
       !make_map(&tm2, w_out, f2.K / half, f2.N, p.El, kRows, 1))
     return MOE_ERR_CUDA;
+  if (C::GROUPS == 2 && p.cap > 8 * kMaxNT) p.cap = 8 * kMaxNT;
   const size_t stage = C::STAGE_W + static_cast<size_t>(p.cap) * (C::PITCH + 4 * C::BOXES) + C::SCALE_BYTES;
-  const size_t fixed = 1024 + kCtlBytes;
+  const size_t red = C::GROUPS == 2 ? kMmaWarps * 32 * 4 * kMaxNT * 4 : 0;
+  const size_t fixed = 1024 + kCtlBytes + red;
   p.stages = static_cast<int>((kSmemLimit - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   // the ring holds the pair sort's bits and words first (at most 136 KB; the smallest ring has 160)
   const size_t sort = (static_cast<size_t>((p.T * p.k + 31) / 32) + 1) * p.El * 4;
-  MOE_HOST_CHECK(p.stages >= 2 && p.stages * stage >= sort, MOE_ERR_UNSUPPORTED);
+  // (a converting warp waits for one stage of its own at a time: a ring shorter
+  // than their number would let one mistake a slot's last round for its next)
+  MOE_HOST_CHECK(p.stages >= C::CONV && p.stages * stage >= sort, MOE_ERR_UNSUPPORTED);
   const size_t smem = fixed + p.stages * stage;
   // no more CTAs than units (a chunk a pair, all segments)
   const int64_t u = static_cast<int64_t>(p.T) * p.k * p.smax * (f1.nblock > f2.nblock ? f1.nblock : f2.nblock);
@@ -1269,7 +1328,7 @@ moe_status launch(const void* w_in, const void* w_out, Params p, int sms, cudaSt
   attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs at once: they wait for one another between the phases
   attr[0].val.cooperative = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(u < sms ? u : sms));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(WT));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
