@@ -20,6 +20,9 @@ gmm_mx_swiglu (or gmm_mx + swiglu_quant_mx) -> gmm_mx -> ragged_gather_reduce.
 The MXFP4 variant (MX4: the same blocks of e2m1 values, two a byte) runs
 quantize_sort_mx4 -> gmm_mx4 -> swiglu_quant_mx4 -> gmm_mx4 ->
 ragged_gather_reduce.
+
+Single decoding steps (up to 64 tokens) take ffn_decode: the whole expert FFN in
+one kernel, on bf16 activations and the same expert weights of any type.
 """
 
 from __future__ import annotations
@@ -835,7 +838,7 @@ class DecodeBuffers:
 
 def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.Tensor], W: ExpertWeights,
                buf: Optional[DecodeBuffers] = None, E: Optional[int] = None, group_offset: int = 0) -> torch.Tensor:
-    """The expert FFN of a decoding step, T <= 64 tokens, in two kernels; bf16 [T, D].
+    """The expert FFN of a decoding step, T <= 64 tokens, in one kernel; bf16 [T, D].
 
     x bf16 [T, D] and h are not quantised (with a few tokens the weights' bytes
     are the cost); W as prepare_weights or prepare_weights_w8 made it, in every

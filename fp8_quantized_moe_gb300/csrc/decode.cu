@@ -7,45 +7,53 @@
 // 3 D F bytes an expert (half for MXFP4), read once, against a few flops a
 // byte.  So nothing is quantised here, the weights stream through shared
 // memory at the rate of HBM, and everything else has to fit beside that
-// stream.  Two kernels, each one persistent CTA per SM:
-//   kernel 1 (PHASE 1)  h = silu(W0 x) * (W1 x) of every (token, expert) pair,
-//                       fp32, into the workspace;
-//   kernel 2 (PHASE 2)  o = Wo h of every pair, fp32, into the workspace; the
-//                       CTA that finishes the last expert of a block of output
-//                       columns sums the block's pairs with their weights, in
-//                       ascending j, and writes y.
-// Kernel 2 is launched while kernel 1 runs (programmatic launch): as a CTA of
-// kernel 1 leaves its SM, one of kernel 2 fills its ring with the first
-// weights of wo and only then waits for kernel 1's results.
+// stream.  One cooperative kernel, a persistent CTA per SM, in two phases:
+//   phase 1  h = silu(W0 x) * (W1 x) of every (token, expert) pair, fp32, into
+//            the workspace;
+//   phase 2  o = Wo h of every pair, fp32, into the workspace; the warp that
+//            finishes the last unit of 16 output columns sums their pairs with
+//            the choices' weights, in ascending j, and writes y.
+// Between them every CTA's h has to be there.  Weights do not wait for that: a
+// ring of wo's goes out while the last of phase 1 is at work.
 //
 // Every CTA first sorts the pairs by expert for itself (at most 1024): a
 // chunk is up to `cap` pairs of one expert.  A unit of work is one chunk, one
-// block of 128 weight rows (PHASE 1: 64 channels of wi_0 and the same of wi_1)
+// block of 128 weight rows (phase 1: 64 channels of wi_0 and the same of wi_1)
 // and one segment of K (more than one segment where there are too few blocks
 // to fill the SMs evenly; the segments' sums meet in fp32 in ascending order,
-// PHASE 1's where kernel 2 reads them).  Units run expert-major: the CTAs then
-// read a few experts at a time, long runs of memory each (with the blocks of
-// all experts side by side the same kernel streamed 1.1 TB/s instead of 3.9).
+// phase 1's where phase 2 reads them).  Units run expert-major: the CTAs then
+// read a few experts at a time, long runs of memory each.  (64 tokens over 256
+// experts: with the blocks of all experts side by side the bare stream ran at
+// 1.1 TB/s, expert-major at 3.9.)
 //
-// Roles: warp 0 moves the weights, one TMA box of 128 rows x 128 bytes a
-// stage.  One copy instruction a stage and no more: a stream of single 16 KB
-// boxes runs at 7.2 TB/s here, with four small bulk copies beside each (rows
-// of activations, scales) at 5.1.  So warps 1..3 fetch those themselves, each
-// every third stage, the next one's loads in flight while it waits: they
-// store the stage's weight scale words, and its activations as f16, each
-// (row, 128-byte span of the weights) scaled by the power of two that puts its
-// largest value in [2^14, 2^15): f16 then holds every bf16 value to within
-// 2^-39 of the span's largest, and h to 2^-12 relative (against 2^-9 of the
-// result's bf16).
-// Warps 4..11 contract, 16 weight rows each: ldmatrix brings 16 rows x 32
-// bytes of weights, one conversion makes two f16 weights (exact for e4m3, int8
-// and e2m1, NaN codes included), and mma.m16n8k16 multiplies them with eight
-// tokens.  The tensor core is nowhere near its limit, so the plain warp-wide
-// MMA serves: its operands come from registers, where the weights are
-// converted, and its M is only 16.  In PHASE 1 rows 0..7 of a fragment are
-// wi_0 channels and rows 8..15 the same wi_1 channels, so a thread holds both
-// factors of its h.  Span sums are scaled (weight block scale, activation span
-// scale) into fp32 accumulators.
+// Roles:
+//   warp 0       the weights, a TMA box of 128 rows x 128 bytes each (two a stage),
+//                and by cp.async the activations' rows and the scale words.  TMA
+//                for the boxes alone: single 16 KB boxes stream at 7.2 TB/s here,
+//                with four small bulk copies beside each at 5.1.
+//   CONV warps   turn a stage's activations into f16 in place, each (row, span of
+//                a box's K) scaled by the power of two that puts its largest value
+//                in [2^14, 2^15).  f16 then holds a bf16 value exactly down to
+//                2^-28 of the span's largest and to 2^-39 of that below, and h to
+//                2^-11 relative.  (The result's bf16 has 2^-8.)
+//   8 warps a group contract, 16 weight rows each: ldmatrix brings 16 rows x 32
+//                bytes, one conversion makes two f16 weights (exact for e4m3, int8
+//                and e2m1, NaN codes included), mma.m16n8k16 multiplies them with
+//                eight tokens.  At a few tokens the tensor core is far from its
+//                limit (16 % busy), so the warp-wide MMA serves: its operands come
+//                from registers, where the weights are converted anyway, and its M
+//                is only 16.  In phase 1 rows 0..7 of a fragment are wi_0 channels
+//                and rows 8..15 the same wi_1 channels, so a thread holds both
+//                factors of its h.  Span sums are scaled (weight block scale,
+//                activation span scale) into fp32 accumulators.
+//
+// Measured with warm code and cold weights, TB/s of weights and scales (of the
+// measured 6.79): 64 tokens, 218 experts of 7168 x 2048, blockwise e4m3 1.60 ms, 6.2;
+// 7 tokens, 8 experts of 4096 x 14336, int8 0.205 ms, 6.05; one token, 2 of these,
+// e4m3 62 us, 5.9 (about 8 us of it start, phase change and end); 16 tokens, 103
+// experts of 7168 x 2048, MXFP4 0.65 ms, 3.7 (bound by issue: 3200 warp instructions
+// a 16 KB box, ALU pipe 47 % and issue slots 52 % busy); one token of 8 experts of
+// 2048 x 768 17 us, where start, phase change and end are most of it.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets
 // its copies land and returns.

@@ -586,7 +586,7 @@ size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
  *   e = topk_ids[t, j], in ascending j.
  * With a few tokens the bytes of the chosen experts' weights are the cost, so
  * the activations stay bf16 and h fp32 (held as f16 with a scale for each 128
- * or 256 values while they are multiplied, relative error at most 2^-12); only
+ * or 256 values while they are multiplied, relative error at most 2^-11); only
  * the weights are quantised, and the sums are fp32.  (The prompt's path above
  * quantises x and h as well, so the two do not agree bit for bit.)  Results do
  * not depend on the order in which CTAs run.
