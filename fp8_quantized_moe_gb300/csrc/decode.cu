@@ -73,7 +73,7 @@ constexpr int kMaxNT = 2;     // two groups: eight tokens times this a chunk (re
 // e2m1's stage holds twice the values of the other types' bytes and takes longer
 // to convert and to multiply than to arrive: two groups of contracting warps, on
 // alternate stages, and five warps that convert (16 tokens over 256 experts: 703 us
-// with one group and three warps, 689 with two groups, 651 with five warps, too).
+// with one group and three warps, 689 with two groups, 656 with five warps, too).
 __host__ __device__ constexpr int groups_of(int wt) { return wt == 3 ? 2 : 1; }
 __host__ __device__ constexpr int conv_of(int wt) { return wt == 3 ? 5 : 3; }
 __host__ __device__ constexpr int threads_of(int wt) { return 32 * (1 + conv_of(wt) + kMmaWarps * groups_of(wt)); }
@@ -84,6 +84,7 @@ constexpr int kMaxSegs = 8;
 constexpr int kMaxPairs = 1024;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxDim = 32768;  // D and F
 constexpr int kSmemLimit = 232448;
 
 enum { kE4M3 = 0, kInt8 = 1, kMx8 = 2, kMx4 = 3 };
@@ -127,7 +128,6 @@ struct Cfg {
   // Boxes (128 bytes of each weight row) a stage: two, so that a warp has two
   // boxes' loads in flight and half the hand-offs; one for e2m1, whose box
   // holds twice the values and whose activations take the space
-  static constexpr int GROUPS = groups_of(WT), CONV = conv_of(WT);
   static constexpr int BOXES = WT == kMx4 ? 1 : 2;
   static constexpr int BOX_K = WT == kMx4 ? 256 : 128;  // values of K in a box: a span of an activation row
   static constexpr int KE = BOXES * BOX_K;              // and in a stage
@@ -739,7 +739,9 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
           p.sync[1] = 0;
         }
       }
-      return __shfl_sync(0xffffffffu, ok, 0) != 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      __syncwarp();  // what lane 0 has seen holds for every lane's copies
+      return ok != 0;
     };
     auto run = [&](auto phase_tag) {
       constexpr int PHASE = decltype(phase_tag)::value;
@@ -860,7 +862,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
           mbar_wait_bounded(smem_u32(&ctl->full[j % S]), (j / S) & 1, &ctl->no_abort, kWaitLimitNs);
     }
     __syncwarp();
-  } else if (warp <= G::CONV) {
+  } else if (warp <= conv_of(WT)) {
     // ---------------------- activations to f16 and MX scale codes to bf16, in place
     uint32_t step = warp - 1;  // this warp's next stage of the CTA's,
     int left = warp - 1;       // and how many stages of the phase lie before it
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
 
       Step q = walk.begin();
       left = walk.skip(q, left);
-      for (; !walk.done(q); step += G::CONV, left = walk.skip(q, G::CONV)) {
+      for (; !walk.done(q); step += conv_of(WT), left = walk.skip(q, conv_of(WT))) {
         const uint32_t s = step % S, ph = (step / S) & 1;
         if (!mbar_wait_bounded_warp(smem_u32(&ctl->xraw[s]), ph, abort_flag, kWaitLimitNs)) {
           timed_out = true;
@@ -960,6 +962,13 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
             store_span<PER>(w, at1, av + (b1 * cap + i1) * 4, lane);
           }
         }
+        // Two groups: each waits for every stage, the other's too (a slot's rounds
+        // alternate between them, and of a barrier only the last round's parity can
+        // be told), so one barrier stands for weights and activations
+        if (groups_of(WT) == 2 && !mbar_wait_bounded_warp(smem_u32(&ctl->full[s]), ph, abort_flag, kWaitLimitNs)) {
+          timed_out = true;
+          break;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->xfull[s]));
       }
@@ -972,7 +981,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
     }
   } else {
     // ----------------------------------------------------------- contraction
-    const int mw = (warp - 1 - G::CONV) % kMmaWarps, group = (warp - 1 - G::CONV) / kMmaWarps;
+    const int mw = (warp - 1 - conv_of(WT)) % kMmaWarps, group = (warp - 1 - conv_of(WT)) / kMmaWarps;
     uint32_t handed = 0;  // two groups: units whose sums went from the second to the first
     const int g = lane >> 2, t4 = lane & 3;
     uint32_t s = 0, ph = 0;
@@ -1020,7 +1029,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
         };
         auto wait = [&] {
           if (!mbar_wait_bounded_warp(smem_u32(&ctl->xfull[ls]), lph, abort_flag, kWaitLimitNs) ||
-              !mbar_wait_bounded_warp(smem_u32(&ctl->full[ls]), lph, abort_flag, kWaitLimitNs)) {
+              (groups_of(WT) == 1 && !mbar_wait_bounded_warp(smem_u32(&ctl->full[ls]), lph, abort_flag, kWaitLimitNs))) {
             timed_out = true;
             *abort_flag = 1;
           }
@@ -1056,7 +1065,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
             }
           }
         };
-        if constexpr (G::GROUPS == 2) {
+        if constexpr (groups_of(WT) == 2) {
           // every other stage; the ring position moves on over the partner's, too
           auto step_on = [&](uint32_t& a, uint32_t& b) {
             if (++a == S) {
@@ -1065,9 +1074,9 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
             }
           };
           for (int j = first; j < last; ++j) {
+            wait();
+            if (timed_out) break;
             if (((j - first) & 1) == group) {
-              wait();
-              if (timed_out) break;
               Box<WT, PHASE, NT> b;
               load(b, j);
               work(b, j);
@@ -1174,7 +1183,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
         else if (n <= 16)
           unit(std::integral_constant<int, 2>{}, q);
         else
-          unit(std::integral_constant<int, G::GROUPS == 2 ? 2 : 4>{}, q);
+          unit(std::integral_constant<int, groups_of(WT) == 2 ? 2 : 4>{}, q);
         if (PHASE == 2 && !timed_out && group == 0) {
           // the last unit (over all CTAs) that gets to these 16 columns sums their
           // pairs into y: each warp for the rows of its own, without its neighbours
@@ -1186,8 +1195,9 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
           const int d = q.blk * kRows + 16 * mw + 4 * (lane & 3);
           const bool all = done == static_cast<unsigned>(nchunk * walk.segs - 1);
           if (all && lane == 0) p.count[q.blk * kMmaWarps + mw] = 0;  // for the next call
-          if (all && d < f.N) {
+          if (all && d < f.N) {  // (N % 16 == 0: for all lanes or none)
             __threadfence();
+            __syncwarp();
             const int64_t seg_pitch = static_cast<int64_t>(slots) * f.N;
             for (int t = lane >> 2; t < p.T; t += 8) {
               float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1292,9 +1302,11 @@ int max_segs(int64_t R) {
 }
 
 // Workspace: the sync words and a counter for every 16 output columns (zero
-// between calls) | h fp32 [R, F] or partial a [segs][R, 2F] | o fp32
+// between calls; room for the largest D, so that calls of other shapes may
+// follow on the same workspace) | h fp32 [R, F] or partial a [segs][R, 2F] | o fp32
 // [segs][R, D], each part 256-byte aligned.
-int64_t count_bytes(int64_t D) { return align256((kSyncWords + blocks(D, kRows) * kMmaWarps) * 4); }
+constexpr int64_t kCountBytes = (kSyncWords + kMaxDim / kRows * kMmaWarps) * 4;
+static_assert(kCountBytes % 256 == 0, "h starts 256-byte aligned");
 int64_t h_bytes(int64_t R, int64_t F) {
   const int64_t s = max_segs(R);
   return align256(R * F * 4 * (s > 1 ? 2 * s : 1));
@@ -1303,7 +1315,7 @@ int64_t o_bytes(int64_t R, int64_t D) { return align256(R * D * 4 * max_segs(R))
 
 bool shape_ok(int64_t T, int k, int64_t D, int64_t F) {
   return T >= 0 && T <= kMaxTokens && k > 0 && k <= 32 && T * k <= kMaxPairs && D > 0 && F > 0 && D % 16 == 0 &&
-         F % 16 == 0 && D <= 32768 && F <= 32768;
+         F % 16 == 0 && D <= kMaxDim && F <= kMaxDim;
 }
 
 template <int WT>
@@ -1315,9 +1327,9 @@ moe_status launch(const void* w_in, const void* w_out, Params p, int sms, cudaSt
   if (!make_map(&tm1, w_in, f1.K / half, f1.N, 2ull * p.El, kRows / 2, 2) ||
       !make_map(&tm2, w_out, f2.K / half, f2.N, p.El, kRows, 1))
     return MOE_ERR_CUDA;
-  if (C::GROUPS == 2 && p.cap > 8 * kMaxNT) p.cap = 8 * kMaxNT;
+  if (groups_of(WT) == 2 && p.cap > 8 * kMaxNT) p.cap = 8 * kMaxNT;
   const size_t stage = C::STAGE_W + static_cast<size_t>(p.cap) * (C::PITCH + 4 * C::BOXES) + C::SCALE_BYTES;
-  const size_t red = C::GROUPS == 2 ? kMmaWarps * 32 * 4 * kMaxNT * 4 : 0;
+  const size_t red = groups_of(WT) == 2 ? kMmaWarps * 32 * 4 * kMaxNT * 4 : 0;
   const size_t fixed = 1024 + kCtlBytes + red;
   p.stages = static_cast<int>((kSmemLimit - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
@@ -1325,12 +1337,12 @@ moe_status launch(const void* w_in, const void* w_out, Params p, int sms, cudaSt
   const size_t sort = (static_cast<size_t>((p.T * p.k + 31) / 32) + 1) * p.El * 4;
   // (a converting warp waits for one stage of its own at a time: a ring shorter
   // than their number would let one mistake a slot's last round for its next)
-  MOE_HOST_CHECK(p.stages >= C::CONV && p.stages * stage >= sort, MOE_ERR_UNSUPPORTED);
+  MOE_HOST_CHECK(p.stages >= conv_of(WT) && p.stages * stage >= sort, MOE_ERR_UNSUPPORTED);
   const size_t smem = fixed + p.stages * stage;
   // no more CTAs than units (a chunk a pair, all segments)
   const int64_t u = static_cast<int64_t>(p.T) * p.k * p.smax * (f1.nblock > f2.nblock ? f1.nblock : f2.nblock);
   auto kernel = decode_kernel<WT>;
-  MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs at once: they wait for one another between the phases
@@ -1368,7 +1380,7 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_take_err
 
 extern "C" size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F) {
   if (!shape_ok(T, k, D, F)) return 0;
-  return static_cast<size_t>(count_bytes(D) + h_bytes(T * k, F) + o_bytes(T * k, D));
+  return static_cast<size_t>(kCountBytes + h_bytes(T * k, F) + o_bytes(T * k, D));
 }
 
 extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int k,
@@ -1401,8 +1413,8 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   cudaStream_t st = as_stream(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int64_t R = T * k;
-  float* h = reinterpret_cast<float*>(ws + count_bytes(D));
-  float* o = reinterpret_cast<float*>(ws + count_bytes(D) + h_bytes(R, F));
+  float* h = reinterpret_cast<float*>(ws + kCountBytes);
+  float* o = reinterpret_cast<float*>(ws + kCountBytes + h_bytes(R, F));
   const int ke = 256;  // values of K in a stage, of either width
   const int d = static_cast<int>(D), f = static_cast<int>(F);
   Params p{};

@@ -607,8 +607,9 @@ size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
  *   workspace moe_ffn_decode_workspace_bytes(T, k, D, F) bytes of device
  *             memory, 16-byte aligned, ZERO before its first use: it holds
  *             counters, which every call leaves at zero (after a call that set
- *             MOE_DEVERR_TIMEOUT it has to be zeroed again).  Calls that may
- *             overlap on the GPU need workspaces of their own.
+ *             MOE_DEVERR_TIMEOUT it has to be zeroed again).  Calls of several
+ *             shapes may follow on one that is large enough for each; calls that
+ *             may overlap on the GPU need workspaces of their own.
  * D % 16 == 0, F % 16 == 0 (both % 128 with blockwise or MX scales), D and
  * F <= 32768, E <= 1024; every pointer but topk_ids and topk_w 16-byte
  * aligned.  MOE_ERR_UNSUPPORTED off sm_103.  The call can be captured into a

@@ -265,6 +265,21 @@ def test_empty_and_shorter_batches():
     assert torch.equal(buf.y[5:], rest)  # rows behind the batch stay as they were
 
 
+def test_shapes_that_follow_on_one_workspace():
+    """A model whose layers differ: the counters of one shape may not lie in
+    another's sums."""
+    shapes = [(7, 3, 256, 1024, "mx4"), (2, 2, 2048, 128, "e4m3-block"), (64, 4, 128, 512, "mx8"), (1, 1, 8192, 256, "int8-channel")]
+    bufs = [moe.DecodeBuffers(T, D, 4, k, F, "cuda") for T, k, D, F, _ in shapes]
+    ws = torch.zeros(max(b.ws_bytes for b in bufs), dtype=torch.uint8, device="cuda")
+    for b in bufs:
+        b.ws, b.ws_bytes = ws, ws.numel()
+    for seed in (30, 31):
+        for (T, k, D, F, kind), buf in zip(shapes, bufs):
+            rng, x, ids, w = case(seed, T, k, 4, D)
+            W = make_weights(kind, 4, D, F, rng)
+            check(moe.ffn_decode(x, dev(ids), dev(w), W, buf), x, ids, w, W)
+
+
 def test_captured_and_replayed():
     """Two graphs on the same buffers, replayed in turn with new inputs."""
     rng, x, ids, w = case(12, 6, 2, 4, 256)
