@@ -29,7 +29,16 @@
 //
 // Tiles run expert-major, then N tile, then M tile: CTAs that run together
 // share an expert's weights.  A group's M tiles start at its first row; rows
-// past its end are computed and not stored.  Every wait is bounded; on expiry
+// past its end are computed and not stored.
+//
+// Measured: 16384 x 28672 x 4096 over 8 groups 841 us (4.6 PFLOP/s), 16384 x 1536
+// x 2048 over 128 groups 51 us (5.5 TB/s), 32 of 64 groups of 12000 x 4096 x 7168
+// 135 us (4.6 TB/s).  The large one is bound by the MMA issue order: its MMAs
+// take about 900 clocks a stage when the scale copies are left out, the six
+// copies the rest of 1145.  (Pairs of CTAs, each with half of B, read a third
+// less through shared memory and L2 and took 898 us: neither is the bound.)
+//
+// Every wait is bounded; on expiry
 // the kernel raises MOE_DEVERR_TIMEOUT, lets what it issued finish and returns.
 #include <cudaTypedefs.h>
 
@@ -274,15 +283,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sft = tmem + kSfCol0 + s * kSfCols;  // per K block: A's 4 columns, then B's 8
           const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kABytes);
           const int nh = min(2, p.nkb - 2 * kb);  // 128-wide K blocks of this stage
-          for (int h = 0; h < nh; ++h) {
-            const uint32_t sfa = sft + 12 * h, sfb = sfa + 4;
-            tmem_cp_32x128b_warpx4(sfa, smem_desc_plain(sfa_sm + kAtom * h));
-            tmem_cp_32x128b_warpx4(sfb, smem_desc_plain(sfb_sm + 2 * kAtom * h));
-            tmem_cp_32x128b_warpx4(sfb + 4, smem_desc_plain(sfb_sm + 2 * kAtom * h + kAtom));
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              mma_mx4(tmem, da + 4 * h + 2 * half, db + 4 * h + 2 * half, idesc_mx4(kBM, kBN, 2 * half), sfa, sfb,
-                      kb > 0 || h > 0 || half > 0);
+          auto copy = [&](int h, int c) {  // atom c of K block h: A's, B's two
+            tmem_cp_32x128b_warpx4(sft + 12 * h + 4 * c, smem_desc_plain(c == 0 ? sfa_sm + kAtom * h
+                                                                                : sfb_sm + 2 * kAtom * h + kAtom * (c - 1)));
+          };
+          auto multiply = [&](int h, int half) {
+            mma_mx4(tmem, da + 4 * h + 2 * half, db + 4 * h + 2 * half, idesc_mx4(kBM, kBN, 2 * half), sft + 12 * h,
+                    sft + 12 * h + 4, kb > 0 || h > 0 || half > 0);
+          };
+          // The second block's copies between the first one's products: a product
+          // that follows its copies directly waits for them (907 us with each
+          // block's copies before its two products, 841 this way; all six first,
+          // or the next stage's ahead of this one's products, are slower still)
+          copy(0, 0);
+          copy(0, 1);
+          copy(0, 2);
+          multiply(0, 0);
+          if (nh > 1) {
+            copy(1, 0);
+            copy(1, 1);
+          }
+          multiply(0, 1);
+          if (nh > 1) {
+            copy(1, 2);
+            multiply(1, 0);
+            multiply(1, 1);
           }
           mma_commit(smem_u32(&ctl->empty[s]));
           mma_commit(smem_u32(&ctl->sfempty[q]));
