@@ -48,9 +48,9 @@
 //                activation span scale) into fp32 accumulators.
 //
 // Measured with warm code and cold weights, TB/s of weights and scales (of the
-// measured 6.79): 64 tokens, 218 experts of 7168 x 2048, blockwise e4m3 1.60 ms, 6.2;
-// 7 tokens, 8 experts of 4096 x 14336, int8 0.205 ms, 6.05; one token, 2 of these,
-// e4m3 62 us, 5.9 (about 8 us of it start, phase change and end); 16 tokens, 103
+// measured 6.79): 64 tokens, 218 experts of 7168 x 2048, blockwise e4m3 1.57 ms, 6.3;
+// 7 tokens, 8 experts of 4096 x 14336, int8 0.203 ms, 6.1; one token, 2 of these,
+// e4m3 61 us, 6.0 (about 8 us of it start, phase change and end); 16 tokens, 103
 // experts of 7168 x 2048, MXFP4 0.65 ms, 3.7 (bound by issue: 3200 warp instructions
 // a 16 KB box, ALU pipe 47 % and issue slots 52 % busy); one token of 8 experts of
 // 2048 x 768 17 us, where start, phase change and end are most of it.
