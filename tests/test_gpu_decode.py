@@ -265,6 +265,29 @@ def test_empty_and_shorter_batches():
     assert torch.equal(buf.y[5:], rest)  # rows behind the batch stay as they were
 
 
+@pytest.mark.parametrize("kind", ["e4m3-block", "int8-channel", "mx8", "mx4"])
+def test_most_pairs_and_experts(kind):
+    """1024 pairs over 1024 experts: full tables, and units of a single stage."""
+    rng, x, ids, w = case(40, 64, 16, 1024, 128)
+    W = make_weights(kind, 1024, 128, 128, rng)
+    check(moe.ffn_decode(x, dev(ids), dev(w), W), x, ids, w, W)
+
+
+@pytest.mark.parametrize("kind", ["e4m3-channel", "mx8", "mx4"])
+@pytest.mark.parametrize("D,F", [(1280, 640), (256, 1792)])
+def test_a_hundred_calls_alike(kind, D, F):
+    """Odd numbers of stages: the ring's rounds fall on every slot and group."""
+    rng, x, ids, w = case(41, 16, 8, 64, D)
+    W = make_weights(kind, 64, D, F, rng)
+    idd, wd, buf = dev(ids), dev(w), moe.DecodeBuffers(16, D, 64, 8, F, "cuda")
+    first = moe.ffn_decode(x, idd, wd, W, buf).clone()
+    check(first, x, ids, w, W)
+    differs = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(100):
+        differs |= (moe.ffn_decode(x, idd, wd, W, buf) != first).any()
+    assert not differs.item() and moe.device_error() == 0
+
+
 def test_shapes_that_follow_on_one_workspace():
     """A model whose layers differ: the counters of one shape may not lie in
     another's sums."""
