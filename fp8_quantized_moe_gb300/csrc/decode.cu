@@ -1378,9 +1378,17 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_take_err
   return e;
 }
 
+// The most that any batch of up to T tokens needs: a few pairs' sums of segments
+// can take more than more pairs' whole sums (h: 1024 F bytes for 16 pairs in eight
+// segments, 260 F for 65 pairs in one).
 extern "C" size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F) {
   if (!shape_ok(T, k, D, F)) return 0;
-  return static_cast<size_t>(kCountBytes + h_bytes(T * k, F) + o_bytes(T * k, D));
+  int64_t most = 0;
+  for (int64_t t = 1; t <= T; ++t) {
+    const int64_t b = h_bytes(t * k, F) + o_bytes(t * k, D);
+    most = b > most ? b : most;
+  }
+  return static_cast<size_t>(kCountBytes + most);
 }
 
 extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int k,

@@ -607,7 +607,8 @@ size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
  *   workspace moe_ffn_decode_workspace_bytes(T, k, D, F) bytes of device
  *             memory, 16-byte aligned, ZERO before its first use: it holds
  *             counters, which every call leaves at zero (after a call that set
- *             MOE_DEVERR_TIMEOUT it has to be zeroed again).  Calls of several
+ *             MOE_DEVERR_TIMEOUT it has to be zeroed again).  One that was made
+ *             for T tokens serves every smaller batch, and calls of several
  *             shapes may follow on one that is large enough for each; calls that
  *             may overlap on the GPU need workspaces of their own.
  * D % 16 == 0, F % 16 == 0 (both % 128 with blockwise or MX scales), D and
@@ -627,9 +628,10 @@ moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const floa
                           moe_scale_mode out_mode, uint16_t* y, void* workspace, size_t workspace_bytes,
                           moe_stream_t stream);
 
-/* Bytes of moe_ffn_decode's workspace (0 for a shape that the call refuses):
- * 4 T k (D + F) and a little, or, for fewer than 128 pairs, about 512 (D + 2 F)
- * at most (sums of segments of K). */
+/* Bytes of moe_ffn_decode's workspace for batches of up to T tokens (0 for a
+ * shape that the call refuses; never less for a larger T): 4 T k (D + F) and a
+ * little, or, where that is more, what a smaller batch's sums of segments of K
+ * take, about 512 (D + 2 F) at most. */
 size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, int64_t F);
 
 #ifdef __cplusplus

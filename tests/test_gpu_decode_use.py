@@ -1,0 +1,24 @@
+"""Decoding steps as a server runs them: batches that grow and shrink on the same
+buffers.  Values against the float64 oracle, in the bound that
+test_gpu_decode.py derives."""
+
+import pytest
+
+from tests.gpu_helpers import dev
+from tests.test_gpu_decode import case, check, make_weights
+
+pytestmark = pytest.mark.gpu
+
+moe = pytest.importorskip("fp8_quantized_moe_gb300")
+
+
+@pytest.mark.parametrize("kind", ["e4m3-block", "mx4"])
+@pytest.mark.parametrize("T,k,steps", [(64, 2, (64, 33, 32, 16, 8, 5, 1)), (16, 8, (16, 8, 7, 2, 1)), (63, 1, (63, 32, 16, 1))])
+def test_a_batch_that_drains(kind, T, k, steps):
+    rng, x, ids, w = case(T, T, k, 12, 512)
+    W = make_weights(kind, 12, 512, 256, rng)
+    buf = moe.DecodeBuffers(T, 512, 12, k, 256, "cuda")
+    for n in steps + steps[::-1]:
+        y = moe.ffn_decode(x[:n], dev(ids[:n]), dev(w[:n]), W, buf)
+        assert y.data_ptr() == buf.y.data_ptr()
+        check(y, x[:n], ids[:n], w[:n], W)
