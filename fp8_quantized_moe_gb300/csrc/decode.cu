@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->xraw[s]), 32);
       mbar_init(smem_u32(&ctl->xfull[s]), 1);
-      mbar_init(smem_u32(&ctl->empty[s]), kMmaWarps);
+      mbar_init(smem_u32(&ctl->empty[s]), kMmaWarps * groups_of(WT));
     }
     ctl->abort_flag = 0;
     ctl->no_abort = 0;
@@ -962,9 +962,8 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
             store_span<PER>(w, at1, av + (b1 * cap + i1) * 4, lane);
           }
         }
-        // Two groups: each waits for every stage, the other's too (a slot's rounds
-        // alternate between them, and of a barrier only the last round's parity can
-        // be told), so one barrier stands for weights and activations
+        // Two groups: each waits for every stage, the other's too, so one barrier
+        // stands for weights and activations
         if (groups_of(WT) == 2 && !mbar_wait_bounded_warp(smem_u32(&ctl->full[s]), ph, abort_flag, kWaitLimitNs)) {
           timed_out = true;
           break;
@@ -1066,7 +1065,10 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
           }
         };
         if constexpr (groups_of(WT) == 2) {
-          // every other stage; the ring position moves on over the partner's, too
+          // Every other stage; the ring position moves on over the partner's, too.  A
+          // stage is given back by both groups: a barrier tells only the parity of
+          // its last round, so the slot may not be filled again before this warp
+          // has seen the partner's round.
           auto step_on = [&](uint32_t& a, uint32_t& b) {
             if (++a == S) {
               a = 0;
@@ -1081,6 +1083,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
               load(b, j);
               work(b, j);
             } else {
+              if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
               step_on(ls, lph);
               step_on(s, ph);
             }

@@ -3,6 +3,7 @@ buffers.  Values against the float64 oracle, in the bound that
 test_gpu_decode.py derives."""
 
 import pytest
+import torch
 
 from tests.gpu_helpers import dev
 from tests.test_gpu_decode import case, check, make_weights
@@ -22,3 +23,19 @@ def test_a_batch_that_drains(kind, T, k, steps):
         y = moe.ffn_decode(x[:n], dev(ids[:n]), dev(w[:n]), W, buf)
         assert y.data_ptr() == buf.y.data_ptr()
         check(y, x[:n], ids[:n], w[:n], W)
+
+
+@pytest.mark.parametrize("T,k,E", [(8, 2, 8), (16, 4, 8), (64, 8, 16)])
+@pytest.mark.parametrize("D,F", [(256, 768), (1536, 128), (2304, 1280)])
+def test_mx4_ring_goes_round(T, k, E, D, F):
+    """Two groups on alternate stages: rings of both chunk widths, units of one
+    stage, of odd and of even numbers, one after the other; 200 calls alike."""
+    rng, x, ids, w = case(T + D, T, k, E, D)
+    W = make_weights("mx4", E, D, F, rng)
+    idd, wd, buf = dev(ids), dev(w), moe.DecodeBuffers(T, D, E, k, F, "cuda")
+    first = moe.ffn_decode(x, idd, wd, W, buf).clone()
+    check(first, x, ids, w, W)
+    differs = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(200):
+        differs |= (moe.ffn_decode(x, idd, wd, W, buf) != first).any()
+    assert not differs.item() and moe.device_error() == 0
