@@ -43,6 +43,7 @@ SIGNATURES = {
     "moe_ragged_sort_noalloc": ([P, i64, i32, i32, P, P, i64, i32, P, P, P, P, P, P, P], i32),
     "moe_router_topk": ([P, P, i64, i64, i32, i32, P, P, P, P], i32),
     "moe_test_stall_epilogue": ([ctypes.c_uint64], None),
+    "moe_test_stall_consumers": ([ctypes.c_uint64], None),
     "moe_router_backward_workspace_bytes": ([i64, i64, i32], sz),
     "moe_router_backward": ([P, P, P, P, P, P, P, i64, i64, i32, i32, P, P, P, P, P, sz, P], i32),
     "moe_quantize_rows_mx": ([P, i64, i64, P, P, P], i32),

@@ -1,4 +1,6 @@
 // Library-wide entry points: status strings and the device error word.
+#include <atomic>
+
 #include "common.cuh"
 
 extern "C" cudaError_t moe_detail_take_error_quantize(unsigned int* out);
@@ -7,6 +9,11 @@ extern "C" cudaError_t moe_detail_take_error_combine(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_gmm(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_gmm_mx4(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_decode(unsigned int* out);
+
+// test hook: 0, or the wait limit in ns
+static std::atomic<uint64_t> g_stall_ns{0};
+extern "C" void moe_test_stall_consumers(uint64_t limit_ns) { g_stall_ns.store(limit_ns); }
+extern "C" __attribute__((visibility("hidden"))) uint64_t moe_detail_stall_ns() { return g_stall_ns.load(); }
 
 extern "C" const char* moe_status_string(moe_status s) {
   switch (s) {

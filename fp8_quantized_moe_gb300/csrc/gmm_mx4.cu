@@ -79,11 +79,13 @@ struct Params {
   const uint32_t* lhs_sf;
   const uint32_t* rhs_sf;
   uint16_t* out;
+  uint64_t stall_ns;  // test hook (moe_test_stall_consumers): 0, or the wait limit in ns
 };
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages], sffull[kSfSlots], sfempty[kSfSlots];
   uint64_t tfull, tempty, drain;
+  uint64_t never;  // test hook: a barrier that nothing arrives on
   uint32_t tmem_base;
   int abort_flag, no_abort, err, total;
   int start[kMaxGroups + 1], prefix[kMaxGroups + 1];  // local groups' first rows and tiles; the last: their ends
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl->tfull), 1);
     mbar_init(smem_u32(&ctl->tempty), kEpiWarps);
     mbar_init(smem_u32(&ctl->drain), 1);
+    mbar_init(smem_u32(&ctl->never), 1);
     ctl->abort_flag = 0;
     ctl->no_abort = 0;
     fence_mbar_init();
@@ -255,10 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (timed_out) {
         *abort_flag = 1;
         ctl->err = 2;
-        // loads already issued land before the CTA can exit
-        for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-          mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
       }
+      // The last loads land before the CTA can exit, whichever role's wait ran out
+      // (this one may have issued them all and be done).
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+        mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -369,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + half * (kBN / 2);
     uint8_t* stg = stg_base + (warp - kCtrlWarps) * kStgBytes;
     uint32_t acc = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++acc) {
+    if (p.stall_ns && !mbar_wait_bounded_warp(smem_u32(&ctl->never), 0, abort_flag, p.stall_ns)) timed_out = true;
+    for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x, ++acc) {
       const Tile tl = get_tile(p, ctl, t);
       if (!mbar_wait_bounded_warp(smem_u32(&ctl->tfull), acc & 1, abort_flag, kWaitLimitNs)) {
         timed_out = true;
@@ -500,6 +505,8 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_take_err
   return e;
 }
 
+extern "C" __attribute__((visibility("hidden"))) uint64_t moe_detail_stall_ns();
+
 extern "C" moe_status gmm_fp4_mx(const uint8_t* lhs_q, const uint8_t* lhs_sf, const uint8_t* rhs_q,
                                  const uint8_t* rhs_sf, const int32_t* group_sizes, int E, int group_offset,
                                  int E_local, int64_t M, int64_t K, int64_t N, uint16_t* out, moe_stream_t stream) {
@@ -532,7 +539,7 @@ extern "C" moe_status gmm_fp4_mx(const uint8_t* lhs_q, const uint8_t* lhs_sf, co
   if (!make_map(&B, rhs_q, K / 2, static_cast<uint64_t>(E_local) * N, true)) return MOE_ERR_CUDA;
   Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(N), static_cast<int>(K / 128),
            static_cast<int>(ntiles), reinterpret_cast<const uint32_t*>(lhs_sf),
-           reinterpret_cast<const uint32_t*>(rhs_sf), out};
+           reinterpret_cast<const uint32_t*>(rhs_sf), out, moe_detail_stall_ns()};
   MOE_CUDA_TRY(cudaFuncSetAttribute(gmm_mx4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(kSmem)));
   gmm_mx4_kernel<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, kSmem, st>>>(A, B, p);

@@ -101,6 +101,9 @@ int moe_num_sms(void);
  * Process-wide; not for production use. */
 void moe_test_stall_epilogue(uint64_t limit_ns);
 
+/* The same hook for gmm_fp4_mx (its epilogue warps). */
+void moe_test_stall_consumers(uint64_t limit_ns);
+
 /* ------------------------------------------------------------------------
  * Step 1 -- activation quantisation ([Q-EP] description: quantise before the
  * all-gather and the activation sort; [Q-GMM] review reply: fp8_dynamic uses
