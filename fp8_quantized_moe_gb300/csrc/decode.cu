@@ -109,11 +109,13 @@ struct Params {
   int T, k, E, g0, El;
   int cap, stages;  // pairs a chunk; ring stages
   int smax;         // segments of K at most
+  uint64_t stall_ns;  // test hook (moe_test_stall_consumers): 0, or the wait limit in ns
 };
 
 struct Ctl {
   uint64_t full[kMaxStages], xraw[kMaxStages], xfull[kMaxStages], empty[kMaxStages];
   uint64_t rfull[kMmaWarps], rempty[kMmaWarps];  // a warp's sums have been left for its partner, and taken
+  uint64_t never;  // test hook: a barrier that nothing arrives on
   int abort_flag, no_abort, err, nchunk, segs1, segs2;
   uint16_t pos[kMaxPairs];     // slot of pair i (pairs sorted by expert), 0xFFFF: not local
   uint16_t order[kMaxPairs];   // pair of slot s
@@ -644,6 +646,7 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
       mbar_init(smem_u32(&ctl->rfull[w]), 32);
       mbar_init(smem_u32(&ctl->rempty[w]), 32);
     }
+    mbar_init(smem_u32(&ctl->never), 1);
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->xraw[s]), 32);
@@ -855,12 +858,13 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
     if (timed_out) {
       *abort_flag = 1;
       ctl->err = 2;
-      // copies in flight land before the CTA exits
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (lane == 0)
-        for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
-          mbar_wait_bounded(smem_u32(&ctl->full[j % S]), (j / S) & 1, &ctl->no_abort, kWaitLimitNs);
     }
+    // Copies in flight land before the CTA exits, whichever warp's wait ran out
+    // (this one may have issued them all and be done).
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (lane == 0)
+      for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
+        mbar_wait_bounded(smem_u32(&ctl->full[j % S]), (j / S) & 1, &ctl->no_abort, kWaitLimitNs);
     __syncwarp();
   } else if (warp <= conv_of(WT)) {
     // ---------------------- activations to f16 and MX scale codes to bf16, in place
@@ -1251,7 +1255,11 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
         if (!walk.done(q)) walk.open(q);
       }
     };
-    run(std::integral_constant<int, 1>{});
+    if (p.stall_ns && !mbar_wait_bounded_warp(smem_u32(&ctl->never), 0, abort_flag, p.stall_ns)) {
+      timed_out = true;
+      *abort_flag = 1;
+    }
+    if (!timed_out) run(std::integral_constant<int, 1>{});
     if (!timed_out) {
       __threadfence();
       __syncwarp();
@@ -1394,6 +1402,8 @@ extern "C" size_t moe_ffn_decode_workspace_bytes(int64_t T, int k, int64_t D, in
   return static_cast<size_t>(kCountBytes + most);
 }
 
+extern "C" __attribute__((visibility("hidden"))) uint64_t moe_detail_stall_ns();
+
 extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int k,
                                      int E, int group_offset, int E_local, int64_t D, int64_t F,
                                      moe_weight_type type, const void* w_in, const void* s_in, moe_scale_mode in_mode,
@@ -1450,6 +1460,7 @@ extern "C" moe_status moe_ffn_decode(const uint16_t* x, const int32_t* topk_ids,
   p.cap = T <= 8 || R <= 2 * static_cast<int64_t>(E_local) ? 8
                                                            : (T <= 16 || R <= 6 * static_cast<int64_t>(E_local) ? 16 : 32);
   p.smax = max_segs(R);
+  p.stall_ns = moe_detail_stall_ns();
   switch (type) {
     case MOE_WEIGHT_E4M3: return launch<kE4M3>(w_in, w_out, p, sms, st);
     case MOE_WEIGHT_INT8: return launch<kInt8>(w_in, w_out, p, sms, st);

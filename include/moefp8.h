@@ -101,7 +101,8 @@ int moe_num_sms(void);
  * Process-wide; not for production use. */
 void moe_test_stall_epilogue(uint64_t limit_ns);
 
-/* The same hook for gmm_fp4_mx (its epilogue warps). */
+/* The same hook for gmm_fp4_mx (its epilogue warps) and moe_ffn_decode (its
+ * contracting warps). */
 void moe_test_stall_consumers(uint64_t limit_ns);
 
 /* ------------------------------------------------------------------------

@@ -1,7 +1,7 @@
-"""The failure path of the MXFP4 product: its consumers are held on a barrier
-that nothing arrives on (a test hook, 200 us), so that their wait runs out.  The
-kernel stops, lets its copies and products finish, returns and reports
-MOE_DEVERR_TIMEOUT; the context stays usable."""
+"""The failure paths of the MXFP4 product and of the decoding step: the warps that
+consume are held on a barrier that nothing arrives on (a test hook, 200 us), so
+that their wait runs out.  The kernel stops, lets its copies and products finish,
+returns and reports MOE_DEVERR_TIMEOUT; the context stays usable."""
 
 import contextlib
 
@@ -9,6 +9,7 @@ import pytest
 
 from tests.gpu_helpers import dev
 from tests.mx4_helpers import pack, sf_kmajor
+from tests.test_gpu_decode import KINDS, case, check, make_weights
 from tests.test_gpu_mx4 import assert_product, mx4_case
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +44,20 @@ def test_product(M, K, N, E):
     out = moe.gmm_mx4(*args)
     assert moe.device_error() == 0
     assert_product(out, sizes, a, asf, w, wsf)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,k,E,D,F", [
+    (1, 1, 2, 128, 128),     # a CTA's weights of both phases fit the ring
+    (16, 4, 8, 1024, 1280),  # the producer waits for its ring
+])
+def test_decoding_step(kind, T, k, E, D, F):
+    rng, x, ids, w = case(T + D, T, k, E, D)
+    W = make_weights(kind, E, D, F, rng)
+    buf = moe.DecodeBuffers(T, D, E, k, F, "cuda")
+    idd, wd = dev(ids), dev(w)
+    with consumers_held():
+        moe.ffn_decode(x, idd, wd, W, buf)
+        assert moe.device_error() == TIMEOUT
+    buf.ws.zero_()  # the counters of a call that did not end
+    check(moe.ffn_decode(x, idd, wd, W, buf), x, ids, w, W)
