@@ -824,7 +824,10 @@ def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W
 
 
 class DecodeBuffers:
-    """The output and the workspace of ffn_decode for up to T tokens, allocated once."""
+    """The output and the workspace of ffn_decode for up to T tokens, allocated once.
+
+    After a step that timed out (device_error() & 0x4) the workspace holds what
+    that step left, and every step on it reports the error until reset()."""
 
     def __init__(self, T, D, E, k, F, device):
         self.T, self.D, self.E, self.k, self.F = T, D, E, k, F
@@ -834,6 +837,10 @@ class DecodeBuffers:
         self.y = torch.empty(T, D, dtype=torch.bfloat16, device=device)
         self.ws = torch.zeros(n, dtype=torch.uint8, device=device)  # (its counters have to start at zero)
         self.ws_bytes = n
+
+    def reset(self):
+        """Zero the workspace, on the current stream, after a step that timed out."""
+        self.ws.zero_()
 
 
 def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.Tensor], W: ExpertWeights,

@@ -56,7 +56,8 @@
 // 2048 x 768 17 us, where start, phase change and end are most of it.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets
-// its copies land and returns.
+// its copies land, marks the workspace, whose counters it leaves as they are, and
+// returns.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -86,6 +87,9 @@ constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxDim = 32768;  // D and F
 constexpr int kSmemLimit = 232448;
+// Set in the workspace's first counter by a call that timed out: the counters
+// then hold what it left, and the calls after it stop instead of counting on.
+constexpr unsigned int kBroken = 0x80000000u;
 
 enum { kE4M3 = 0, kInt8 = 1, kMx8 = 2, kMx4 = 3 };
 enum { kScaleChannel = 0, kScaleBlock = 1, kScaleTensor = 2, kScaleMx = 3 };
@@ -104,7 +108,7 @@ struct Params {
   const int32_t* ids;
   const float* topk_w;
   uint16_t* y;
-  unsigned int* sync;   // [0] warps done with phase 1, [1] CTAs that have seen all of them; zero between calls
+  unsigned int* sync;   // [0] warps done with phase 1 (or kBroken), [1] CTAs that have seen all of them; zero between calls
   unsigned int* count;  // finished units of every 16 output columns; zero between calls
   int T, k, E, g0, El;
   int cap, stages;  // pairs a chunk; ring stages
@@ -731,14 +735,14 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
       if (lane == 0) {
         const unsigned int all = gridDim.x * kMmaWarps;
         const uint64_t t0 = globaltimer_ns();
-        while (load_acquire(p.sync) != all) {
-          if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) {
+        for (unsigned int v; (v = load_acquire(p.sync)) != all;) {
+          if ((v & kBroken) || *abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) {
             ok = 0;
             break;
           }
         }
         if (ok && atomicAdd(p.sync + 1, 1u) == gridDim.x - 1) {
-          p.sync[0] = 0;
+          atomicSub(p.sync, all);  // (kBroken stays, if another CTA has set it since)
           p.sync[1] = 0;
         }
       }
@@ -1272,7 +1276,10 @@ __global__ void __launch_bounds__(threads_of(WT), 1)
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0 && ctl->err) raise_error(&g_err, MOE_DEVERR_TIMEOUT);
+  if (threadIdx.x == 0 && ctl->err) {
+    atomicOr(p.sync, kBroken);
+    raise_error(&g_err, MOE_DEVERR_TIMEOUT);
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

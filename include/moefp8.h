@@ -611,7 +611,8 @@ size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
  *   workspace moe_ffn_decode_workspace_bytes(T, k, D, F) bytes of device
  *             memory, 16-byte aligned, ZERO before its first use: it holds
  *             counters, which every call leaves at zero (after a call that set
- *             MOE_DEVERR_TIMEOUT it has to be zeroed again).  One that was made
+ *             MOE_DEVERR_TIMEOUT it has to be zeroed again; until then calls on
+ *             it set the error anew and leave y undefined).  One that was made
  *             for T tokens serves every smaller batch, and calls of several
  *             shapes may follow on one that is large enough for each; calls that
  *             may overlap on the GPU need workspaces of their own.

@@ -59,5 +59,25 @@ def test_decoding_step(kind, T, k, E, D, F):
     with consumers_held():
         moe.ffn_decode(x, idd, wd, W, buf)
         assert moe.device_error() == TIMEOUT
-    buf.ws.zero_()  # the counters of a call that did not end
+    buf.reset()
     check(moe.ffn_decode(x, idd, wd, W, buf), x, ids, w, W)
+
+
+@pytest.mark.parametrize("kind", ["e4m3-block", "mx4"])
+def test_steps_after_one_that_timed_out(kind):
+    """What it left in the workspace gives no wrong result in silence: steps report
+    the error until the buffers are reset; steps on other buffers go on."""
+    rng, x, ids, w = case(3, 9, 4, 8, 512)
+    W = make_weights(kind, 8, 512, 256, rng)
+    buf, other = (moe.DecodeBuffers(9, 512, 8, 4, 256, "cuda") for _ in range(2))
+    idd, wd = dev(ids), dev(w)
+    with consumers_held():
+        moe.ffn_decode(x, idd, wd, W, buf)
+        assert moe.device_error() == TIMEOUT
+    for n in (9, 2):
+        moe.ffn_decode(x[:n], idd[:n], wd[:n], W, buf)
+        assert moe.device_error() == TIMEOUT
+    check(moe.ffn_decode(x, idd, wd, W, other), x, ids, w, W)
+    buf.reset()
+    for _ in range(2):
+        check(moe.ffn_decode(x, idd, wd, W, buf), x, ids, w, W)
