@@ -826,10 +826,13 @@ def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W
 class DecodeBuffers:
     """The output and the workspace of ffn_decode for up to T tokens, allocated once.
 
+    They may be used on any stream at once: the constructor waits until the
+    workspace is zero (not while the current stream is captured, and not with
+    `settle` false; it is then zero in the current stream's order).
     After a step that timed out (device_error() & 0x4) the workspace holds what
     that step left, and every step on it reports the error until reset()."""
 
-    def __init__(self, T, D, E, k, F, device):
+    def __init__(self, T, D, E, k, F, device, settle: bool = True):
         self.T, self.D, self.E, self.k, self.F = T, D, E, k, F
         n = int(lib().moe_ffn_decode_workspace_bytes(T, k, D, F))
         if not n:
@@ -837,9 +840,13 @@ class DecodeBuffers:
         self.y = torch.empty(T, D, dtype=torch.bfloat16, device=device)
         self.ws = torch.zeros(n, dtype=torch.uint8, device=device)  # (its counters have to start at zero)
         self.ws_bytes = n
+        if settle and self.ws.is_cuda:
+            with torch.cuda.device(self.ws.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
 
     def reset(self):
-        """Zero the workspace, on the current stream, after a step that timed out."""
+        """Zero the workspace, in the current stream's order, after a step that timed out."""
         self.ws.zero_()
 
 
@@ -853,7 +860,8 @@ def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.T
     [T, k] or None (ones).  W may hold the experts [group_offset, group_offset
     + W.w_in.shape[0]) of E; the others add nothing.  With `buf` (made for T
     tokens or more) the result is a part of buf.y and nothing is allocated; calls
-    that may overlap on the GPU need buffers of their own."""
+    that may overlap on the GPU need buffers of their own.  Without, buffers are
+    made and zeroed in the current stream's order for the one call."""
     T, k = _arg("ffn_decode topk_ids", topk_ids, torch.int32, 2).shape
     D = _arg("ffn_decode x", x, torch.bfloat16, 2).shape[1]
     El, F2 = W.w_in.shape[:2]
@@ -877,7 +885,7 @@ def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.T
     ps_in = _ptr("ffn_decode s_in", W.s_in, s_type, s_in, dev)
     ps_out = _ptr("ffn_decode s_out", W.s_out, s_type, s_out, dev)
     if buf is None:
-        buf = DecodeBuffers(max(T, 1), D, E, k, F, x.device)
+        buf = DecodeBuffers(max(T, 1), D, E, k, F, x.device, settle=False)
     elif buf.T < T or buf.k != k or buf.D != D or buf.F != F or buf.y.get_device() != dev:
         raise MoEError("ffn_decode: the buffers were made for another shape or device")
     y = buf.y if T == buf.T else buf.y[:T]

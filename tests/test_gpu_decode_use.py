@@ -39,3 +39,47 @@ def test_mx4_ring_goes_round(T, k, E, D, F):
     for _ in range(200):
         differs |= (moe.ffn_decode(x, idd, wd, W, buf) != first).any()
     assert not differs.item() and moe.device_error() == 0
+
+
+def test_buffers_are_ready_on_any_stream():
+    """The workspace is zero when the constructor returns, whatever the creating
+    stream still has to do and whatever the memory held before."""
+    n = moe.DecodeBuffers(8, 1024, 4, 2, 1024, "cuda").ws_bytes
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    junk = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    del junk  # (its memory is the next to be handed out for this size)
+    torch.cuda._sleep(200_000_000)  # some 0.1 s of work on the creating stream
+    buf = moe.DecodeBuffers(8, 1024, 4, 2, 1024, "cuda")
+    with torch.cuda.stream(side):
+        seen = buf.ws.any()
+    side.synchronize()
+    assert not seen.item()
+    rng, x, ids, w = case(50, 8, 2, 4, 1024)
+    W = make_weights("e4m3-channel", 4, 1024, 1024, rng)
+    idd, wd = dev(ids), dev(w)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    buf = moe.DecodeBuffers(8, 1024, 4, 2, 1024, "cuda")
+    with torch.cuda.stream(side):
+        y = moe.ffn_decode(x, idd, wd, W, buf)
+    side.synchronize()
+    check(y, x, ids, w, W)
+
+
+def test_captured_without_buffers():
+    """The buffers of a call without any are made, and zeroed, in the graph."""
+    rng, x, ids, w = case(51, 5, 2, 4, 256)
+    W = make_weights("mx8", 4, 256, 128, rng)
+    idd, wd = dev(ids), dev(w)
+    moe.ffn_decode(x, idd, wd, W)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = moe.ffn_decode(x, idd, wd, W)
+        z = moe.ffn_decode(x, idd, wd, W, moe.DecodeBuffers(8, 256, 4, 2, 128, "cuda"))
+    for _ in range(3):
+        y.fill_(7.0), z.fill_(7.0)
+        g.replay()
+        check(y, x, ids, w, W)
+        check(z, x, ids, w, W)
