@@ -859,8 +859,8 @@ def ffn_decode(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: Optional[torch.T
     type.  topk_ids int32 [T, k], topk_w fp32
     [T, k] or None (ones).  W may hold the experts [group_offset, group_offset
     + W.w_in.shape[0]) of E; the others add nothing.  With `buf` (made for T
-    tokens or more) the result is a part of buf.y and nothing is allocated; calls
-    that may overlap on the GPU need buffers of their own.  Without, buffers are
+    tokens or more) the result is a part of buf.y, which may also hold x, and
+    nothing is allocated; calls that may overlap on the GPU need buffers of their own.  Without, buffers are
     made and zeroed in the current stream's order for the one call."""
     T, k = _arg("ffn_decode topk_ids", topk_ids, torch.int32, 2).shape
     D = _arg("ffn_decode x", x, torch.bfloat16, 2).shape[1]

@@ -35,7 +35,11 @@
 //                a box's K) scaled by the power of two that puts its largest value
 //                in [2^14, 2^15).  f16 then holds a bf16 value exactly down to
 //                2^-28 of the span's largest and to 2^-39 of that below, and h to
-//                2^-11 relative.  (The result's bf16 has 2^-8.)
+//                2^-11 relative down to there.  (The result's bf16 has 2^-8: with
+//                h in fp32 it would be 1.659e-3 from exact, with f16 it is 1.671e-3,
+//                relative Frobenius, one result in ten off by one bf16 step.)
+//                A sum over MX blocks grows to 2^23 times the largest weight's
+//                magnitude before the span scale comes off: weights to 2^104.
 //   8 warps a group contract, 16 weight rows each: ldmatrix brings 16 rows x 32
 //                bytes, one conversion makes two f16 weights (exact for e4m3, int8
 //                and e2m1, NaN codes included), mma.m16n8k16 multiplies them with
@@ -270,7 +274,7 @@ __device__ __forceinline__ void weights8(uint32_t w, uint32_t (&v)[4]) {
 }
 
 // ---- the pairs by expert ---------------------------------------------------
-// Every CTA of both kernels sorts for itself, to the same tables.
+// Every CTA sorts for itself, to the same tables.
 
 __device__ __forceinline__ int local_expert(const Params& p, int i) {
   const int id = __ldg(p.ids + i);

@@ -589,11 +589,12 @@ size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
  *   y[t] = bf16( sum_j topk_w[t, j] * Wo[e] (silu(W0[e] x[t]) * (W1[e] x[t])) ),
  *   e = topk_ids[t, j], in ascending j.
  * With a few tokens the bytes of the chosen experts' weights are the cost, so
- * the activations stay bf16 and h fp32 (held as f16 with a scale for each 128
- * or 256 values while they are multiplied, relative error at most 2^-11); only
- * the weights are quantised, and the sums are fp32.  (The prompt's path above
- * quantises x and h as well, so the two do not agree bit for bit.)  Results do
- * not depend on the order in which CTAs run.
+ * the activations stay bf16 and h fp32; only the weights are quantised, and the
+ * sums are fp32.  While they are multiplied, x and h are held as f16 with a
+ * power-of-two scale for each 128 or 256 values: x exactly, h to 2^-11 relative,
+ * and either to 2^-39 of the largest of these values where one is below 2^-28 of
+ * it.  (The prompt's path above quantises x and h as well, so the two do not
+ * agree bit for bit.)  Results do not depend on the order in which CTAs run.
  *
  *   x         bf16 [T, D], T <= 64, T * k <= 1024
  *   topk_ids  int32 [T, k], expert ids in [0, E), the same one twice allowed;
@@ -605,9 +606,11 @@ size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
  *       gmm_fp8_w8 (modes PER_ROW, PER_ROW_BLOCK128, PER_TENSOR; the two
  *       tensors may have different modes)
  *     MOE_WEIGHT_MXFP8, MOE_WEIGHT_MXFP4: codes and scale codes as for
- *       gmm_fp8_mx and gmm_fp4_mx; in_mode and out_mode are not read
+ *       gmm_fp8_mx and gmm_fp4_mx; in_mode and out_mode are not read.  Weights
+ *       up to 2^104 in magnitude: above, a block's sum may overflow before the
+ *       activations' scale is put back
  *   Experts outside [group_offset, group_offset + E_local) add nothing.
- *   y         bf16 [T, D]
+ *   y         bf16 [T, D]; may be x (every CTA has read x before one writes y)
  *   workspace moe_ffn_decode_workspace_bytes(T, k, D, F) bytes of device
  *             memory, 16-byte aligned, ZERO before its first use: it holds
  *             counters, which every call leaves at zero (after a call that set
