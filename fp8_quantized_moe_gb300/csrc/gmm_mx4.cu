@@ -33,10 +33,11 @@
 //
 // Measured: 16384 x 28672 x 4096 over 8 groups 841 us (4.6 PFLOP/s), 16384 x 1536
 // x 2048 over 128 groups 51 us (5.5 TB/s), 32 of 64 groups of 12000 x 4096 x 7168
-// 135 us (4.6 TB/s).  The large one is bound by the MMA issue order: its MMAs
-// take about 900 clocks a stage when the scale copies are left out, the six
-// copies the rest of 1145.  (Pairs of CTAs, each with half of B, read a third
-// less through shared memory and L2 and took 898 us: neither is the bound.)
+// 135 us (4.6 TB/s).  Of the large one's 1145 clocks a stage the six scale
+// copies take some 215 (682 us without them).  What holds the other 930 is not
+// known: four such MMAs take 512 at their nominal rate.  (Pairs of CTAs, each with
+// half of B, read a third less through shared memory and L2: 657 us without the
+// copies, 898 with them.)
 //
 // Every wait is bounded; on expiry
 // the kernel raises MOE_DEVERR_TIMEOUT, lets what it issued finish and returns.
