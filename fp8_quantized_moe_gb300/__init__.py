@@ -21,6 +21,12 @@ The MXFP4 variant (MX4: the same blocks of e2m1 values, two a byte) runs
 quantize_sort_mx4 -> gmm_mx4 -> swiglu_quant_mx4 -> gmm_mx4 ->
 ragged_gather_reduce.
 
+Expert weights with one scale for each 128 x 128 block (PER_BLOCK128) are for training as
+well: gmm_block contracts them with activations that carry one scale per row and 128 columns
+and, transposed, gives the input gradient; tgmm_mx the weight gradient from bf16 operands;
+ffn_forward and ffn_backward run on them, and router_balance_loss with its gradient joins
+router_backward.
+
 Single decoding steps (up to 64 tokens) take ffn_decode: the whole expert FFN in
 one kernel, on bf16 activations and the same expert weights of any type.
 """
@@ -42,6 +48,7 @@ PER_TENSOR = 2
 PER_GROUP_COL = 3
 MX32 = 4  # MXFP8: uint8 E8M0 codes, K-block-major [cols/128, rows, 4]
 MX4 = 5  # MXFP4: packed e2m1 codes, two a byte, with scale codes as MX32
+PER_BLOCK128 = 6  # weights: one fp32 scale for each 128 x 128 block, [E, ceil(N/128), K/128]
 
 __all__ = [
     "PER_ROW", "PER_ROW_BLOCK128", "PER_TENSOR", "PER_GROUP_COL", "MoEError", "lib", "device_error",
@@ -52,6 +59,9 @@ __all__ = [
     "dequantize_rows_mx4", "quantize_sort_mx4", "swiglu_quant_mx4", "gmm_mx4", "quantize_weights_int8", "gmm_w8", "gmm_w8_workspace_bytes",
     "prepare_weights_w8",
     "ExpertWeights", "prepare_weights", "FFNBuffers", "ffn_forward", "ffn_backward", "DecodeBuffers", "ffn_decode",
+    "PER_BLOCK128", "decode_weights", "quantize_weights_block", "gmm_block", "tgmm_mx", "tgmm_mx_workspace_bytes",
+    "gather_scale_quant_block", "swiglu_bwd_quant_block", "BalanceLoss", "router_balance_loss",
+    "router_balance_loss_backward",
 ]
 
 
@@ -408,6 +418,95 @@ def swiglu_quant_mx4(a: torch.Tensor, h_q=None, h_sf=None):
     return h_q, h_sf
 
 
+def quantize_weights_block(w: torch.Tensor, transposed: bool = False, q=None, s=None, q_t=None, s_t=None):
+    """bf16 [E, N, K] -> (e4m3 codes [E, N, K], fp32 scales [E, ceil(N/128), K/128]), one scale for each 128 x 128
+    block; with `transposed` also the transposed weights' (codes [E, K, N], scales [E, K/128, N/128]), N % 128 == 0."""
+    what = "quantize_weights_block"
+    E, N, K = _arg(what, w, torch.bfloat16, 3).shape
+    dev, at = _dev(what, w), w.device
+    pw = _ptr(what, w, torch.bfloat16, (E, N, K), dev)
+    q = torch.empty(E, N, K, dtype=torch.uint8, device=at) if q is None else q
+    s = torch.empty(E, _nb(N), K // 128, dtype=torch.float32, device=at) if s is None else s
+    pq = _ptr(what + " q", q, torch.uint8, (E, N, K), dev)
+    ps = _ptr(what + " s", s, torch.float32, (E, _nb(N), K // 128), dev)
+    pqt = pst = None
+    if transposed:
+        q_t = torch.empty(E, K, N, dtype=torch.uint8, device=at) if q_t is None else q_t
+        s_t = torch.empty(E, K // 128, N // 128, dtype=torch.float32, device=at) if s_t is None else s_t
+        pqt = _ptr(what + " q_t", q_t, torch.uint8, (E, K, N), dev)
+        pst = _ptr(what + " s_t", s_t, torch.float32, (E, K // 128, N // 128), dev)
+    check(lib().moe_quantize_weights_block(pw, E, N, K, pq, ps, pqt, pst, _s()), "moe_quantize_weights_block")
+    return (q, s, q_t, s_t) if transposed else (q, s)
+
+
+def gmm_block(lhs_q: torch.Tensor, lhs_s: torch.Tensor, rhs_q: torch.Tensor, rhs_s: torch.Tensor,
+              group_sizes: Optional[torch.Tensor] = None, group_offset: int = 0, out=None) -> torch.Tensor:
+    """Grouped matmul of codes lhs_q [M, K] (scales lhs_s [M, K/128], as quantize_rows gives them with
+    PER_ROW_BLOCK128) and rhs_q [E_local, N, K] (scales rhs_s [E_local, ceil(N/128), K/128], as
+    quantize_weights_block gives them) -> bf16 [M, N].  The experts are [group_offset, group_offset + E_local)
+    of group_sizes' E; without group_sizes (and with one expert) every row is the expert's: a dense product."""
+    what = "gmm_block"
+    M, K = _arg("gmm_block lhs_q", lhs_q, torch.uint8, 2).shape
+    El, N, _ = _arg("gmm_block rhs_q", rhs_q, torch.uint8, 3).shape
+    dev = _dev(what, lhs_q)
+    if group_sizes is None:
+        E, pg = 1, None
+        if El != 1 or group_offset:
+            raise MoEError("gmm_block: without group_sizes, rhs_q holds one expert")
+    else:
+        E = _arg("gmm_block group_sizes", group_sizes, torch.int32, 1).shape[0]
+        pg = _ptr("gmm_block group_sizes", group_sizes, torch.int32, (E,), dev)
+    pl = _ptr("gmm_block lhs_q", lhs_q, torch.uint8, (M, K), dev)
+    pls = _ptr("gmm_block lhs_s", lhs_s, torch.float32, (M, K // 128), dev)
+    pr = _ptr("gmm_block rhs_q", rhs_q, torch.uint8, (El, N, K), dev)
+    prs = _ptr("gmm_block rhs_s", rhs_s, torch.float32, (El, _nb(N), K // 128), dev)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device=lhs_q.device) if out is None else out
+    po = _ptr("gmm_block out", out, torch.bfloat16, (M, N), dev)
+    if M:
+        check(lib().gmm_fp8_block(pl, pls, pr, prs, pg, E, group_offset, El, M, K, N, po, _s()), "gmm_fp8_block")
+    return out
+
+
+def tgmm_mx_workspace_bytes(M: int, K: int, N: int, E_local: int) -> int:
+    """Bytes of tgmm_mx's workspace (0 for a shape that it does not take)."""
+    return int(lib().tgmm_fp8_mx_workspace_bytes(M, K, N, E_local))
+
+
+def tgmm_mx(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Tensor, group_offset: int = 0,
+            E_local: Optional[int] = None, lhs_rows: Optional[torch.Tensor] = None, k: int = 1, out=None,
+            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Weight gradient of a grouped matmul: fp32 [E_local, K, N], the sum over each expert's rows of lhs [M, K]
+    times rhs [M, N] (bf16 both), each rounded to e4m3 with a power-of-two scale for every 32 rows of an expert and
+    column.  With lhs_rows (int32 [M], sorted_src of a sort of T tokens) row m of the lhs is lhs[lhs_rows[m] // k],
+    lhs then being [T, K].  workspace: tgmm_mx_workspace_bytes(M, K, N, E_local) bytes; calls that may overlap on
+    the GPU need workspaces of their own."""
+    what = "tgmm_mx"
+    L, K = _arg("tgmm_mx lhs", lhs, torch.bfloat16, 2).shape
+    M, N = _arg("tgmm_mx rhs", rhs, torch.bfloat16, 2).shape
+    E = _arg("tgmm_mx group_sizes", group_sizes, torch.int32, 1).shape[0]
+    dev, at = _dev(what, lhs), lhs.device
+    El = E - group_offset if E_local is None else E_local
+    if lhs_rows is None and (k != 1 or L != M):
+        raise MoEError(f"tgmm_mx: lhs has {L} rows and rhs {M}; lhs_rows picks rows of lhs, k at a time")
+    px = _ptr("tgmm_mx lhs", lhs, torch.bfloat16, (L, K), dev)
+    pd = _ptr("tgmm_mx rhs", rhs, torch.bfloat16, (M, N), dev)
+    pg = _ptr("tgmm_mx group_sizes", group_sizes, torch.int32, (E,), dev)
+    pi = None if lhs_rows is None else _ptr("tgmm_mx lhs_rows", lhs_rows, torch.int32, (M,), dev)
+    if El <= 0:
+        raise MoEError(f"tgmm_mx: E_local is {El}")
+    out = torch.empty(El, K, N, dtype=torch.float32, device=at) if out is None else out
+    po = _ptr("tgmm_mx out", out, torch.float32, (El, K, N), dev)
+    if not M:
+        return out.zero_()
+    L_ = lib()
+    if workspace is None:
+        workspace = torch.empty(max(16, L_.tgmm_fp8_mx_workspace_bytes(M, K, N, El)), dtype=torch.uint8, device=at)
+    pw = _ptr("tgmm_mx workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+    check(L_.tgmm_fp8_mx(px, L, pi, k, pd, pg, E, group_offset, El, M, K, N, po, pw, workspace.numel(), _s()),
+          "tgmm_fp8_mx")
+    return out
+
+
 def gmm(lhs_q, lhs_scale, lhs_mode, rhs_q, rhs_scale, rhs_mode, group_sizes, group_offset: int = 0,
         E_local: Optional[int] = None, out=None):
     """Grouped matmul -> bf16 [M, N]."""
@@ -553,6 +652,41 @@ def swiglu_bwd_quant(dH: torch.Tensor, a: torch.Tensor):
     return dA, dA_q, dA_s
 
 
+def gather_scale_quant_block(G: torch.Tensor, w: Optional[torch.Tensor], sorted_src: torch.Tensor, k: int):
+    """gather_scale_quant with one scale per row and 128 columns: (dO bf16 [T*k, D], codes, scales [T*k, D/128])."""
+    what = "gather_scale_quant_block"
+    T, D = _arg(what, G, torch.bfloat16, 2).shape
+    R, dev, at = T * k, _dev(what, G), G.device
+    pG = _ptr(what, G, torch.bfloat16, (T, D), dev)
+    pw = None if w is None else _ptr(what + " w", w.view(-1), torch.float32, (R,), dev)
+    ps = _ptr(what + " sorted_src", sorted_src, torch.int32, (R,), dev)
+    dO = torch.empty(R, D, dtype=torch.bfloat16, device=at)
+    dO_q = torch.empty(R, D, dtype=torch.uint8, device=at)
+    dO_s = torch.empty(R, D // 128, dtype=torch.float32, device=at)
+    if R:
+        check(lib().moe_gather_scale_quant_block(pG, pw, ps, T, k, D, dO.data_ptr(), dO_q.data_ptr(), dO_s.data_ptr(),
+                                                 _s()), "moe_gather_scale_quant_block")
+    return dO, dO_q, dO_s
+
+
+def swiglu_bwd_quant_block(dH: torch.Tensor, a: torch.Tensor):
+    """swiglu_bwd_quant with one scale per row and 128 columns, and h = bf16(silu(a0) a1):
+    (dA bf16 [R, 2F], codes, scales [R, 2F/128], h bf16 [R, F])."""
+    what = "swiglu_bwd_quant_block"
+    R, F = _arg(what, dH, torch.bfloat16, 2).shape
+    dev, at = _dev(what, dH), dH.device
+    pd = _ptr(what, dH, torch.bfloat16, (R, F), dev)
+    pa = _ptr(what + " a", a, torch.bfloat16, (R, 2 * F), dev)
+    dA = torch.empty(R, 2 * F, dtype=torch.bfloat16, device=at)
+    dA_q = torch.empty(R, 2 * F, dtype=torch.uint8, device=at)
+    dA_s = torch.empty(R, 2 * F // 128, dtype=torch.float32, device=at)
+    h = torch.empty(R, F, dtype=torch.bfloat16, device=at)
+    if R:
+        check(lib().moe_swiglu_bwd_quant_block(pd, pa, R, F, dA.data_ptr(), dA_q.data_ptr(), dA_s.data_ptr(),
+                                               h.data_ptr(), _s()), "moe_swiglu_bwd_quant_block")
+    return dA, dA_q, dA_s, h
+
+
 def quantize_group_cols(g: torch.Tensor, group_sizes: torch.Tensor, group_offset: int = 0,
                         E_local: Optional[int] = None, scales_only: bool = False):
     """Per-(expert, column) e4m3 codes and scales of g; (None, scales) with scales_only."""
@@ -617,9 +751,69 @@ def router_topk(x: torch.Tensor, w_gate: torch.Tensor, k: int):
     return logits, ids, w
 
 
+@dataclasses.dataclass
+class BalanceLoss:
+    """What router_balance_loss computed, and what its gradient needs."""
+    loss: torch.Tensor    # fp32 [1]
+    counts: torch.Tensor  # int32 [seqs, E]: pairs of valid rows routed to each expert
+    mean: torch.Tensor    # fp32 [seqs, E]: mean probability over valid rows
+    tokens: torch.Tensor  # int32 [seqs]: valid rows
+    k: int
+    coef: float
+    valid: Optional[torch.Tensor] = None
+
+
+def router_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, coef: float = 1.0, seqs: int = 1,
+                        valid: Optional[torch.Tensor] = None) -> BalanceLoss:
+    """Balance loss of router logits fp32 [T, E] and their choices int32 [T, k], the T rows being `seqs` sequences
+    of equal length: coef times the mean over sequences of sum_e (E counts_e / (k n)) mean_e, with n the
+    sequence's valid rows.  valid: bool [T]; a row that is not counts nowhere (padding), whatever it holds."""
+    what = "router_balance_loss"
+    T, E = _arg("router_balance_loss logits", logits, torch.float32, 2).shape
+    k = _arg("router_balance_loss topk_ids", topk_ids, torch.int32, 2).shape[1]
+    dev, at = _dev(what, logits), logits.device
+    pl = _ptr("router_balance_loss logits", logits, torch.float32, (T, E), dev)
+    pi = _ptr("router_balance_loss topk_ids", topk_ids, torch.int32, (T, k), dev)
+    pv = None if valid is None else _ptr("router_balance_loss valid", valid, torch.bool, (T,), dev)
+    L = lib()
+    nws = L.moe_router_balance_workspace_bytes(T, E, k, seqs)
+    if not nws:
+        raise MoEError(f"router_balance_loss does not take T = {T}, E = {E}, k = {k}, seqs = {seqs}")
+    loss = torch.empty(1, dtype=torch.float32, device=at)
+    counts = torch.empty(seqs, E, dtype=torch.int32, device=at)
+    mean = torch.empty(seqs, E, dtype=torch.float32, device=at)
+    tokens = torch.empty(seqs, dtype=torch.int32, device=at)
+    ws = torch.empty(nws, dtype=torch.uint8, device=at)
+    check(L.moe_router_balance(pl, pi, pv, T, E, k, seqs, coef, loss.data_ptr(), counts.data_ptr(), mean.data_ptr(),
+                               tokens.data_ptr(), ws.data_ptr(), nws, _s()), "moe_router_balance")
+    return BalanceLoss(loss, counts, mean, tokens, k, coef, valid)
+
+
+def router_balance_loss_backward(logits: torch.Tensor, b: BalanceLoss, grad: Optional[torch.Tensor] = None,
+                                 out=None) -> torch.Tensor:
+    """Gradient of router_balance_loss in the logits it was given, fp32 [T, E] (zero in rows that are not valid);
+    grad: fp32 [1], the loss's own gradient (None: 1).  Counts are constants.  router_backward takes it as
+    dlogits_aux."""
+    what = "router_balance_loss_backward"
+    T, E = _arg("router_balance_loss_backward logits", logits, torch.float32, 2).shape
+    seqs, dev = b.tokens.shape[0], _dev(what, logits)
+    pl = _ptr("router_balance_loss_backward logits", logits, torch.float32, (T, E), dev)
+    pc = _ptr("router_balance_loss_backward counts", b.counts, torch.int32, (seqs, E), dev)
+    pt = _ptr("router_balance_loss_backward tokens", b.tokens, torch.int32, (seqs,), dev)
+    pv = None if b.valid is None else _ptr("router_balance_loss_backward valid", b.valid, torch.bool, (T,), dev)
+    pg = None if grad is None else _ptr("router_balance_loss_backward grad", grad, torch.float32, (1,), dev)
+    out = torch.empty(T, E, dtype=torch.float32, device=logits.device) if out is None else out
+    po = _ptr("router_balance_loss_backward out", out, torch.float32, (T, E), dev)
+    check(lib().moe_router_balance_backward(pl, pv, T, E, b.k, seqs, b.coef, pc, pt, pg, po, _s()),
+          "moe_router_balance_backward")
+    return out
+
+
 def router_backward(G: torch.Tensor, o: torch.Tensor, pos: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,
-                    logits: torch.Tensor, ids: torch.Tensor, workspace: Optional[torch.Tensor] = None):
-    """Router gradient: (dw fp32 [T, k], dlogits bf16 [T, E], grad_gate fp32 [E, D], state_grad bf16 [T, D])."""
+                    logits: torch.Tensor, ids: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                    dlogits_aux: Optional[torch.Tensor] = None):
+    """Router gradient: (dw fp32 [T, k], dlogits bf16 [T, E], grad_gate fp32 [E, D], state_grad bf16 [T, D]).
+    dlogits_aux: fp32 [T, E], another loss's gradient in the logits (router_balance_loss_backward), added to theirs."""
     T, D = x.shape
     E = w_gate.shape[0]
     k = ids.shape[1]
@@ -631,8 +825,10 @@ def router_backward(G: torch.Tensor, o: torch.Tensor, pos: torch.Tensor, x: torc
     nws = lib().moe_router_backward_workspace_bytes(T, D, E)
     if workspace is None or workspace.numel() < nws:
         workspace = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
-    check(lib().moe_router_backward(_p(G), _p(o), _p(pos), _p(x), _p(w_gate), _p(logits), _p(ids), T, D, E, k,
-                                    _p(dw), _p(dl), _p(gg), _p(sg), _p(workspace), workspace.numel(), _s()),
+    aux = None if dlogits_aux is None else _ptr("router_backward dlogits_aux", dlogits_aux, torch.float32, (T, E),
+                                                _dev("router_backward", x))
+    check(lib().moe_router_backward_aux(_p(G), _p(o), _p(pos), _p(x), _p(w_gate), _p(logits), _p(ids), aux, T, D, E, k,
+                                        _p(dw), _p(dl), _p(gg), _p(sg), _p(workspace), workspace.numel(), _s()),
           "moe_router_backward")
     return dw, dl, gg, sg
 
@@ -666,6 +862,7 @@ class ExpertWeights:
     s_in_t: Optional[torch.Tensor] = None
     w_out_t: Optional[torch.Tensor] = None
     s_in_split: Optional[torch.Tensor] = None  # [s_w0, s_w1]: the two K halves of w_in_t
+    s_out_t: Optional[torch.Tensor] = None  # PER_BLOCK128: the block scales of w_out_t
 
 
 def prepare_weights(w_in: torch.Tensor, w_out: torch.Tensor, w_mode: int, static: Optional[dict] = None,
@@ -673,10 +870,22 @@ def prepare_weights(w_in: torch.Tensor, w_out: torch.Tensor, w_mode: int, static
     """Quantise the bf16 expert weights once (outside the timed FFN).
 
     Static scheme: wi_0, wi_1 and wo each carry one fixed scale; the wi_0 |
-    wi_1 concatenation then has a per-channel scale vector."""
+    wi_1 concatenation then has a per-channel scale vector.  The backward pass takes
+    PER_TENSOR (static) or PER_BLOCK128 weights."""
     dev = w_in.device
     E, F2, D = w_in.shape
     F = F2 // 2
+    if w_mode == PER_BLOCK128:
+        if not for_backward:
+            qin, sin = quantize_weights_block(w_in)
+            qo, so = quantize_weights_block(w_out)
+            return ExpertWeights(qin, sin, PER_BLOCK128, qo, so, PER_BLOCK128)
+        if D % 128 != 0 or F % 128 != 0:
+            raise MoEError("the backward pass needs D % 128 == 0 and F % 128 == 0")
+        qin, sin, qin_t, sin_t = quantize_weights_block(w_in, transposed=True)
+        qo, so, qo_t, so_t = quantize_weights_block(w_out, transposed=True)
+        return ExpertWeights(qin, sin, PER_BLOCK128, qo, so, PER_BLOCK128, w_in_t=qin_t, s_in_t=sin_t, w_out_t=qo_t,
+                             s_out_t=so_t)
     if w_mode == MX32:
         qin, sin = quantize_weights_mx(w_in)
         qo, so = quantize_weights_mx(w_out)
@@ -724,6 +933,16 @@ def prepare_weights_w8(w_in: torch.Tensor, w_out: torch.Tensor, w_mode: int) -> 
     return ExpertWeights(qin, sin, w_mode, qo, so, w_mode)
 
 
+def decode_weights(W: ExpertWeights) -> ExpertWeights:
+    """PER_BLOCK128 weights as ffn_decode takes them: the same codes, each block's scale repeated for its 128
+    channels ([E, K/128, N], a 32nd of the codes' bytes).  To be made once, as prepare_weights' result is."""
+    if W.in_mode != PER_BLOCK128:
+        raise MoEError("decode_weights: expected PER_BLOCK128 weights")
+    wide = lambda s, N: s.transpose(1, 2).repeat_interleave(128, 2)[..., :N].contiguous()  # noqa: E731
+    return ExpertWeights(W.w_in, wide(W.s_in, W.w_in.shape[1]), PER_ROW_BLOCK128, W.w_out,
+                         wide(W.s_out, W.w_out.shape[1]), PER_ROW_BLOCK128)
+
+
 class FFNBuffers:
     """Every intermediate of one forward (and backward) pass, allocated once."""
 
@@ -742,6 +961,7 @@ class FFNBuffers:
         self.o = f(R, D, dt=torch.bfloat16)
         self.y = f(T, D, dt=torch.bfloat16)
         self._w8_ws = None
+        self._tgmm_ws = None
         if backward:
             self.dH = f(R, F, dt=torch.bfloat16)
             self.dXs = f(R, D, dt=torch.bfloat16)
@@ -755,6 +975,14 @@ class FFNBuffers:
             n = gmm_w8_workspace_bytes(self.T * self.k, max(self.D, self.F))
             self._w8_ws = torch.empty(n, dtype=torch.uint8, device=self.y.device)
         return self._w8_ws
+
+    def tgmm_workspace(self, E: int) -> torch.Tensor:
+        """tgmm_mx's workspace for either weight gradient of E experts, allocated on first use."""
+        if self._tgmm_ws is None:
+            R = self.T * self.k
+            n = max(tgmm_mx_workspace_bytes(R, self.D, 2 * self.F, E), tgmm_mx_workspace_bytes(R, self.F, self.D, E))
+            self._tgmm_ws = torch.empty(max(n, 16), dtype=torch.uint8, device=self.y.device)
+        return self._tgmm_ws
 
 
 def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, act_mode: int,
@@ -790,6 +1018,15 @@ def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W
         gmm_mx4(s["xs_q"], s["xs_scale"], W.w_in, W.s_in, s["group_sizes"], out=buf.a)
         swiglu_quant_mx4(buf.a, h_q=buf.h_q, h_sf=buf.h_s)
         gmm_mx4(buf.h_q, buf.h_s, W.w_out, W.s_out, s["group_sizes"], out=buf.o)
+        ragged_gather_reduce(buf.o, s["pos"], topk_w, k, out=buf.y)
+        return buf.y
+    if W.in_mode == PER_BLOCK128:
+        if act_mode != PER_ROW_BLOCK128:
+            raise MoEError("PER_BLOCK128 weights take PER_ROW_BLOCK128 activations")
+        s = quantize_sort(x, topk_ids, E, act_mode, out=buf.sort)
+        gmm_block(s["xs_q"], s["xs_scale"], W.w_in, W.s_in, s["group_sizes"], out=buf.a)
+        swiglu_quant(buf.a, act_mode, h_q=buf.h_q, h_scale=buf.h_s)
+        gmm_block(buf.h_q, buf.h_s, W.w_out, W.s_out, s["group_sizes"], out=buf.o)
         ragged_gather_reduce(buf.o, s["pos"], topk_w, k, out=buf.y)
         return buf.y
     if W.in_mode == MX4:
@@ -903,19 +1140,39 @@ def _decode_scale(mode: int, El: int, N: int, K: int) -> tuple:
         return (El, _nb(K), N)
     if mode == PER_TENSOR:
         return (1,)
-    raise MoEError(f"ffn_decode: scale mode {mode}")
+    raise MoEError(f"ffn_decode: scale mode {mode}" + (" (decode_weights gives what it takes)" if mode == PER_BLOCK128 else ""))
 
 
 def ffn_backward(dY: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, buf: FFNBuffers,
-                 static_x: torch.Tensor, static_h: torch.Tensor, keep: Optional[dict] = None):
-    """Backward pass of the static scheme after ffn_forward on `buf`.
+                 static_x: Optional[torch.Tensor] = None, static_h: Optional[torch.Tensor] = None,
+                 keep: Optional[dict] = None, x: Optional[torch.Tensor] = None):
+    """Backward pass after ffn_forward on `buf`: of the static scheme (static_x and static_h
+    as the forward had them), or of PER_BLOCK128 weights (x as the forward had it).
 
     Returns (dX bf16 [T, D], dW_in fp32 [E, D, 2F], dW_out fp32 [E, F, D]):
     dW_in holds grad_wi_0 | grad_wi_1 and dW_out grad_wo, in the pages'
     [E, in, out] layouts.  With `keep` (a dict), the intermediate gradients
-    (dO, dO_q, dO_s, dA, dA_q, dA_s, dAg_s, dOg_s) are stored in it."""
+    (dO, dO_q, dO_s, dA, dA_q, dA_s, dAg_s, dOg_s; with PER_BLOCK128 weights h in place
+    of the last two) are stored in it."""
     s = buf.sort
     k = buf.k
+    if W.in_mode == PER_BLOCK128:
+        if W.w_in_t is None or x is None:
+            raise MoEError("ffn_backward: PER_BLOCK128 weights made with for_backward, and x, are needed")
+        sizes, ws = s["group_sizes"], buf.tgmm_workspace(W.w_in.shape[0])
+        dO, dO_q, dO_s = gather_scale_quant_block(dY, topk_w, s["sorted_src"], k)
+        gmm_block(dO_q, dO_s, W.w_out_t, W.s_out_t, sizes, out=buf.dH)
+        dA, dA_q, dA_s, h = swiglu_bwd_quant_block(buf.dH, buf.a)
+        gmm_block(dA_q, dA_s, W.w_in_t, W.s_in_t, sizes, out=buf.dXs)
+        ragged_gather_reduce(buf.dXs, s["pos"], None, k, out=buf.dX)
+        # both operands of a weight gradient are rounded along the rows that it contracts
+        dW_in = tgmm_mx(x, dA, sizes, lhs_rows=s["sorted_src"], k=k, workspace=ws)
+        dW_out = tgmm_mx(h, dO, sizes, workspace=ws)
+        if keep is not None:
+            keep.update(dO=dO, dO_q=dO_q, dO_s=dO_s, dA=dA, dA_q=dA_q, dA_s=dA_s, h=h)
+        return buf.dX, dW_in, dW_out
+    if static_x is None or static_h is None:
+        raise MoEError("ffn_backward: the static scheme needs static_x and static_h")
     dO, dO_q, dO_s = gather_scale_quant(dY, topk_w, s["sorted_src"], k)
     gmm(dO_q, dO_s, PER_ROW, W.w_out_t, W.s_out, PER_TENSOR, s["group_sizes"], out=buf.dH)
     dA, dA_q, dA_s = swiglu_bwd_quant(buf.dH, buf.a)

@@ -17,6 +17,7 @@ P = ctypes.c_void_p
 i64 = ctypes.c_int64
 i32 = ctypes.c_int
 sz = ctypes.c_size_t
+f32 = ctypes.c_float
 
 # name -> (argtypes, restype); restype i32 is a moe_status
 SIGNATURES = {
@@ -60,6 +61,16 @@ SIGNATURES = {
     "gmm_fp8_w8": ([P, P, i32, P, P, i32, P, i32, i32, i32, i64, i64, i64, P, P, sz, P], i32),
     "moe_ffn_decode": ([P, P, P, i64, i32, i32, i32, i32, i64, i64, i32, P, P, i32, P, P, i32, P, P, sz, P], i32),
     "moe_ffn_decode_workspace_bytes": ([i64, i32, i64, i64], sz),
+    "moe_quantize_weights_block": ([P, i64, i64, i64, P, P, P, P, P], i32),
+    "gmm_fp8_block": ([P, P, P, P, P, i32, i32, i32, i64, i64, i64, P, P], i32),
+    "tgmm_fp8_mx_workspace_bytes": ([i64, i64, i64, i32], sz),
+    "tgmm_fp8_mx": ([P, i64, P, i32, P, P, i32, i32, i32, i64, i64, i64, P, P, sz, P], i32),
+    "moe_gather_scale_quant_block": ([P, P, P, i64, i32, i64, P, P, P, P], i32),
+    "moe_swiglu_bwd_quant_block": ([P, P, i64, i64, P, P, P, P, P], i32),
+    "moe_router_backward_aux": ([P, P, P, P, P, P, P, P, i64, i64, i32, i32, P, P, P, P, P, sz, P], i32),
+    "moe_router_balance_workspace_bytes": ([i64, i32, i32, i64], sz),
+    "moe_router_balance": ([P, P, P, i64, i32, i32, i64, f32, P, P, P, P, P, sz, P], i32),
+    "moe_router_balance_backward": ([P, P, i64, i32, i32, i64, f32, P, P, P, P, P], i32),
     "gmm_fp8_w8_workspace_bytes": ([i64, i64], sz),
 }
 

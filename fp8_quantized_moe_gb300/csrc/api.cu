@@ -9,6 +9,9 @@ extern "C" cudaError_t moe_detail_take_error_combine(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_gmm(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_gmm_mx4(unsigned int* out);
 extern "C" cudaError_t moe_detail_take_error_decode(unsigned int* out);
+extern "C" cudaError_t moe_detail_take_error_gmm_block(unsigned int* out);
+extern "C" cudaError_t moe_detail_take_error_tgmm_mx(unsigned int* out);
+extern "C" cudaError_t moe_detail_take_error_balance(unsigned int* out);
 
 // test hook: 0, or the wait limit in ns
 static std::atomic<uint64_t> g_stall_ns{0};
@@ -33,7 +36,9 @@ extern "C" moe_status moe_get_device_error(moe_stream_t stream, int* code) {
   unsigned int all = 0, v = 0;
   cudaError_t (*take[])(unsigned int*) = {moe_detail_take_error_quantize, moe_detail_take_error_sort,
                                           moe_detail_take_error_combine, moe_detail_take_error_gmm,
-                                          moe_detail_take_error_gmm_mx4, moe_detail_take_error_decode};
+                                          moe_detail_take_error_gmm_mx4, moe_detail_take_error_decode,
+                                          moe_detail_take_error_gmm_block, moe_detail_take_error_tgmm_mx,
+                                          moe_detail_take_error_balance};
   for (auto fn : take) {
     if (fn(&v) != cudaSuccess) return MOE_ERR_CUDA;
     all |= v;

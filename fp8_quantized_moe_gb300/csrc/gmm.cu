@@ -3188,7 +3188,7 @@ extern "C" moe_status tgmm_fp8_gcq(const uint8_t* lhs_q, const float* lhs_scale,
 // ---------------------------------------------------------------------------
 extern "C" cudaError_t moe_detail_router_dw(const uint16_t* G, const uint16_t* o, const int32_t* pos, int64_t T,
                                             int k, int64_t D, float* dw, cudaStream_t st);
-extern "C" cudaError_t moe_detail_router_dlogits(const float* logits, const int32_t* ids, const float* dw, int64_t T,
+extern "C" cudaError_t moe_detail_router_dlogits(const float* logits, const int32_t* ids, const float* dw, const float* aux, int64_t T,
                                                  int E, int k, int Ep, int64_t Tp, uint16_t* dl, uint16_t* dl_pad,
                                                  uint16_t* dlT, cudaStream_t st);
 extern "C" cudaError_t moe_detail_transpose_u16(const uint16_t* src, int64_t R, int64_t C, uint16_t* dst, int64_t Rp,
@@ -3285,6 +3285,16 @@ extern "C" moe_status moe_router_backward(const uint16_t* G, const uint16_t* o, 
                                           int64_t T, int64_t D, int E, int k, float* dw, uint16_t* dlogits,
                                           float* grad_gate, uint16_t* state_grad, void* workspace,
                                           size_t workspace_bytes, moe_stream_t stream) {
+  return moe_router_backward_aux(G, o, pos, x, w_gate, logits, topk_ids, nullptr, T, D, E, k, dw, dlogits, grad_gate,
+                                 state_grad, workspace, workspace_bytes, stream);
+}
+
+extern "C" moe_status moe_router_backward_aux(const uint16_t* G, const uint16_t* o, const int32_t* pos,
+                                              const uint16_t* x, const uint16_t* w_gate, const float* logits,
+                                              const int32_t* topk_ids, const float* dlogits_aux, int64_t T, int64_t D,
+                                              int E, int k, float* dw, uint16_t* dlogits, float* grad_gate,
+                                              uint16_t* state_grad, void* workspace, size_t workspace_bytes,
+                                              moe_stream_t stream) {
   MOE_HOST_CHECK(G && o && pos && x && w_gate && logits && topk_ids && dw && dlogits && grad_gate && state_grad &&
                      workspace,
                  MOE_ERR_INVALID_ARG);
@@ -3304,7 +3314,7 @@ extern "C" moe_status moe_router_backward(const uint16_t* G, const uint16_t* o, 
   router_ws_layout(T, D, E, &w, workspace);
   const int64_t Tp = round8(T), Ep = round8(E);
   MOE_CUDA_TRY(moe_detail_router_dw(G, o, pos, T, k, D, dw, st));
-  MOE_CUDA_TRY(moe_detail_router_dlogits(logits, topk_ids, dw, T, E, k, static_cast<int>(Ep), Tp, dlogits, w.dl_pad,
+  MOE_CUDA_TRY(moe_detail_router_dlogits(logits, topk_ids, dw, dlogits_aux, T, E, k, static_cast<int>(Ep), Tp, dlogits, w.dl_pad,
                                          w.dlT, st));
   MOE_CUDA_TRY(moe_detail_transpose_u16(x, T, D, w.xT, Tp, st));
   MOE_CUDA_TRY(moe_detail_transpose_u16(w_gate, E, D, w.wgT, Ep, st));

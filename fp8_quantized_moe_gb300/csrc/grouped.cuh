@@ -1,0 +1,85 @@
+// What the grouped kernels on block-scaled 8-bit operands share: tensor maps,
+// device queries, launches of CTA pairs, and the rows that belong to no local
+// group.  (Included by several translation units; everything is local to each.)
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxDevices = 256;  // host-side per-device caches
+
+// Rows of out (bf16 [M, N]) before the first and after the last local group: zeros.
+__global__ void __launch_bounds__(256) zero_outside_rows_kernel(uint16_t* out, int64_t M, int64_t N,
+                                                                const int32_t* sizes, int E, int g0, int El) {
+  __shared__ int64_t bound[2];
+  if (threadIdx.x < 32) {
+    int64_t lo = 0, hi = 0;
+    for (int g = threadIdx.x; g < E; g += 32) {
+      const int64_t sz = __ldg(sizes + g);
+      lo += g < g0 ? sz : 0;
+      hi += g < g0 + El ? sz : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo += __shfl_xor_sync(0xffffffffu, lo, o);
+      hi += __shfl_xor_sync(0xffffffffu, hi, o);
+    }
+    if (threadIdx.x == 0) {  // (sizes that do not add up to M: an error of the product's kernel)
+      bound[0] = min(max(lo, static_cast<int64_t>(0)), M);
+      bound[1] = min(max(hi, bound[0]), M);
+    }
+  }
+  __syncthreads();
+  const int64_t n16 = N / 8, head = bound[0] * n16, gap = (bound[1] - bound[0]) * n16;
+  const int64_t all = M * n16 - gap, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  uint4* o = reinterpret_cast<uint4*>(out);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step)
+    o[i < head ? i : i + gap] = make_uint4(0, 0, 0, 0);
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A byte matrix [rows, cols] of row pitch `pitch` for boxes of box_rows x 128
+// bytes in the 128-byte swizzle; reads past the extents return zeros.
+inline bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t pitch,
+                        uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The current device's SMs, or 0 when it is not an sm_103 (or on an error).
+inline int sm103_count() {
+  int dev = 0, major = 0, minor = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return major == 10 && minor == 3 ? sms : 0;
+}
+
+}  // namespace
+}  // namespace moe

@@ -5,6 +5,9 @@
 //   moe_gather_scale_quant                         (dO = bf16(w G[src]))
 //   moe_swiglu_bwd_quant                           (dA0 | dA1)
 //   moe_quantize_group_cols                        (per-(expert, column) scales)
+//   moe_quantize_weights_block                     (one scale per 128 x 128 block)
+//   moe_gather_scale_quant_block, moe_swiglu_bwd_quant_block
+//                                                  (the same producers, one scale per row and 128 columns)
 //
 // All of these are HBM-bound.  One CTA handles one row: each thread loads
 // 16-byte vectors (8 bf16; two adjacent ones a unit for most producers),
@@ -557,6 +560,118 @@ __global__ void finalize_scales_kernel(float* scale, int64_t n) {
   if (i < n) scale[i] = absmax_scale(scale[i]);
 }
 
+// quant_n for any scale: below 2^-125 its reciprocal overflows.
+template <int N>
+__device__ __forceinline__ void quant_any(const float* x, float s, float* out) {
+  if (s < 0x1p-125f) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) out[j] = __fdiv_rn(x[j], s);
+  } else {
+    quant_n<N>(x, s, __frcp_rn(s), out);
+  }
+}
+
+// ---- 128 x 128 blocks ------------------------------------------------------
+// Expert weights w [E, N, K] to e4m3 codes with one scale (amax / 448) for each 128 x
+// 128 block of an expert, and the codes of the transposed weights (the same ones).
+// One block of the matrix a CTA, read once: a warp holds 32 rows of 64 columns, a lane
+// 8 consecutive rows of 8 columns, so that a row's codes (8 bytes) and a transposed
+// row's are both in one lane's registers; four lanes fill a 32-byte sector of either.
+__global__ void __launch_bounds__(256, 4) weights_block_kernel(const uint16_t* w, int64_t N, int64_t K, uint8_t* q,
+                                                               float* scale, uint8_t* q_t, float* scale_t) {
+  __shared__ float red[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kbs = static_cast<int>(K / 128), nbs = static_cast<int>((N + 127) / 128);
+  const int kb = blockIdx.x % kbs, nb = static_cast<int>(blockIdx.x / kbs % nbs);
+  const int64_t e = blockIdx.x / kbs / nbs;
+  const int64_t n0 = nb * 128ll + (warp & 3) * 32 + (lane >> 3) * 8, k0 = kb * 128ll + (warp >> 2) * 64 + (lane & 7) * 8;
+  uint4 d[8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d[i] = n0 + i < N ? ldg16(w + (e * N + n0 + i) * K + k0) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    unpack8(d[i], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+  }
+  amax = warp_max(amax);
+  if (lane == 0) red[warp] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, red[j]);
+  const float s = absmax_scale(amax);
+  if (tid == 0) {
+    scale[(e * nbs + nb) * kbs + kb] = s;
+    if (scale_t) scale_t[(e * kbs + kb) * nbs + nb] = s;
+  }
+  uint2 c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x[8], v[8];
+    unpack8(d[i], x);
+    quant_any<8>(x, s, v);
+    c[i] = pack_e4m3x8(v);
+    if (n0 + i < N) *reinterpret_cast<uint2*>(q + (e * N + n0 + i) * K + k0) = c[i];
+  }
+  if (!q_t) return;  // (N % 128 == 0 from here on)
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // 4 columns: the low or high words of the 8 rows
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = h ? c[i].y : c[i].x;
+    uint32_t o[4][2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint32_t t0 = __byte_perm(r[4 * g], r[4 * g + 1], 0x5140), t1 = __byte_perm(r[4 * g + 2], r[4 * g + 3], 0x5140);
+      const uint32_t t2 = __byte_perm(r[4 * g], r[4 * g + 1], 0x7362), t3 = __byte_perm(r[4 * g + 2], r[4 * g + 3], 0x7362);
+      o[0][g] = __byte_perm(t0, t1, 0x5410);
+      o[1][g] = __byte_perm(t0, t1, 0x7632);
+      o[2][g] = __byte_perm(t2, t3, 0x5410);
+      o[3][g] = __byte_perm(t2, t3, 0x7632);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint2*>(q_t + (e * K + k0 + 4 * h + j) * N + n0) = make_uint2(o[j][0], o[j][1]);
+  }
+}
+
+// SwiGLU backward with one scale per row and 128 columns of dA = [dA0 | dA1], and h =
+// bf16(silu(a0) a1), which the backward's weight gradient of wo contracts.  16 lanes
+// hold 128 columns of both halves.
+__global__ void __launch_bounds__(256) swiglu_bwd_block_kernel(SwigluBwdOp op, int64_t R, uint16_t* h, uint8_t* q,
+                                                               float* scale) {
+  const int64_t units = op.F / 8, all = R * units;  // (a multiple of 16)
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step) {
+    const int64_t row = i / units;
+    const int u = static_cast<int>(i - row * units);
+    const int64_t c = 8 * static_cast<int64_t>(u), F = op.F;
+    float v[2][8], z[8], a1[8], hv[8];
+    uint32_t hb[4];
+    op(row, u, v);
+    unpack8(ldg16(op.a + row * 2 * F + c), z);
+    unpack8(ldg16(op.a + row * 2 * F + F + c), a1);
+    swiglu_h_x2<8>(z, a1, hv, hb);
+    *reinterpret_cast<uint4*>(h + row * F + c) = make_uint4(hb[0], hb[1], hb[2], hb[3]);
+    const unsigned half = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[p][j]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
+      const float s = absmax_scale(m);
+      float y[8];
+      quant_any<8>(v[p], s, y);
+      *reinterpret_cast<uint2*>(q + row * 2 * F + p * F + c) = pack_e4m3x8(y);
+      if ((u & 15) == 0) scale[row * (F / 64) + p * (F / 128) + u / 16] = s;
+    }
+  }
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -713,5 +828,47 @@ extern "C" moe_status moe_quantize_group_cols(const uint16_t* g, int64_t M, int6
     group_cols_kernel<true><<<grid, 256, 0, st>>>(g, M, N, group_sizes, E, group_offset, E_local, q, scale);
     MOE_CUDA_TRY(cudaGetLastError());
   }
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_quantize_weights_block(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q,
+                                                 float* scale, uint8_t* q_t, float* scale_t, moe_stream_t stream) {
+  MOE_HOST_CHECK(w && q && scale && E > 0 && N > 0 && K > 0 && K % 128 == 0, MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(!q_t == !scale_t && (!q_t || N % 128 == 0), MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(aligned16(w) && aligned16(q) && aligned16(q_t) && aligned16(scale) && aligned16(scale_t),
+                 MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(N < (1ll << 31) - 128 && K < (1ll << 31) && E < (1ll << 31), MOE_ERR_INVALID_ARG);
+  const int64_t nk = (N + 127) / 128 * (K / 128);
+  MOE_HOST_CHECK(E <= ((1ll << 31) - 1) / nk, MOE_ERR_INVALID_ARG);
+  weights_block_kernel<<<static_cast<unsigned>(E * nk), 256, 0, as_stream(stream)>>>(w, N, K, q, scale, q_t, scale_t);
+  MOE_CUDA_TRY(cudaGetLastError());
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_gather_scale_quant_block(const uint16_t* G, const float* w, const int32_t* sorted_src,
+                                                   int64_t T, int k, int64_t D, uint16_t* dO, uint8_t* dO_q,
+                                                   float* dO_scale, moe_stream_t stream) {
+  MOE_HOST_CHECK(G && sorted_src && dO && dO_q && dO_scale && T >= 0 && k > 0 && D > 0, MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(D % 128 == 0 && D <= kMaxCols && T <= ((1ll << 31) - 1) / k, MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(aligned16(G) && aligned16(dO) && aligned16(dO_q) && aligned16(dO_scale), MOE_ERR_INVALID_ARG);
+  GatherScaleOp op{G, w, sorted_src, T * k, k, D, dO};
+  return launch_rows(op, T * k, static_cast<int>(D / 16), D, MOE_SCALE_PER_ROW_BLOCK128, nullptr, dO_q,
+                     ScaleOut{dO_scale, 0, static_cast<int>(D / 128), nullptr, 0}, as_stream(stream));
+}
+
+extern "C" moe_status moe_swiglu_bwd_quant_block(const uint16_t* dH, const uint16_t* a, int64_t R, int64_t F,
+                                                 uint16_t* dA, uint8_t* dA_q, float* dA_scale, uint16_t* h,
+                                                 moe_stream_t stream) {
+  MOE_HOST_CHECK(dH && a && dA && dA_q && dA_scale && h && R >= 0 && R < (1ll << 31) && F > 0 && F % 128 == 0 &&
+                     2 * F <= kMaxCols,
+                 MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(aligned16(dH) && aligned16(a) && aligned16(dA) && aligned16(dA_q) && aligned16(dA_scale) &&
+                     aligned16(h),
+                 MOE_ERR_INVALID_ARG);
+  if (R == 0) return MOE_OK;
+  const int64_t blocks = (R * (F / 8) + 255) / 256;
+  swiglu_bwd_block_kernel<<<static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, as_stream(stream)>>>(
+      SwigluBwdOp{dH, a, F, dA}, R, h, dA_q, dA_scale);
+  MOE_CUDA_TRY(cudaGetLastError());
   return MOE_OK;
 }

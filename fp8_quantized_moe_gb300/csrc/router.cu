@@ -3,8 +3,9 @@
 // state_grad are measured beside the expert weights' gradients).
 //
 //   dw[t, j]         = <G[t], o[pos[t k + j]]>       (the combine's adjoint in w)
-//   dlogits[t, i]    = bf16( p_i (g_i - s) ),  s = sum_j p[id_j] dw[t, j],
-//                      g_i = dw[t, j] where i = id_j (else 0)
+//   dlogits[t, i]    = bf16( p_i (g_i - s) + aux[t, i] ),  s = sum_j p[id_j] dw[t, j],
+//                      g_i = dw[t, j] where i = id_j (else 0), aux: another loss's
+//                      gradient (the balance loss's), or none
 // with p the fp32 softmax of the row's logits taken exactly as the router's
 // forward takes it (max, e_i = exp(l_i - m), Z summed in ascending i,
 // p_i = e_i / Z).  The two gate gradients are dense bf16 contractions run by
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(256) router_dw_kernel(const uint16_t* G, const
 // copy whose columns E..Ep-1 are zero, and the transpose [Ep, Tp] (zero past
 // T and past E).
 __global__ void __launch_bounds__(128) router_dlogits_kernel(const float* logits, const int32_t* ids, const float* dw,
-                                                             int64_t T, int E, int k, int Ep, int64_t Tp,
+                                                             const float* aux, int64_t T, int E, int k, int Ep, int64_t Tp,
                                                              uint16_t* dl, uint16_t* dl_pad, uint16_t* dlT) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (t >= Tp) return;
@@ -74,7 +75,9 @@ __global__ void __launch_bounds__(128) router_dlogits_kernel(const float* logits
       for (int j = 0; j < k; ++j)
         if (__ldg(ids + t * k + j) == i) g = __ldg(dw + t * k + j);
       const float pi = __fdiv_rn(exp_f32(__fsub_rn(l[i], m)), z);
-      b = static_cast<uint16_t>(pack_bf16x2(__fmul_rn(pi, __fsub_rn(g, s)), 0.0f) & 0xFFFFu);
+      float d = __fmul_rn(pi, __fsub_rn(g, s));
+      if (aux) d = __fadd_rn(d, __ldg(aux + t * E + i));
+      b = static_cast<uint16_t>(pack_bf16x2(d, 0.0f) & 0xFFFFu);
       dl[t * E + i] = b;
     }
     dl_pad[t * Ep + i] = b;
@@ -116,11 +119,11 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_router_d
 }
 
 extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_router_dlogits(
-    const float* logits, const int32_t* ids, const float* dw, int64_t T, int E, int k, int Ep, int64_t Tp,
+    const float* logits, const int32_t* ids, const float* dw, const float* aux, int64_t T, int E, int k, int Ep, int64_t Tp,
     uint16_t* dl, uint16_t* dl_pad, uint16_t* dlT, cudaStream_t st) {
   if (Tp == 0) return cudaSuccess;
-  router_dlogits_kernel<<<static_cast<unsigned>((Tp + 127) / 128), 128, 0, st>>>(logits, ids, dw, T, E, k, Ep, Tp, dl,
-                                                                                 dl_pad, dlT);
+  router_dlogits_kernel<<<static_cast<unsigned>((Tp + 127) / 128), 128, 0, st>>>(logits, ids, dw, aux, T, E, k, Ep, Tp,
+                                                                                 dl, dl_pad, dlT);
   return cudaGetLastError();
 }
 

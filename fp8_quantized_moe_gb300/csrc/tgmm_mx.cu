@@ -1,0 +1,544 @@
+// Weight gradient of a grouped matmul on block-scaled 8-bit operands (sm_103a):
+//   tgmm_fp8_mx  out[e, k, n] = sum_{m in e} r(lhs)[m, k] r(rhs)[m, n]   (fp32 out)
+// from bf16 lhs and rhs, each rounded (r) to e4m3 with one power-of-two scale for
+// every 32 consecutive rows of an expert and column: the contracted dimension is the
+// row, so the tensor core's block-scaled MMA (tcgen05.mma.kind::mxf8f6f4, one E8M0
+// scale per 32 values of K) applies both scales and one fp32 accumulator runs over all
+// of an expert's rows.
+//
+// The scale of a block is the smallest power of two, 2^-127 at least, with
+// amax <= 448 * 2^X, so no value saturates (the MX formats' own rule, floor(log2 amax) - 8,
+// cuts off up to an eighth of the largest value; a gradient sums such values, all cut
+// off to the same side).  Division by it is exact: the code is e4m3's rounding of the
+// value alone.
+//
+// Two kernels:
+//   round_rows_kernel  both operands to codes in the workspace, transposed to
+//     [128-row block][column][128 rows], every expert padded to whole blocks with
+//     zeros; the scale codes as the atoms that tcgen05.cp copies (32 x 16 bytes for 128
+//     columns: byte 16 l + 4 c + j holds column 32 c + l, rows 32 j..).  Bound by memory
+//     (2 bytes read, 1 written): a thread holds 8 columns of 8 consecutive rows, so
+//     that a column's codes are 8 bytes of its own registers and a warp's stores fill
+//     whole sectors; maxima of 32 rows are among 4 lanes.
+//   tgmm_mx_kernel  one persistent CTA per SM, 128 (k) x 256 (n) tiles:
+//     warp 0      TMA producer: per stage one block of 128 rows, A 16 KB, B 32 KB and the
+//                 scale atoms (one bulk copy an operand), four stages.
+//     warp 1      MMA issuer: scale atoms to tensor memory, then an M = 128, N = 256
+//                 MMA for each 32 rows that the block holds.
+//     warps 4..11 epilogue: the accumulator to 128 registers a thread, accumulator
+//                 handed back, then whole 32-byte sectors to memory, beside the next
+//                 tile's MMAs.
+//     Tiles run expert-major, then n tile, then k tile.
+//
+// Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets what
+// it issued finish and returns.
+#include <algorithm>
+
+#include "grouped.cuh"
+
+namespace moe {
+namespace {
+
+__device__ unsigned int g_err;
+
+constexpr int kRB = 128;  // rows of a block (four scales a column)
+constexpr int kAtom = 512;
+
+// ---- local groups --------------------------------------------------------
+struct Tables {
+  int start[kMaxGroups + 1];   // first row of each local group; the last: their end
+  int kstart[kMaxGroups + 1];  // first 128-row block of each
+};
+
+// Filled by all threads of the block (256 at least); false when a size is negative
+// or they do not add up to M.  Ends with a barrier.
+__device__ bool build_tables(const int32_t* sizes, int E, int g0, int El, int64_t M, Tables* t) {
+  __shared__ int64_t wrows[8];
+  __shared__ int wblk[8];
+  __shared__ int bad_any;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) bad_any = 0;
+  __syncthreads();
+  int sz[4] = {0, 0, 0, 0};
+  int64_t rows = 0;
+  int blk = 0;
+  bool bad = false;
+  if (tid < 256) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int g = 4 * tid + i;
+      if (g < E) sz[i] = __ldg(sizes + g);
+      bad = bad || sz[i] < 0;
+      rows += sz[i];
+      if (g >= g0 && g < g0 + El && sz[i] > 0) blk += (sz[i] + kRB - 1) / kRB;
+    }
+    if (bad) bad_any = 1;
+  }
+  int64_t ir = rows;
+  int ib = blk;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t r = __shfl_up_sync(0xffffffffu, ir, o);
+    const int b = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ir += r;
+      ib += b;
+    }
+  }
+  if (warp < 8 && lane == 31) {
+    wrows[warp] = ir;
+    wblk[warp] = ib;
+  }
+  __syncthreads();
+  int64_t total = 0;
+  if (tid < 256) {
+    int64_t r = ir - rows;
+    int b = ib - blk;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) {
+        r += wrows[w];
+        b += wblk[w];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int local = 4 * tid + i - g0;
+      if (4 * tid + i < E && local >= 0 && local < El) {
+        t->start[local] = static_cast<int>(r);
+        t->kstart[local] = b;
+        if (sz[i] > 0) b += (sz[i] + kRB - 1) / kRB;
+        if (local == El - 1) {
+          t->start[El] = static_cast<int>(r + sz[i]);
+          t->kstart[El] = b;
+        }
+      }
+      r += sz[i];
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 8; ++w) total += wrows[w];
+  __syncthreads();
+  return !bad_any && total == M;
+}
+
+// ---- rounding ------------------------------------------------------------
+struct Operand {
+  const uint16_t* x;   // [src_rows, C]
+  const int32_t* idx;  // row m is x[idx[m] / k], or x[m] without
+  int k;
+  int64_t src_rows;
+  int C, ncb, nrb;     // columns; 128-column blocks; atoms a row block (a multiple of what a tile reads)
+  uint8_t* q;          // [row blocks][C][128]
+  uint8_t* sf;         // [row blocks][nrb][512]
+};
+
+// Power-of-two scale of a block from the bf16 bits of its largest magnitude:
+// the E8M0 code X + 127 and, through inv, 2^-X.
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float& inv) {
+  const int field = static_cast<int>(amax_bits >> 7), mant = static_cast<int>(amax_bits & 0x7F);
+  const int code = max(field - 8 + (mant > 0x60 ? 1 : 0), 0);  // X = field - 127 - 8 (+ 1 above 1.75 * 2^8)
+  inv = __uint_as_float(static_cast<uint32_t>(254 - code) << 23);
+  return static_cast<uint32_t>(code);
+}
+
+__global__ void __launch_bounds__(256, 3) round_rows_kernel(const Operand oa, const Operand ob, const int32_t* sizes,
+                                                            int E, int g0, int El, int64_t M) {
+  __shared__ Tables t;
+  __shared__ __align__(16) uint8_t sfs[2][kAtom];
+  if (!build_tables(sizes, E, g0, El, M, &t)) return;  // (the product's kernel raises the error)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // warp: 32 rows (warp & 3) of 64 columns (warp >> 2); lane: 8 rows, 8 columns
+  const int j = warp & 3, rl = lane >> 3, cu = (warp >> 2) * 64 + (lane & 7) * 8;
+  const int per = oa.ncb + ob.ncb;
+  const int64_t total = static_cast<int64_t>(t.kstart[El]) * per;
+  int sel = 0;
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x, sel ^= 1) {
+    const int kb = static_cast<int>(w / per);
+    int cb = static_cast<int>(w - static_cast<int64_t>(kb) * per);
+    const bool second = cb >= oa.ncb;
+    if (second) cb -= oa.ncb;
+    const Operand& o = second ? ob : oa;
+    int lo = 0, hi = El;  // the last group whose first block is <= kb: it is not empty
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (t.kstart[mid] <= kb) lo = mid; else hi = mid;
+    }
+    const int r0 = t.start[lo] + (kb - t.kstart[lo]) * kRB + 32 * j + 8 * rl;  // this thread's first row
+    const int nr = t.start[lo + 1] - r0;                                       // rows of the group from there on
+    const int c0 = cb * 128 + cu;
+    uint4 d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      d[i] = make_uint4(0, 0, 0, 0);
+      if (i < nr && c0 < o.C) {
+        int64_t row = r0 + i;
+        if (o.idx) {
+          const int p = __ldg(o.idx + row);
+          row = static_cast<int64_t>(static_cast<uint32_t>(p) / static_cast<uint32_t>(o.k));
+          if (p < 0 || row >= o.src_rows) {
+            raise_error(&g_err, MOE_DEVERR_BAD_POSITION);
+            continue;
+          }
+        }
+        d[i] = __ldg(reinterpret_cast<const uint4*>(o.x + row * o.C + c0));
+      }
+    }
+    // largest magnitude of each column over the 32 rows: bf16 magnitudes order
+    // like their bits
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[0] = __vmaxu2(m[0], d[i].x & 0x7FFF7FFFu);
+      m[1] = __vmaxu2(m[1], d[i].y & 0x7FFF7FFFu);
+      m[2] = __vmaxu2(m[2], d[i].z & 0x7FFF7FFFu);
+      m[3] = __vmaxu2(m[3], d[i].w & 0x7FFF7FFFu);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      m[c] = __vmaxu2(m[c], __shfl_xor_sync(0xffffffffu, m[c], 8));
+      m[c] = __vmaxu2(m[c], __shfl_xor_sync(0xffffffffu, m[c], 16));
+    }
+    uint8_t* q = o.q + (static_cast<int64_t>(kb) * o.C + c0) * kRB + 32 * j + 8 * rl;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float inv;
+      const uint32_t code = block_scale((c & 1) ? m[c >> 1] >> 16 : m[c >> 1] & 0xFFFFu, inv);
+      if (rl == 0) {
+        const int cc = cu + c;  // column of the 128
+        sfs[sel][16 * (cc & 31) + 4 * (cc >> 5) + j] = static_cast<uint8_t>(code);
+      }
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = (c >> 1) == 0 ? d[i].x : (c >> 1) == 1 ? d[i].y : (c >> 1) == 2 ? d[i].z : d[i].w;
+        v[i] = __fmul_rn((c & 1) ? bf16hi(x) : bf16lo(x), inv);  // exact: a power of two
+      }
+      if (c0 < o.C) *reinterpret_cast<uint2*>(q + c * kRB) = pack_e4m3x8(v);
+    }
+    __syncthreads();  // (the two buffers alternate: one barrier a tile)
+    if (tid < 32)
+      *reinterpret_cast<uint4*>(o.sf + (static_cast<int64_t>(kb) * o.nrb + cb) * kAtom + 16 * tid) =
+          *reinterpret_cast<const uint4*>(&sfs[sel][16 * tid]);
+  }
+}
+
+// ---- product -------------------------------------------------------------
+constexpr int kBM = 128, kBN = 256;
+constexpr int kStages = 4;
+constexpr int kABytes = kBM * kRB, kBBytes = kBN * kRB;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kSfBytes = 3 * kAtom;  // a stage's scale atoms: A's, B's two
+constexpr int kSfCols = 12, kSfCol0 = kBN;
+constexpr int kCtrlWarps = 4, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kCtrlWarps + kEpiWarps);
+static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
+
+struct Params {
+  const int32_t* group_sizes;
+  int E, g0, El;
+  int64_t M;
+  int K, N, ktiles, ntiles;
+  int nrb_a, nrb_b;
+  const uint8_t* sf_a;
+  const uint8_t* sf_b;
+  float* out;
+  uint64_t stall_ns;  // test hook (moe_test_stall_consumers): 0, or the wait limit in ns
+};
+
+struct Ctl {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t tfull, tempty, drain;
+  uint64_t never;  // test hook: a barrier that nothing arrives on
+  uint32_t tmem_base;
+  int abort_flag, no_abort, err;
+  Tables t;
+};
+constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kStageBytes + kSfBytes) + kCtlBytes;
+static_assert(kSmem <= 232448, "shared memory per CTA");
+
+struct Tile {
+  int el, kb0, rows, k0, n0;  // rows: of the expert
+};
+
+__device__ __forceinline__ Tile get_tile(const Params& p, const Ctl* c, int t) {
+  const int per = p.ktiles * p.ntiles;
+  Tile tl;
+  tl.el = t / per;
+  const int r = t - tl.el * per, nt = r / p.ktiles;
+  tl.k0 = (r - nt * p.ktiles) * kBM;
+  tl.n0 = nt * kBN;
+  tl.kb0 = c->t.kstart[tl.el];
+  tl.rows = c->t.start[tl.el + 1] - c->t.start[tl.el];
+  return tl;
+}
+
+__device__ __forceinline__ void store8(float* o, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(o) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(o + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    tgmm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* bp = smem_raw + (base - raw);
+  const uint32_t sf_ring = base + kStages * kStageBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(bp + kStages * (kStageBytes + kSfBytes));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&ctl->tfull), 1);
+    mbar_init(smem_u32(&ctl->tempty), kEpiWarps);
+    mbar_init(smem_u32(&ctl->drain), 1);
+    mbar_init(smem_u32(&ctl->never), 1);
+    ctl->abort_flag = 0;
+    ctl->no_abort = 0;
+    ctl->err = 0;
+    fence_mbar_init();
+  }
+  if (!build_tables(p.group_sizes, p.E, p.g0, p.El, p.M, &ctl->t)) {
+    if (threadIdx.x == 0) raise_error(&g_err, MOE_DEVERR_GROUP_SIZES);
+    return;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const int total = p.El * p.ktiles * p.ntiles;
+  volatile int* abort_flag = &ctl->abort_flag;
+  bool timed_out = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
+        const Tile tl = get_tile(p, ctl, t);
+        const int nkb = (tl.rows + kRB - 1) / kRB;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+            timed_out = true;
+            break;
+          }
+          const uint32_t fb = smem_u32(&ctl->full[s]), sa = base + s * kStageBytes, sf = sf_ring + s * kSfBytes;
+          const int g = tl.kb0 + kb;
+          mbar_arrive_expect_tx(fb, kStageBytes + kSfBytes);
+          // a tile's rows past the operand's last column are the next block's: never stored
+          tma_load_2d(sa, &tmA, 0, g * p.K + tl.k0, fb);
+          tma_load_2d(sa + kABytes, &tmB, 0, g * p.N + tl.n0, fb);
+          bulk_load(sf, p.sf_a + (static_cast<int64_t>(g) * p.nrb_a + tl.k0 / 128) * kAtom, kAtom, fb);
+          bulk_load(sf + kAtom, p.sf_b + (static_cast<int64_t>(g) * p.nrb_b + tl.n0 / 128) * kAtom, 2 * kAtom, fb);
+        }
+      }
+      if (timed_out) {
+        *abort_flag = 1;
+        ctl->err = 2;
+      }
+      // the last loads land before the CTA can exit, whichever role's wait ran out
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+        mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t it = 0, acc = 0;
+      for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
+        const Tile tl = get_tile(p, ctl, t);
+        const int nkb = (tl.rows + kRB - 1) / kRB;
+        if (nkb == 0) continue;
+        if (!mbar_wait_bounded(smem_u32(&ctl->tempty), (acc & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait_bounded(smem_u32(&ctl->full[s]), (it / kStages) & 1, abort_flag, kWaitLimitNs)) {
+            timed_out = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + s * kStageBytes, sf = sf_ring + s * kSfBytes, sft = tmem + kSfCol0 + s * kSfCols;
+          const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kABytes);
+          tmem_cp_32x128b_warpx4(sft, smem_desc_plain(sf));
+          tmem_cp_32x128b_warpx4(sft + 4, smem_desc_plain(sf + kAtom));
+          tmem_cp_32x128b_warpx4(sft + 8, smem_desc_plain(sf + 2 * kAtom));
+          const int nsub = min(4, (tl.rows - kb * kRB + 31) / 32);  // 32-row blocks that hold rows
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4)
+            if (k4 < nsub)
+              mma_mx(tmem, da + 2 * k4, db + 2 * k4, idesc_mx_e4m3(kBM, kBN, k4, k4), sft, sft + 4, kb > 0 || k4 > 0);
+          mma_commit(smem_u32(&ctl->empty[s]));
+        }
+        if (timed_out) break;
+        mma_commit(smem_u32(&ctl->tfull));
+        ++acc;
+      }
+      mma_commit(smem_u32(&ctl->drain));
+      if (!mbar_wait_bounded(smem_u32(&ctl->drain), 0, &ctl->no_abort, kWaitLimitNs)) timed_out = true;
+      if (timed_out) {
+        *abort_flag = 1;
+        ctl->err = 2;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kCtrlWarps) {
+    const int q4 = warp & 3, half = (warp - kCtrlWarps) >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + half * (kBN / 2);
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+    uint32_t acc = 0;
+    if (p.stall_ns && !mbar_wait_bounded_warp(smem_u32(&ctl->never), 0, abort_flag, p.stall_ns)) timed_out = true;
+    for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
+      const Tile tl = get_tile(p, ctl, t);
+      uint32_t v[4][32];
+      if (tl.rows > 0) {
+        if (!mbar_wait_bounded_warp(smem_u32(&ctl->tfull), acc & 1, abort_flag, kWaitLimitNs)) {
+          timed_out = true;
+          break;
+        }
+        ++acc;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(taddr + 32 * i, v[i]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty));
+      } else {  // an expert without rows: zeros
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[i][c] = 0;
+      }
+      const int k = tl.k0 + q4 * 32 + lane, n = tl.n0 + half * (kBN / 2);
+      if (k < p.K) {
+        float* o = p.out + (static_cast<int64_t>(tl.el) * p.K + k) * p.N + n;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (n + 8 * i < p.N) store8(o + 8 * i, &v[i >> 2][8 * (i & 3)], wide);
+      }
+    }
+    if (timed_out) {
+      *abort_flag = 1;
+      ctl->err = 2;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && ctl->err) raise_error(&g_err, MOE_DEVERR_TIMEOUT);
+}
+
+// ---- workspace -----------------------------------------------------------
+// 128-row blocks that any M rows in El groups can take, then both operands' codes
+// and scale atoms.
+struct Layout {
+  int64_t blocks;
+  int nrb_a, nrb_b;
+  int64_t q_a, q_b, sf_a, sf_b, bytes;
+};
+
+bool make_layout(int64_t M, int64_t K, int64_t N, int El, Layout* l) {
+  if (M < 0 || M >= (1ll << 31) - (1 << 18) || K <= 0 || K % 16 || K >= (1 << 30) || N <= 0 || N % 16 ||
+      N >= (1 << 30) || El <= 0 || El > kMaxGroups)
+    return false;
+  l->blocks = M == 0 ? 0 : (M - 1) / kRB + El;  // sum of ceil(size / 128), at the most
+  const int64_t most = std::max(K, N);
+  if (l->blocks > ((1ll << 31) - 1) / most - 1) return false;
+  l->nrb_a = static_cast<int>((K + 127) / 128);
+  l->nrb_b = static_cast<int>((N + 255) / 256) * 2;  // (a tile reads two)
+  l->q_a = 0;
+  l->q_b = l->q_a + l->blocks * K * kRB;
+  l->sf_a = l->q_b + l->blocks * N * kRB;
+  l->sf_b = l->sf_a + l->blocks * l->nrb_a * kAtom;
+  l->bytes = l->sf_b + l->blocks * l->nrb_b * kAtom;
+  return true;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" __attribute__((visibility("hidden"))) cudaError_t moe_detail_take_error_tgmm_mx(unsigned int* out) {
+  unsigned int v = 0, z = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_err, sizeof(v));
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_err, &z, sizeof(z));
+  *out = v;
+  return e;
+}
+
+extern "C" __attribute__((visibility("hidden"))) uint64_t moe_detail_stall_ns();
+
+extern "C" size_t tgmm_fp8_mx_workspace_bytes(int64_t M, int64_t K, int64_t N, int E_local) {
+  Layout l;
+  return make_layout(M, K, N, E_local, &l) ? static_cast<size_t>(std::max<int64_t>(l.bytes, 16)) : 0;
+}
+
+extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const int32_t* lhs_index, int k,
+                                  const uint16_t* rhs, const int32_t* group_sizes, int E, int group_offset,
+                                  int E_local, int64_t M, int64_t K, int64_t N, float* out, void* workspace,
+                                  size_t workspace_bytes, moe_stream_t stream) {
+  MOE_HOST_CHECK(lhs && rhs && group_sizes && out && workspace, MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(E > 0 && E <= kMaxGroups && group_offset >= 0 && E_local > 0 && E_local <= E - group_offset,
+                 MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(k > 0 && lhs_rows >= 0 && (lhs_index || (k == 1 && lhs_rows == M)), MOE_ERR_INVALID_ARG);
+  Layout l;
+  MOE_HOST_CHECK(make_layout(M, K, N, E_local, &l), MOE_ERR_INVALID_ARG);
+  MOE_HOST_CHECK(aligned16(lhs) && aligned16(rhs) && aligned16(out) && aligned16(workspace) &&
+                     workspace_bytes >= static_cast<size_t>(l.bytes),
+                 MOE_ERR_INVALID_ARG);
+  const int64_t ktiles = (K + kBM - 1) / kBM, ntiles = (N + kBN - 1) / kBN, total = E_local * ktiles * ntiles;
+  MOE_HOST_CHECK(total < (1ll << 31), MOE_ERR_INVALID_ARG);
+  const int sms = sm103_count();
+  if (sms <= 0) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t st = as_stream(stream);
+  if (M == 0) {
+    MOE_CUDA_TRY(cudaMemsetAsync(out, 0, static_cast<size_t>(E_local) * K * N * 4, st));
+    return MOE_OK;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  CUtensorMap A, B;
+  if (!make_map_u8(&A, ws + l.q_a, kRB, static_cast<uint64_t>(l.blocks) * K, kRB, kBM)) return MOE_ERR_CUDA;
+  if (!make_map_u8(&B, ws + l.q_b, kRB, static_cast<uint64_t>(l.blocks) * N, kRB, kBN)) return MOE_ERR_CUDA;
+  const Operand oa{lhs, lhs_index, k, lhs_rows, static_cast<int>(K), static_cast<int>((K + 127) / 128), l.nrb_a,
+                   ws + l.q_a, ws + l.sf_a};
+  const Operand ob{rhs, nullptr, 1, M, static_cast<int>(N), static_cast<int>((N + 127) / 128), l.nrb_b,
+                   ws + l.q_b, ws + l.sf_b};
+  const int64_t rounds = l.blocks * (oa.ncb + ob.ncb);
+  round_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(rounds, sms * 3)), 256, 0, st>>>(
+      oa, ob, group_sizes, E, group_offset, E_local, M);
+  MOE_CUDA_TRY(cudaGetLastError());
+  const Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(K), static_cast<int>(N),
+                 static_cast<int>(ktiles), static_cast<int>(ntiles), l.nrb_a, l.nrb_b, ws + l.sf_a, ws + l.sf_b, out,
+                 moe_detail_stall_ns()};
+  MOE_CUDA_TRY(cudaFuncSetAttribute(tgmm_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kSmem)));
+  tgmm_mx_kernel<<<static_cast<unsigned>(std::min<int64_t>(total, sms)), kThreads, kSmem, st>>>(A, B, p);
+  MOE_CUDA_TRY(cudaGetLastError());
+  return MOE_OK;
+}

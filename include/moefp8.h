@@ -101,8 +101,8 @@ int moe_num_sms(void);
  * Process-wide; not for production use. */
 void moe_test_stall_epilogue(uint64_t limit_ns);
 
-/* The same hook for gmm_fp4_mx (its epilogue warps) and moe_ffn_decode (its
- * contracting warps). */
+/* The same hook for gmm_fp4_mx, gmm_fp8_block and tgmm_fp8_mx (their epilogue warps)
+ * and moe_ffn_decode (its contracting warps). */
 void moe_test_stall_consumers(uint64_t limit_ns);
 
 /* ------------------------------------------------------------------------
@@ -396,6 +396,54 @@ moe_status moe_router_backward(const uint16_t* G, const uint16_t* o, const int32
                                int64_t D, int E, int k, float* dw, uint16_t* dlogits, float* grad_gate,
                                uint16_t* state_grad, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* moe_router_backward_aux -- moe_router_backward with another loss's gradient added
+ * to the logits' gradient before it is rounded:
+ *   dlogits[t, i] = bf16( p_i (g_i - s) + dlogits_aux[t, i] ),
+ * so that grad_gate and state_grad hold both.  dlogits_aux fp32 [T, E] (that of
+ * moe_router_balance_backward, say), or NULL. */
+moe_status moe_router_backward_aux(const uint16_t* G, const uint16_t* o, const int32_t* pos, const uint16_t* x,
+                                   const uint16_t* w_gate, const float* logits, const int32_t* topk_ids,
+                                   const float* dlogits_aux, int64_t T, int64_t D, int E, int k, float* dw,
+                                   uint16_t* dlogits, float* grad_gate, uint16_t* state_grad, void* workspace,
+                                   size_t workspace_bytes, moe_stream_t stream);
+
+/* Balance loss of the router.  The T rows are `seqs` sequences of L = T / seqs rows
+ * each, of which n_s are valid; p is the softmax of a row's logits.  For sequence s and
+ * expert e:
+ *   counts[s, e] = pairs (t, j) of valid rows with topk_ids[t, j] = e
+ *   mean[s, e]   = (1 / n_s) sum of p[t, e] over valid rows
+ *   loss         = coef / seqs * sum_s sum_e (E counts[s, e] / (k n_s)) mean[s, e]
+ * (1 times coef where pairs and probabilities are spread evenly.)  A sequence without a
+ * valid row has mean 0 and adds nothing.
+ *   logits    fp32 [T, E] (those of moe_router_topk); -inf closes an expert to a row;
+ *             a row of -inf alone has p = 0; NaN and +inf make a row's p NaN
+ *   topk_ids  int32 [T, k]; the same expert twice in a row counts twice; an id outside
+ *             [0, E) is not counted and sets MOE_DEVERR_BAD_EXPERT_ID
+ *   valid     one byte a row, zero: the row does not count (its logits and ids are not
+ *             read); NULL: all rows do
+ *   loss      fp32 [1]; counts int32 [seqs, E]; mean fp32 [seqs, E]; tokens int32
+ *             [seqs]: n_s
+ *   workspace moe_router_balance_workspace_bytes(T, E, k, seqs) bytes, 16-byte aligned
+ *             (no initialisation needed); calls that may overlap on the GPU need
+ *             workspaces of their own.
+ * Sums are fp32, in a fixed order: the same inputs give the same bits.
+ * T % seqs == 0, 1 <= seqs <= 2^20, 1 <= E <= 1024, 1 <= k <= 32, T * k < 2^31; logits
+ * 16-byte aligned. */
+size_t moe_router_balance_workspace_bytes(int64_t T, int E, int k, int64_t seqs);
+moe_status moe_router_balance(const float* logits, const int32_t* topk_ids, const uint8_t* valid, int64_t T, int E,
+                              int k, int64_t seqs, float coef, float* loss, int32_t* counts, float* mean,
+                              int32_t* tokens, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Its gradient, counts being constants: for a valid row t of sequence s
+ *   dlogits[t, e] = p_e (c_e - sum_j p_j c_j),
+ *   c_e = grad coef E counts[s, e] / (seqs k n_s^2),
+ * and zero for a row that is not.  counts and tokens as moe_router_balance gave them for
+ * the same logits, valid, k, seqs and coef; grad fp32 [1] (the loss's own gradient, a loss
+ * scale) or NULL (1); dlogits fp32 [T, E], 16-byte aligned; it may be logits. */
+moe_status moe_router_balance_backward(const float* logits, const uint8_t* valid, int64_t T, int E, int k,
+                                       int64_t seqs, float coef, const int32_t* counts, const int32_t* tokens,
+                                       const float* grad, float* dlogits, moe_stream_t stream);
+
 /* moe_transpose_u8 -- weight layout preparation for the backward pass (run
  * once, outside the FFN): batched byte transpose src [B, R, C] -> dst
  * [B, C, R] of e4m3 codes.  The input-gradient gmm contracts over the
@@ -583,6 +631,67 @@ moe_status gmm_fp8_w8(const uint8_t* lhs_q, const float* lhs_scale, moe_scale_mo
 /* Bytes of gmm_fp8_w8's optional workspace: 2 * M * K (0 for an empty or
  * out-of-range shape). */
 size_t gmm_fp8_w8_workspace_bytes(int64_t M, int64_t K);
+
+/* ------------------------------------------------------------------------
+ * Weights with one scale for each 128 x 128 block, forward and backward.  The
+ * activations and gradients that meet them carry one scale per row and 128 columns
+ * (MOE_SCALE_PER_ROW_BLOCK128).  Transposing such weights transposes their codes and
+ * scales, so the input gradient's product rounds them no second time.
+ * ------------------------------------------------------------------------ */
+
+/* w bf16 [E, N, K] -> q e4m3 [E, N, K] and scale fp32 [E, ceil(N / 128), K / 128]:
+ * scale = amax / 448 of the block (1 when amax = 0), q = e4m3(fp32(w / scale)), as
+ * moe_quantize_rows rounds.  q_t [E, K, N] and scale_t [E, K / 128, N / 128] (both or
+ * neither may be NULL): the transposed weights'.  K % 128 == 0; N % 128 == 0 with q_t;
+ * every pointer 16-byte aligned. */
+moe_status moe_quantize_weights_block(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, float* scale,
+                                      uint8_t* q_t, float* scale_t, moe_stream_t stream);
+
+/* Steps 3 / 5 and their input gradients on such weights:
+ *   out[m, n] = bf16( sum_kb s_a[m, kb] s_b[g(m), n / 128, kb]
+ *                     sum_{k in block kb} lhs_q[m, k] rhs_q[g(m), n, k] )
+ * fp32 accumulation: 128 products on the tensor cores, the blocks' sums scaled and
+ * added in fp32 registers.
+ *   lhs_q [M, K], lhs_scale [M, K / 128]; rhs_q [E_local, N, K], rhs_scale
+ *   [E_local, ceil(N / 128), K / 128]; out bf16 [M, N].
+ * Groups, group_offset and E_local are as in gmm_fp8: rows outside the local groups are
+ * zero.  group_sizes may be NULL with E = 1: one group of all rows (a dense product).
+ * K % 128 == 0, N % 16 == 0, E <= 1024; every pointer but group_sizes 16-byte aligned.
+ * MOE_ERR_UNSUPPORTED off sm_103. */
+moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale, const uint8_t* rhs_q, const float* rhs_scale,
+                         const int32_t* group_sizes, int E, int group_offset, int E_local, int64_t M, int64_t K,
+                         int64_t N, uint16_t* out, moe_stream_t stream);
+
+/* Weight gradient from the bf16 operands:
+ *   out[e, k, n] = sum_{m in group e} r(lhs)[m, k] r(rhs)[m, n]      (fp32)
+ * with r the rounding to e4m3 times a power of two that 32 consecutive rows of a group
+ * (from its first row on; fewer at its end) share in each column: 2^X, X the smallest
+ * integer, at least -127, with amax <= 448 * 2^X.  No finite value saturates.  The
+ * block-scaled tensor-core MMA applies both scales and accumulates in fp32.
+ *   lhs       bf16 [lhs_rows, K]; row m of the product's lhs is lhs[m] (lhs_index NULL, k =
+ *             1, lhs_rows = M) or lhs[lhs_index[m] / k] (int32 [M]: with sorted_src, the
+ *             tokens of the sorted pairs).  An index outside [0, lhs_rows * k) of a local
+ *             group's row stands for a row of zeros and sets MOE_DEVERR_BAD_POSITION.
+ *   rhs       bf16 [M, N]; out fp32 [E_local, K, N]; a group without rows gets zeros
+ *   workspace tgmm_fp8_mx_workspace_bytes(M, K, N, E_local) bytes, 16-byte aligned (no
+ *             initialisation needed): about M (K + N), each group padded to 128 rows;
+ *             calls that may overlap on the GPU need workspaces of their own.
+ * An infinity stands for 448 * 2^120, above fp32's range, and the finite values of its
+ * block round to zero beside it; a NaN makes every product it enters NaN.  K % 16 == 0, N % 16 == 0, E <= 1024; every pointer but lhs_index and
+ * group_sizes 16-byte aligned.  MOE_ERR_UNSUPPORTED off sm_103. */
+size_t tgmm_fp8_mx_workspace_bytes(int64_t M, int64_t K, int64_t N, int E_local);
+moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const int32_t* lhs_index, int k, const uint16_t* rhs,
+                       const int32_t* group_sizes, int E, int group_offset, int E_local, int64_t M, int64_t K,
+                       int64_t N, float* out, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_gather_scale_quant and moe_swiglu_bwd_quant with one scale per row and 128
+ * columns: dO_scale [T*k, D / 128], dA_scale [R, 2F / 128].  The second also gives h
+ * bf16 [R, F] = bf16(silu(a0) a1), which wo's gradient contracts.  D % 128 == 0;
+ * F % 128 == 0, 2F <= 32768. */
+moe_status moe_gather_scale_quant_block(const uint16_t* G, const float* w, const int32_t* sorted_src, int64_t T, int k,
+                                        int64_t D, uint16_t* dO, uint8_t* dO_q, float* dO_scale, moe_stream_t stream);
+moe_status moe_swiglu_bwd_quant_block(const uint16_t* dH, const uint16_t* a, int64_t R, int64_t F, uint16_t* dA,
+                                      uint8_t* dA_q, float* dA_scale, uint16_t* h, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The expert FFN of a decoding step (a few tokens), in one cooperative kernel:
