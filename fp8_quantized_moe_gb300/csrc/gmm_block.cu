@@ -12,23 +12,39 @@
 // (its row, its warp's 128 channels): one fused multiply-add an element and block,
 // and no scale is read per element.
 //
-// Bound.  A pair of CTAs works on 256 x 256 tiles, 128 rows a CTA; a K block is
-// four M = 256, N = 256, K = 32 tcgen05.mma.kind::f8f6f4 of the pair, 554 clocks at
-// their measured rate, and the fold takes 256 clocks of each SM's fp32 pipes and the
-// reading of 128 KB of tensor memory beside it.
-//
-// Layout of a CTA (12 warps, one CTA per SM, persistent):
-//   warp 0      TMA producer: this CTA's 128 A rows and its half (128 rows) of the
-//               B tile per stage, 32 KB, six stages, 128-byte swizzle.
-//   warp 1      of the pair's even CTA: MMA issuer.
+// Layout of a CTA (12 warps, one CTA per SM, 128 x 256 tiles):
+//   warp 0      TMA producer: 128 A rows and 256 B rows of 128 bytes per stage, 48 KB,
+//               four stages, 128-byte swizzle.
+//   warp 1      MMA issuer: four M = 128, N = 256, K = 32 tcgen05.mma.kind::f8f6f4 a block.
 //   warps 4..11 epilogue: warp w has tensor-memory lanes 32 (w % 4).. (rows) and
 //               128 of the tile's columns: 128 running sums a thread.
-// Two 256-column accumulators take alternate K blocks.  Row and block scales come
-// straight to registers, four K blocks at a time and four blocks ahead.
+// Two 256-column accumulators take alternate K blocks.
 //
 // Tiles run expert-major, then N tile, then M tile: CTAs that run together share
 // an expert's weights.  A group's M tiles start at its first row; rows past its end
 // are computed and not stored.
+//
+// Few tiles (SPLIT: two CTAs a tile still fit on the device): a cluster of 2, 4 or 8 CTAs
+// shares a tile, each with a part of the K blocks; the partial tiles meet in shared
+// memory (the stages', which are done with) and every CTA adds up and stores a slice of
+// the columns, in the order of the CTAs.
+//
+// Bound and measurements.  A block is 554 clocks of MMA at the measured rate; the same
+// loop without any fold takes 730-760 (both accumulators handed back and forth: the two
+// are not enough to hide the way from commit to epilogue and back), with it 860-870, 2.4 to
+// 2.6 PFLOP/s where the plain product of gmm_fp8 (one accumulator a tile) has 3.1 to 3.4.
+// Measured on 49152 x 4096 x 7168, 64 of 96 groups: 851 us; 16384 x 4096 x 28672, 8 groups:
+// 1.50 ms; 16384 x 1536 x 2048 over 128 groups 109 us (floor of its bytes: 72).  On the way there:
+//   - tensor-memory loads of 16 columns, two at a time, against 32 columns: 2.4 against
+//     1.7 PFLOP/s (32 registers in a row cost moves and spills);
+//   - the epilogue's waits sleeping in the barrier (a suspend-time hint) against polling:
+//     5 %; polling without pause made even the loop without a fold 20 % slower: the
+//     polls take shared memory's time from the MMA's operands;
+//   - pairs of CTAs on 256 x 256 tiles (half of B each): 1.55 against 1.50 ms on the large groups,
+//     906 against 851 us on ragged ones (256-row tiles leave more rows empty);
+//   - four accumulators of 128 columns (N = 128 MMAs read A twice as often): 1.93 ms;
+//   - 16 epilogue warps of 64 columns: 1.69 ms; the next block's first columns loaded
+//     before a block's last sums: 1.74 ms.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets what
 // it issued finish and returns.
@@ -40,12 +56,13 @@ namespace {
 __device__ unsigned int g_err;
 
 constexpr int kBM = 128, kBN = 256, kBK = 128;
-constexpr int kStages = 6;
-constexpr int kABytes = kBM * kBK, kBBytes = kBN / 2 * kBK;
+constexpr int kStages = 4;
+constexpr int kABytes = kBM * kBK, kBBytes = kBN * kBK;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kCtrlWarps = 4, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kCtrlWarps + kEpiWarps);
-// registers a thread: 168 at launch, handed from the control warpgroup to the epilogue
+// registers a thread: 168 at launch (a 384-thread CTA alone on its SM), handed from the
+// control warpgroup to the epilogue
 constexpr uint32_t kCtrlRegs = 40, kEpiRegs = 232;
 static_assert(128 * kCtrlRegs + 256 * kEpiRegs <= 168 * kThreads, "register split");
 
@@ -63,17 +80,19 @@ struct Params {
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t tfull[2], tempty[2], drain;
+  uint64_t pfull;  // SPLIT: every CTA's partial tile is in its shared memory
   uint64_t never;  // test hook: a barrier that nothing arrives on
   uint32_t tmem_base;
   int abort_flag, no_abort, err, total;
-  int start[kMaxGroups + 1], prefix[kMaxGroups + 1];  // local groups' first rows and units; the last: their ends
+  int start[kMaxGroups + 1], prefix[kMaxGroups + 1];  // local groups' first rows and tiles; the last: their ends
 };
 constexpr size_t kCtlBytes = (sizeof(Ctl) + 127) / 128 * 128;
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kCtlBytes;
 static_assert(kSmem <= 232448, "shared memory per CTA");
+static_assert(kStages * kStageBytes >= kBM * kBN * 4, "SPLIT: a partial tile in the stages");
 
-// Local groups' first rows and first units (pairs of M tiles times N tiles), by
-// warp 0 (any size negative or a sum other than M: err).
+// Local groups' first rows and first tiles, by warp 0 (any size
+// negative or a sum other than M: err).
 __device__ void build_tables(const Params& p, Ctl* c) {
   const int lane = threadIdx.x & 31;
   int64_t rows = 0;
@@ -85,7 +104,7 @@ __device__ void build_tables(const Params& p, Ctl* c) {
     bad = bad || sz < 0;
     const bool mine = g < p.E && local >= 0 && local < p.El;
     int64_t ir = sz;
-    const int nu = mine && sz > 0 ? (sz + 2 * kBM - 1) / (2 * kBM) * p.ntiles : 0;
+    const int nu = mine && sz > 0 ? (sz + kBM - 1) / kBM * p.ntiles : 0;
     int iu = nu;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -113,73 +132,78 @@ __device__ void build_tables(const Params& p, Ctl* c) {
 }
 
 struct Tile {
-  int el, row0, rows, n0;  // rows <= 0: the odd CTA of a pair past the group's end
+  int el, row0, rows, n0;
 };
 
-__device__ __forceinline__ Tile get_tile(const Params& p, const Ctl* c, int t, int rank) {
-  int lo = 0, hi = p.El;  // the last group whose first unit is <= t: it is not empty
+__device__ __forceinline__ Tile get_tile(const Params& p, const Ctl* c, int t) {
+  int lo = 0, hi = p.El;  // the last group whose first tile is <= t: it is not empty
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (c->prefix[mid] <= t) lo = mid; else hi = mid;
   }
   Tile tl;
   tl.el = lo;
-  const int sz = c->start[lo + 1] - c->start[lo], mp = (sz + 2 * kBM - 1) / (2 * kBM), local = t - c->prefix[lo];
-  const int nt = local / mp, mi = 2 * (local - nt * mp) + rank;
+  const int sz = c->start[lo + 1] - c->start[lo], mt = (sz + kBM - 1) / kBM, local = t - c->prefix[lo];
+  const int nt = local / mt, mi = local - nt * mt;
   tl.row0 = c->start[lo] + mi * kBM;
   tl.rows = min(kBM, sz - mi * kBM);
   tl.n0 = nt * kBN;
   return tl;
 }
 
-// 32 lanes x 32 columns of tensor memory as 16 packed fp32 pairs a thread.
-__device__ __forceinline__ void tmem_ld_x32_pairs(uint32_t taddr, uint64_t (&r)[16]) {
-  asm volatile(
-      "{\n\t.reg .b32 t<32>;\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, "
-      "t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n\t"
-      "mov.b64 %0, {t0, t1};\n\tmov.b64 %1, {t2, t3};\n\tmov.b64 %2, {t4, t5};\n\tmov.b64 %3, {t6, t7};\n\t"
-      "mov.b64 %4, {t8, t9};\n\tmov.b64 %5, {t10, t11};\n\tmov.b64 %6, {t12, t13};\n\tmov.b64 %7, {t14, t15};\n\t"
-      "mov.b64 %8, {t16, t17};\n\tmov.b64 %9, {t18, t19};\n\tmov.b64 %10, {t20, t21};\n\tmov.b64 %11, {t22, t23};\n\t"
-      "mov.b64 %12, {t24, t25};\n\tmov.b64 %13, {t26, t27};\n\tmov.b64 %14, {t28, t29};\n\tmov.b64 %15, {t30, t31};\n\t}"
-      : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]), "=l"(r[7]), "=l"(r[8]),
-        "=l"(r[9]), "=l"(r[10]), "=l"(r[11]), "=l"(r[12]), "=l"(r[13]), "=l"(r[14]), "=l"(r[15])
-      : "r"(taddr)
-      : "memory");
+// The epilogue's wait: one outcome for the whole warp, asleep in the barrier.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded_idle(bar, parity, abort_flag, kWaitLimitNs));
 }
-// The loads have landed; the values are used only after it.
-__device__ __forceinline__ void tmem_wait_ld_pairs(uint64_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+l"(r[0]), "+l"(r[1]), "+l"(r[2]), "+l"(r[3]), "+l"(r[4]), "+l"(r[5]), "+l"(r[6]), "+l"(r[7]),
-                 "+l"(r[8]), "+l"(r[9]), "+l"(r[10]), "+l"(r[11]), "+l"(r[12]), "+l"(r[13]), "+l"(r[14]), "+l"(r[15])
-               :
+
+// The same for writes of other CTAs of the cluster (acquire at cluster scope).
+__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  auto attempt = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  bool ok = attempt();
+  const uint64_t t0 = globaltimer_ns();
+  while (!ok && !*abort_flag && globaltimer_ns() - t0 <= kWaitLimitNs) ok = attempt();
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
                : "memory");
+  return v;
 }
 
-// Scales of K blocks kb .. kb + 3 (past the last: not read).
-__device__ __forceinline__ void load_scales4(const float* s, int kb, int nkb, bool vec, float (&v)[4]) {
-  if (vec) {
-    const float4 f = __ldg(reinterpret_cast<const float4*>(s + kb));
-    v[0] = f.x;
-    v[1] = f.y;
-    v[2] = f.z;
-    v[3] = f.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = kb + j < nkb ? __ldg(s + kb + j) : 0.f;
-  }
+// 16-byte unit u (columns 4 u..) of row r of a partial tile: units swizzled by row, so that
+// eight rows' (a thread's each) stores meet no bank twice.
+__device__ __forceinline__ uint32_t part_offset(int r, int u) {
+  return static_cast<uint32_t>(r * (kBN * 4) + ((u ^ (r & 7)) << 4));
 }
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     gmm_block_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (base - raw) + kStages * kStageBytes);
+  uint8_t* bp = smem_raw + (base - raw);
+  Ctl* ctl = reinterpret_cast<Ctl*>(bp + kStages * kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // a pair works on one sequence of units; its even CTA (rank 0) issues the MMAs
-  // and owns the full and accumulator-empty barriers
-  const int rank = static_cast<int>(__clusterRelativeBlockRank());
-  const int unit0 = static_cast<int>(__clusterIdx().x), units = static_cast<int>(__clusterGridDimInClusters().x);
+  // SPLIT: a cluster has one tile, this CTA the K blocks [kb_lo, kb_hi) of it
+  const int rank = SPLIT ? static_cast<int>(__clusterRelativeBlockRank()) : 0;
+  const int parts = SPLIT ? static_cast<int>(__clusterSizeInBlocks()) : 1;
+  const int t0 = SPLIT ? static_cast<int>(__clusterIdx().x) : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? (1 << 30) : static_cast<int>(gridDim.x);
+  const int kb_lo = SPLIT ? rank * p.nkb / parts : 0, kb_hi = SPLIT ? (rank + 1) * p.nkb / parts : p.nkb;
 
   if (warp == 0) build_tables(p, ctl);
   if (threadIdx.x == 32) {
@@ -189,8 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&ctl->tfull[a]), 1);
-      mbar_init(smem_u32(&ctl->tempty[a]), 2 * kEpiWarps);
+      mbar_init(smem_u32(&ctl->tempty[a]), kEpiWarps);
     }
+    mbar_init(smem_u32(&ctl->pfull), static_cast<uint32_t>(parts * kEpiWarps));
     mbar_init(smem_u32(&ctl->drain), 1);
     mbar_init(smem_u32(&ctl->never), 1);
     ctl->abort_flag = 0;
@@ -198,28 +223,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   __syncthreads();
-  // both CTAs of a pair read the same group sizes, so they leave here together
+  // the CTAs of a cluster read the same group sizes, so they leave here together
   if (ctl->err) {
     if (threadIdx.x == 0) raise_error(&g_err, MOE_DEVERR_GROUP_SIZES);
     return;
   }
+  if (SPLIT && t0 >= ctl->total) return;  // (and here)
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
-    tmem_relinquish_pair();
+    tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
   tc_fence_before();
-  // the peer's barriers are initialised and its columns allocated before any
-  // operand, commit or release crosses between the two CTAs
-  cluster_sync_all();
+  if (SPLIT) cluster_sync_all(); else __syncthreads();  // (a peer's pfull is initialised before it is arrived on)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  if (rank == 1 && threadIdx.x == 0 &&
-      ld_shared_cluster_u32(mapa_shared(smem_u32(&ctl->tmem_base), 0)) != tmem)
-    raise_error(&g_err, MOE_DEVERR_TMEM);  // the pair's accumulators would not line up
   const int total = ctl->total;
   volatile int* abort_flag = &ctl->abort_flag;
   bool timed_out = false;
@@ -229,48 +250,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       if (lane == 0) {
         uint32_t it = 0;
-        for (int t = unit0; t < total && !timed_out; t += units) {
-          const Tile tl = get_tile(p, ctl, t, rank);
-          const int brow = tl.el * p.N + tl.n0 + rank * (kBN / 2);
-          for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        for (int t = t0; t < total && !timed_out; t += step) {
+          const Tile tl = get_tile(p, ctl, t);
+          const int brow = tl.el * p.N + tl.n0;
+          for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
             const int s = it % kStages;
             if (!mbar_wait_bounded_idle(smem_u32(&ctl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
               timed_out = true;
               break;
             }
-            const uint32_t sa = base + s * kStageBytes;
-            // both CTAs' boxes complete on the even CTA's full barrier
-            const uint32_t fb = mapa_shared(smem_u32(&ctl->full[s]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl->full[s]), 2 * kStageBytes);
-            tma_load_2d_pair(sa, &tmA, kb * kBK, tl.row0, fb);
-            tma_load_2d_pair(sa + kABytes, &tmB, kb * kBK, brow, fb);
+            const uint32_t sa = base + s * kStageBytes, fb = smem_u32(&ctl->full[s]);
+            mbar_arrive_expect_tx(fb, kStageBytes);
+            tma_load_2d(sa, &tmA, kb * kBK, tl.row0, fb);
+            tma_load_2d(sa + kABytes, &tmB, kb * kBK, brow, fb);
           }
         }
         if (timed_out) {
           *abort_flag = 1;
           ctl->err = 2;
         }
-        // The last loads land before the CTAs can exit, whichever role's wait ran
-        // out.  The even CTA's barriers count both CTAs' loads; a load of the odd
-        // one that the even one never announced lands within microseconds.
-        if (rank == 0) {
-          for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-            mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1, &ctl->no_abort,
-                              ctl->err ? kWaitLimitNs / 8 : kWaitLimitNs);
-        } else if (timed_out) {
-          mbar_wait_bounded(smem_u32(&ctl->never), 0, &ctl->no_abort, 1000000ull);
-        }
+        // the last loads land before the CTA can exit, whichever role's wait ran out
+        for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+          mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
       }
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0 && rank == 0) {
+      if (lane == 0) {
         uint32_t it = 0;
-        for (int t = unit0; t < total && !timed_out; t += units) {
-          for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        for (int t = t0; t < total && !timed_out; t += step) {
+          for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
             const int s = it % kStages;
             const uint32_t a = it & 1;
-            if (!mbar_wait_bounded(smem_u32(&ctl->full[s]), (it / kStages) & 1, abort_flag, kWaitLimitNs) ||
-                !mbar_wait_bounded(smem_u32(&ctl->tempty[a]), ((it >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+            if (!mbar_wait_bounded_idle(smem_u32(&ctl->full[s]), (it / kStages) & 1, abort_flag, kWaitLimitNs) ||
+                !mbar_wait_bounded_idle(smem_u32(&ctl->tempty[a]), ((it >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
               timed_out = true;
               break;
             }
@@ -279,12 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kABytes);
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4)  // 32 bytes of K: 2 in the descriptors' 16-byte units
-              mma_f8_pair(tmem + a * kBN, da + 2 * k4, db + 2 * k4, idesc_e4m3_f32(2 * kBM, kBN), k4 > 0);
-            mma_commit_pair_mc(smem_u32(&ctl->empty[s]), 0x3);  // frees the stage in both CTAs
-            mma_commit_pair_mc(smem_u32(&ctl->tfull[a]), 0x3);
+              mma_f8(tmem + a * kBN, da + 2 * k4, db + 2 * k4, idesc_e4m3_f32(kBM, kBN), k4 > 0);
+            mma_commit(smem_u32(&ctl->empty[s]));
+            mma_commit(smem_u32(&ctl->tfull[a]));
           }
         }
-        mma_commit_pair(smem_u32(&ctl->drain));
+        mma_commit(smem_u32(&ctl->drain));
         if (!mbar_wait_bounded(smem_u32(&ctl->drain), 0, &ctl->no_abort, kWaitLimitNs)) timed_out = true;
         if (timed_out) {
           *abort_flag = 1;
@@ -295,77 +307,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     setmaxnreg_inc<kEpiRegs>();
-    const int q4 = warp & 3, half = (warp - kCtrlWarps) >> 2;
+    const int q4 = warp & 3, half = (warp - kCtrlWarps) >> 2, r = q4 * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + half * (kBN / 2);
-    const bool vec = (p.nkb & 3) == 0;  // every row's scales start on 16 bytes
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     uint32_t it = 0;
     if (p.stall_ns && !mbar_wait_bounded_warp(smem_u32(&ctl->never), 0, abort_flag, p.stall_ns)) timed_out = true;
-    for (int t = unit0; t < total && !timed_out; t += units) {
-      const Tile tl = get_tile(p, ctl, t, rank);
-      const int r = q4 * 32 + lane, nb = min(tl.n0 / kBK + half, p.nblk - 1);
-      const bool work = tl.rows > q4 * 32 && tl.n0 + half * (kBN / 2) < p.N;  // (of the warp)
-      // a row past the group's end takes the scales of its last one (an odd CTA past
-      // it: of any row)
-      const int64_t srow = tl.rows > 0 ? tl.row0 + min(r, tl.rows - 1) : 0;
-      const float* sa = p.lhs_s + srow * p.nkb;
-      const float* sb = p.rhs_s + (static_cast<int64_t>(tl.el) * p.nblk + nb) * p.nkb;
+    for (int t = t0; t < total && !timed_out; t += step) {
+      const Tile tl = get_tile(p, ctl, t);
+      // (a row past the group's end takes its last one's scales, channels past N the last block's)
+      const float* sa = p.lhs_s + static_cast<int64_t>(tl.row0 + min(r, tl.rows - 1)) * p.nkb;
+      const float* sb = p.rhs_s + (static_cast<int64_t>(tl.el) * p.nblk + min(tl.n0 / kBK + half, p.nblk - 1)) * p.nkb;
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      float na[4], nw[4];
-      load_scales4(sa, 0, p.nkb, vec, na);
-      load_scales4(sb, 0, p.nkb, vec, nw);
-      for (int kb0 = 0; kb0 < p.nkb && !timed_out; kb0 += 4) {
-        float s4[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s4[j] = __fmul_rn(na[j], nw[j]);
-        if (kb0 + 4 < p.nkb) {
-          load_scales4(sa, kb0 + 4, p.nkb, vec, na);
-          load_scales4(sb, kb0 + 4, p.nkb, vec, nw);
+      // the next block's scale is asked for a block ahead
+      float next = __fmul_rn(__ldg(sa + kb_lo), __ldg(sb + kb_lo));
+#pragma unroll 1
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        const uint64_t s2 = f2_pack(next, next);
+        if (kb + 1 < kb_hi) next = __fmul_rn(__ldg(sa + kb + 1), __ldg(sb + kb + 1));
+        const uint32_t a = it & 1;
+        if (!wait_warp(smem_u32(&ctl->tfull[a]), (it >> 1) & 1, abort_flag)) {
+          timed_out = true;
+          break;
         }
+        ++it;
+        tc_fence_after();
+        const uint32_t ta = taddr + a * kBN;
+        // two loads of 16 columns in flight while two are added up; the accumulator
+        // goes back before the last two are
+        uint64_t u[4][8];
+        tmem_ld_32x32b_x16_pairs(ta, u[0]);
+        tmem_ld_32x32b_x16_pairs(ta + 16, u[1]);
+        tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (kb0 + j >= p.nkb) break;
-          const uint32_t a = it & 1;
-          if (!mbar_wait_bounded_warp(smem_u32(&ctl->tfull[a]), (it >> 1) & 1, abort_flag, kWaitLimitNs)) {
-            timed_out = true;
-            break;
+        for (int c = 0; c < 4; ++c) {
+          const int x = 2 * (c & 1), y = 2 - x;
+          if (c < 3) {
+            tmem_ld_32x32b_x16_pairs(ta + 32 * (c + 1), u[y]);
+            tmem_ld_32x32b_x16_pairs(ta + 32 * (c + 1) + 16, u[y + 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[a]));
           }
-          ++it;
-          tc_fence_after();
-          const uint32_t ta = taddr + a * kBN;
-          const uint64_t s2 = f2_pack(s4[j], s4[j]);
-          uint64_t u[16], v[16];
-          if (work) {
-            tmem_ld_x32_pairs(ta, u);
-            tmem_wait_ld_pairs(u);
-            tmem_ld_x32_pairs(ta + 32, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = f2_fma(u[i], s2, acc[i]);
-            tmem_wait_ld_pairs(v);
-            tmem_ld_x32_pairs(ta + 64, u);
+          for (int i = 0; i < 8; ++i) acc[16 * c + i] = f2_fma(u[x][i], s2, acc[16 * c + i]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[16 + i] = f2_fma(v[i], s2, acc[16 + i]);
-            tmem_wait_ld_pairs(u);
-            tmem_ld_x32_pairs(ta + 96, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[32 + i] = f2_fma(u[i], s2, acc[32 + i]);
-            tmem_wait_ld_pairs(v);
-          }
-          tc_fence_before();
-          __syncwarp();
-          // (relaxed: it orders only tensor-memory loads that have completed)
-          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctl->tempty[a]), 0));
-          if (work) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[48 + i] = f2_fma(v[i], s2, acc[48 + i]);
-          }
+          for (int i = 0; i < 8; ++i) acc[16 * c + 8 + i] = f2_fma(u[x + 1][i], s2, acc[16 * c + 8 + i]);
+          if (c < 3) tmem_wait_ld();
         }
       }
       if (timed_out) break;
-      if (r < tl.rows) {
-        uint16_t* o = p.out + (tl.row0 + r) * static_cast<int64_t>(p.N) + tl.n0 + half * (kBN / 2);
+      if (SPLIT) {
+        // Partial tiles into the stages (every load has landed and every MMA read them:
+        // the last accumulator was full), then slices of columns from all of them.
+        if (r < tl.rows) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float x, y, z, w;
+            f2_unpack(acc[2 * j], x, y);
+            f2_unpack(acc[2 * j + 1], z, w);
+            *reinterpret_cast<float4*>(bp + part_offset(r, 32 * half + j)) = make_float4(x, y, z, w);
+          }
+        }
+        __syncwarp();
+        if (lane < parts) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->pfull), lane));
+        if (!wait_warp_cluster(smem_u32(&ctl->pfull), 0, abort_flag)) {
+          timed_out = true;
+          break;
+        }
+        const int cols = kBN / parts, per = cols / 8;  // 8 columns: 16 bytes of bf16
+        for (int i = threadIdx.x - 32 * kCtrlWarps; i < tl.rows * per; i += 32 * kEpiWarps) {
+          const int row = i / per, c = rank * cols + 8 * (i - row * per);
+          if (tl.n0 + c >= p.N) continue;
+          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          for (int q = 0; q < parts; ++q) {
+            const float4 lo = ld_cluster_f4(mapa_shared(base + part_offset(row, c / 4), q));
+            const float4 hi = ld_cluster_f4(mapa_shared(base + part_offset(row, c / 4 + 1), q));
+            v[0] += lo.x;
+            v[1] += lo.y;
+            v[2] += lo.z;
+            v[3] += lo.w;
+            v[4] += hi.x;
+            v[5] += hi.y;
+            v[6] += hi.z;
+            v[7] += hi.w;
+          }
+          *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(tl.row0 + row) * p.N + tl.n0 + c) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        }
+      } else if (r < tl.rows) {
+        uint16_t* o = p.out + static_cast<int64_t>(tl.row0 + r) * p.N + tl.n0 + half * (kBN / 2);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // 16 columns: one 32-byte sector of the row
           if (tl.n0 + half * (kBN / 2) + 16 * i >= p.N) break;
@@ -394,12 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
-  // neither CTA leaves (or frees its columns) while the other may still write its
-  // tensor memory or arrive on its barriers
-  cluster_sync_all();
+  if (SPLIT) cluster_sync_all(); else __syncthreads();  // (no CTA leaves while a peer reads its part)
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && ctl->err) raise_error(&g_err, MOE_DEVERR_TIMEOUT);
 }
@@ -431,57 +463,44 @@ extern "C" moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale
   MOE_HOST_CHECK(aligned16(lhs_q) && aligned16(lhs_scale) && aligned16(rhs_q) && aligned16(rhs_scale) && aligned16(out),
                  MOE_ERR_INVALID_ARG);
   const int64_t ntiles = (N + kBN - 1) / kBN;
-  const int64_t max_units = ((M + 2 * kBM - 1) / (2 * kBM) + E_local) * ntiles;
-  MOE_HOST_CHECK(max_units < (1ll << 31), MOE_ERR_INVALID_ARG);
+  const int64_t most = ((M + kBM - 1) / kBM + E_local) * ntiles;  // tiles, at the most
+  MOE_HOST_CHECK(most < (1ll << 31), MOE_ERR_INVALID_ARG);
   const int sms = sm103_count();
   if (sms <= 0) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   cudaStream_t st = as_stream(stream);
   CUtensorMap A, B;
   if (!make_map_u8(&A, lhs_q, K, M, K, kBM)) return MOE_ERR_CUDA;
-  if (!make_map_u8(&B, rhs_q, K, static_cast<uint64_t>(E_local) * N, K, kBN / 2)) return MOE_ERR_CUDA;
-  Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(N), static_cast<int>(K / 128),
-           static_cast<int>(ntiles), static_cast<int>((N + 127) / 128), lhs_scale, rhs_scale, out,
-           moe_detail_stall_ns()};
-  MOE_CUDA_TRY(cudaFuncSetAttribute(gmm_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kSmem)));
+  if (!make_map_u8(&B, rhs_q, K, static_cast<uint64_t>(E_local) * N, K, kBN)) return MOE_ERR_CUDA;
+  const Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(N), static_cast<int>(K / 128),
+                 static_cast<int>(ntiles), static_cast<int>((N + 127) / 128), lhs_scale, rhs_scale, out,
+                 moe_detail_stall_ns()};
+  // CTAs a tile: as many as the device holds, no more than there are K blocks
+  int parts = 1;
+  while (parts < 8 && 2 * parts * most <= sms && 2 * parts <= p.nkb) parts *= 2;
+  auto kernel = parts > 1 ? gmm_block_kernel<true> : gmm_block_kernel<false>;
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
+  if (E_local < E) {
+    zero_outside_rows_kernel<<<sms * 4, 256, 0, st>>>(out, M, N, group_sizes, E, group_offset, E_local);
+    MOE_CUDA_TRY(cudaGetLastError());
+  }
+  if (parts == 1) {
+    kernel<<<static_cast<unsigned>(most < sms ? most : sms), kThreads, kSmem, st>>>(A, B, p);
+    MOE_CUDA_TRY(cudaGetLastError());
+    return MOE_OK;
+  }
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(parts * most));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // pairs that are resident at once, per device
-  static std::mutex mu;
-  static int resident[kMaxDevices] = {};
-  int dev = 0, pairs = 0;
-  MOE_CUDA_TRY(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    pairs = resident[dev];
-  }
-  if (pairs == 0) {
-    // the register split may only hand out what the CTA is launched with
-    cudaFuncAttributes fa{};
-    MOE_CUDA_TRY(cudaFuncGetAttributes(&fa, gmm_block_kernel));
-    if (static_cast<int64_t>(fa.numRegs) * kThreads < 128ll * kCtrlRegs + 256ll * kEpiRegs) return MOE_ERR_UNSUPPORTED;
-    cfg.gridDim = dim3(2 * (sms / 2));
-    MOE_CUDA_TRY(cudaOccupancyMaxActiveClusters(&pairs, gmm_block_kernel, &cfg));
-    if (pairs <= 0) return MOE_ERR_UNSUPPORTED;
-    std::lock_guard<std::mutex> lock(mu);
-    resident[dev] = pairs;
-  }
-  if (E_local < E) {
-    zero_outside_rows_kernel<<<sms * 4, 256, 0, st>>>(out, M, N, group_sizes, E, group_offset, E_local);
-    MOE_CUDA_TRY(cudaGetLastError());
-  }
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(max_units < pairs ? max_units : pairs));
-  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, gmm_block_kernel, A, B, p));
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, A, B, p));
   return MOE_OK;
 }

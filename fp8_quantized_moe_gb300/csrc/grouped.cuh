@@ -1,6 +1,5 @@
 // What the grouped kernels on block-scaled 8-bit operands share: tensor maps,
-// device queries, launches of CTA pairs, and the rows that belong to no local
-// group.  (Included by several translation units; everything is local to each.)
+// device queries, and the rows that belong to no local group.  (Included by several translation units; everything is local to each.)
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -13,7 +12,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxGroups = 1024;
-constexpr int kMaxDevices = 256;  // host-side per-device caches
 
 // Rows of out (bf16 [M, N]) before the first and after the last local group: zeros.
 __global__ void __launch_bounds__(256) zero_outside_rows_kernel(uint16_t* out, int64_t M, int64_t N,
