@@ -18,13 +18,13 @@
 //   warp 1      MMA issuer: four M = 128, N = 256, K = 32 tcgen05.mma.kind::f8f6f4 a block.
 //   warps 4..11 epilogue: warp w has tensor-memory lanes 32 (w % 4).. (rows) and
 //               128 of the tile's columns: 128 running sums a thread.
-// Two 256-column accumulators take alternate K blocks.
+// The producing and issuing warps run with all lanes (wait_uniform).  Two 256-column accumulators take alternate K blocks.
 //
 // Tiles run expert-major, then N tile, then M tile: CTAs that run together share
 // an expert's weights.  A group's M tiles start at its first row; rows past its end
 // are computed and not stored.
 //
-// Few tiles (SPLIT: two CTAs a tile still fit on the device): a cluster of 2, 4 or 8 CTAs
+// Few tiles (SPLIT): a cluster of 2, 4 or 8 CTAs
 // shares a tile, each with a part of the K blocks; the partial tiles meet in shared
 // memory (the stages', which are done with) and every CTA adds up and stores a slice of
 // the columns, in the order of the CTAs.
@@ -248,54 +248,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kCtrlWarps) {
     setmaxnreg_dec<kCtrlRegs>();
     if (warp == 0) {
-      if (lane == 0) {
-        uint32_t it = 0;
-        for (int t = t0; t < total && !timed_out; t += step) {
-          const Tile tl = get_tile(p, ctl, t);
-          const int brow = tl.el * p.N + tl.n0;
-          for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
-            const int s = it % kStages;
-            if (!mbar_wait_bounded_idle(smem_u32(&ctl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
-              timed_out = true;
-              break;
-            }
-            const uint32_t sa = base + s * kStageBytes, fb = smem_u32(&ctl->full[s]);
+      const bool leader = elect_one();
+      const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]);
+      uint32_t it = 0, s = 0, ph = 1;
+      for (int t = t0; t < total && !timed_out; t += step) {
+        const Tile tl = get_tile(p, ctl, t);
+        const int brow = tl.el * p.N + tl.n0;
+        for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+          if (!wait_uniform(empty0 + 8 * s, ph, abort_flag)) {
+            timed_out = true;
+            break;
+          }
+          if (leader) {
+            const uint32_t sa = base + s * kStageBytes, fb = full0 + 8 * s;
             mbar_arrive_expect_tx(fb, kStageBytes);
             tma_load_2d(sa, &tmA, kb * kBK, tl.row0, fb);
             tma_load_2d(sa + kABytes, &tmB, kb * kBK, brow, fb);
           }
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
-        if (timed_out) {
-          *abort_flag = 1;
-          ctl->err = 2;
-        }
-        // the last loads land before the CTA can exit, whichever role's wait ran out
-        for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-          mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
       }
       __syncwarp();
+      if (timed_out && lane == 0) {
+        *abort_flag = 1;
+        ctl->err = 2;
+      }
+      // the last loads land before the CTA can exit, whichever role's wait ran out
+      if (lane == 0)
+        for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+          mbar_wait_bounded(full0 + 8 * (j % kStages), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
+      __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
-        uint32_t it = 0;
-        for (int t = t0; t < total && !timed_out; t += step) {
-          for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
-            const int s = it % kStages;
-            const uint32_t a = it & 1;
-            if (!mbar_wait_bounded_idle(smem_u32(&ctl->full[s]), (it / kStages) & 1, abort_flag, kWaitLimitNs) ||
-                !mbar_wait_bounded_idle(smem_u32(&ctl->tempty[a]), ((it >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
-              timed_out = true;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sa = base + s * kStageBytes;
-            const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kABytes);
+      const bool leader = elect_one();
+      const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]);
+      const uint32_t tfull0 = smem_u32(&ctl->tfull[0]), tempty0 = smem_u32(&ctl->tempty[0]);
+      const uint64_t da0 = smem_desc_sw128(base), db0 = smem_desc_sw128(base + kABytes);
+      uint32_t s = 0, ph = 0, a = 0, aph = 1;
+      for (int t = t0; t < total && !timed_out; t += step) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
+          if (!wait_uniform(full0 + 8 * s, ph, abort_flag) || !wait_uniform(tempty0 + 8 * a, aph, abort_flag)) {
+            timed_out = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+          if (leader) {
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4)  // 32 bytes of K: 2 in the descriptors' 16-byte units
               mma_f8(tmem + a * kBN, da + 2 * k4, db + 2 * k4, idesc_e4m3_f32(kBM, kBN), k4 > 0);
-            mma_commit(smem_u32(&ctl->empty[s]));
-            mma_commit(smem_u32(&ctl->tfull[a]));
+            mma_commit(empty0 + 8 * s);
+            mma_commit(tfull0 + 8 * a);
           }
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+          a ^= 1;
+          aph ^= a == 0;
         }
+      }
+      __syncwarp();
+      if (leader) {
         mma_commit(smem_u32(&ctl->drain));
         if (!mbar_wait_bounded(smem_u32(&ctl->drain), 0, &ctl->no_abort, kWaitLimitNs)) timed_out = true;
         if (timed_out) {
@@ -382,17 +398,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = i / per, c = rank * cols + 8 * (i - row * per);
           if (tl.n0 + c >= p.N) continue;
           float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          for (int q = 0; q < parts; ++q) {
-            const float4 lo = ld_cluster_f4(mapa_shared(base + part_offset(row, c / 4), q));
-            const float4 hi = ld_cluster_f4(mapa_shared(base + part_offset(row, c / 4 + 1), q));
-            v[0] += lo.x;
-            v[1] += lo.y;
-            v[2] += lo.z;
-            v[3] += lo.w;
-            v[4] += hi.x;
-            v[5] += hi.y;
-            v[6] += hi.z;
-            v[7] += hi.w;
+          for (int q0 = 0; q0 < parts; q0 += 4) {  // four CTAs' loads in flight, added in order
+            float4 lo[4], hi[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q0 + q < parts) {
+                lo[q] = ld_cluster_f4(mapa_shared(base + part_offset(row, c / 4), q0 + q));
+                hi[q] = ld_cluster_f4(mapa_shared(base + part_offset(row, c / 4 + 1), q0 + q));
+              }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q0 + q < parts) {
+                v[0] += lo[q].x;
+                v[1] += lo[q].y;
+                v[2] += lo[q].z;
+                v[3] += lo[q].w;
+                v[4] += hi[q].x;
+                v[5] += hi[q].y;
+                v[6] += hi[q].z;
+                v[7] += hi[q].w;
+              }
           }
           *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(tl.row0 + row) * p.N + tl.n0 + c) =
               make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
@@ -475,9 +500,14 @@ extern "C" moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale
   const Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(N), static_cast<int>(K / 128),
                  static_cast<int>(ntiles), static_cast<int>((N + 127) / 128), lhs_scale, rhs_scale, out,
                  moe_detail_stall_ns()};
-  // CTAs a tile: as many as the device holds, no more than there are K blocks
+  // CTAs a tile: twice as many while the device holds them and the K blocks that are saved
+  // (0.4 us each) take longer than the joining: 1.5 us and 2.3 us for 128 rows with the first
+  // two, 0.4 and 2.4 for each doubling after that.  Measured on one row x 1536 x 2048: 9.9, 8.2,
+  // 6.9, 6.6 us with 1, 2, 4, 8; on 128 rows 11.7, 12.3, 13.2, 15.2, with K = 4096 17.9, 15.5, 14.8, 16.1.
+  const int64_t rows = M < kBM ? M : kBM;
   int parts = 1;
-  while (parts < 8 && 2 * parts * most <= sms && 2 * parts <= p.nkb) parts *= 2;
+  while (parts < 8 && 2 * parts * most <= sms && 128ll * p.nkb > 2 * parts * ((parts == 1 ? 512 : 128) + 6 * rows))
+    parts *= 2;
   auto kernel = parts > 1 ? gmm_block_kernel<true> : gmm_block_kernel<false>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
   if (E_local < E) {

@@ -12,6 +12,37 @@ namespace moe {
 namespace {
 
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxDevices = 256;  // host-side per-device caches
+
+// One lane of the warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Bounded wait of a whole warp that issues loads or MMAs.  Such a warp runs its loop with
+// all lanes, and only the issuing instructions are one lane's: what they take (addresses,
+// descriptors) is then the warp's, in uniform registers, and a stage costs half the clocks
+// of a loop that one lane runs alone (tgmm_fp8_mx without MMAs: 190 against 340 ns a stage).
+__device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 64;\n\t"
+      "@q bra AGAIN;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok != 0)) return true;
+  return __all_sync(0xffffffffu, mbar_wait_bounded_idle(bar, parity, abort_flag, kWaitLimitNs));
+}
 
 // Rows of out (bf16 [M, N]) before the first and after the last local group: zeros.
 __global__ void __launch_bounds__(256) zero_outside_rows_kernel(uint16_t* out, int64_t M, int64_t N,

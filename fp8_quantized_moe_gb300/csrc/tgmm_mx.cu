@@ -20,15 +20,28 @@
 //     (2 bytes read, 1 written): a thread holds 8 columns of 8 consecutive rows, so
 //     that a column's codes are 8 bytes of its own registers and a warp's stores fill
 //     whole sectors; maxima of 32 rows are among 4 lanes.
-//   tgmm_mx_kernel  one persistent CTA per SM, 128 (k) x 256 (n) tiles:
-//     warp 0      TMA producer: per stage one block of 128 rows, A 16 KB, B 32 KB and the
-//                 scale atoms (one bulk copy an operand), four stages.
-//     warp 1      MMA issuer: scale atoms to tensor memory, then an M = 128, N = 256
-//                 MMA for each 32 rows that the block holds.
-//     warps 4..11 epilogue: the accumulator to 128 registers a thread, accumulator
-//                 handed back, then whole 32-byte sectors to memory, beside the next
-//                 tile's MMAs.
+//   tgmm_mx_kernel  persistent pairs of CTAs, 256 (k) x 256 (n) tiles, 128 rows of
+//     k and half of B a CTA (16 warps, one CTA per SM):
+//     warp 0       TMA producer: per stage one block of 128 rows, A 16 KB and half of B
+//                  16 KB, and the scale atoms of this CTA's k rows and of all of n.
+//     warp 1       of the pair's even CTA: MMA issuer, an M = 256, N = 256 MMA for each 32
+//                  rows that the block holds.
+//     warps 4..7   the scale atoms from shared to tensor memory, each to its quarter of the
+//                  lanes (tcgen05.st; copied by tcgen05.cp they would stand in the tensor
+//                  core's own queue, in front of the products).
+//     warps 8..15  epilogue: the accumulator to 128 registers a thread, accumulator
+//                  handed back, then whole 32-byte sectors to memory, beside the next
+//                  tile's MMAs.
 //     Tiles run expert-major, then n tile, then k tile.
+//     One CTA per 128 x 256 tile needs 48 KB a block and SM, 768 clocks at the 64 bytes a
+//     clock that an SM takes in; a pair needs 32 KB.
+//     Measured: 16384 rows, 4096 x 28672, 8 experts 1.60 ms with the rounding (0.30);
+//     without the stores 1.33, without the MMAs 1.35, with neither 0.96: loads, MMAs and
+//     stores (3.8 GB) overlap only in part.  One CTA a 128 x 256 tile, its issuing loops run by
+//     one lane and its scales by tcgen05.cp: 1.87; the pair with such loops: 1.75.  49152
+//     rows, 4096 x 2816, 64 experts: 835 us; 16384 rows, 2048 x 1536, 128 experts: 331 us
+//     (1.6 GB of gradients; stores alone 260).  Stores by TMA from shared memory: 855 us and
+//     1.69 ms on the first two.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets what
 // it issued finish and returns.
@@ -225,13 +238,18 @@ __global__ void __launch_bounds__(256, 3) round_rows_kernel(const Operand oa, co
 
 // ---- product -------------------------------------------------------------
 constexpr int kBM = 128, kBN = 256;
-constexpr int kStages = 4;
-constexpr int kABytes = kBM * kRB, kBBytes = kBN * kRB;
+constexpr int kStages = 6;
+constexpr int kABytes = kBM * kRB, kBBytes = kBN / 2 * kRB;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kSfBytes = 3 * kAtom;  // a stage's scale atoms: A's, B's two
-constexpr int kSfCols = 12, kSfCol0 = kBN;
-constexpr int kCtrlWarps = 4, kEpiWarps = 8;
+constexpr int kSfCols = 16, kSfCol0 = kBN;  // tensor-memory columns of a stage's scales: A's 4, B's 8, 4 unused
+constexpr int kCtrlWarps = 8, kEpiWarps = 8;
+constexpr int kSfWarp = 4;  // the first of the four that move scales
 constexpr int kThreads = 32 * (kCtrlWarps + kEpiWarps);
+// registers a thread: 128 at launch (a 512-thread CTA alone on its SM), handed from the
+// first two warpgroups to the epilogue
+constexpr uint32_t kCtrlRegs = 56, kEpiRegs = 200;
+static_assert(256 * kCtrlRegs + 256 * kEpiRegs <= 128 * kThreads, "register split");
 static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
 
 struct Params {
@@ -247,7 +265,8 @@ struct Params {
 };
 
 struct Ctl {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kStages], empty[kStages];  // full: the even CTA's counts both CTAs
+  uint64_t sfull[kStages];                 // this CTA's scale atoms have landed
   uint64_t tfull, tempty, drain;
   uint64_t never;  // test hook: a barrier that nothing arrives on
   uint32_t tmem_base;
@@ -262,12 +281,13 @@ struct Tile {
   int el, kb0, rows, k0, n0;  // rows: of the expert
 };
 
-__device__ __forceinline__ Tile get_tile(const Params& p, const Ctl* c, int t) {
+// (ktiles: pairs of 128 rows of k)
+__device__ __forceinline__ Tile get_tile(const Params& p, const Ctl* c, int t, int rank) {
   const int per = p.ktiles * p.ntiles;
   Tile tl;
   tl.el = t / per;
   const int r = t - tl.el * per, nt = r / p.ktiles;
-  tl.k0 = (r - nt * p.ktiles) * kBM;
+  tl.k0 = (2 * (r - nt * p.ktiles) + rank) * kBM;  // (K or more: an odd CTA without rows)
   tl.n0 = nt * kBN;
   tl.kb0 = c->t.kstart[tl.el];
   tl.rows = c->t.start[tl.el + 1] - c->t.start[tl.el];
@@ -285,6 +305,24 @@ __device__ __forceinline__ void store8(float* o, const uint32_t* v, bool wide) {
   }
 }
 
+// D (+)= (A 2^(sfa - 127)) (B 2^(sfb - 127))^T over a CTA pair: M = 256 rows, 128 from each
+// CTA; each CTA's tensor memory holds the scales of its own rows of A and of all of B.
+__device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Four 32-bit columns of this warp's lane quarter.
+__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint4& v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w));
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     tgmm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -293,14 +331,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sf_ring = base + kStages * kStageBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(bp + kStages * (kStageBytes + kSfBytes));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // a pair works on one sequence of tiles; its even CTA (rank 0) issues the MMAs
+  // and owns the full and accumulator-empty barriers
+  const int rank = static_cast<int>(__clusterRelativeBlockRank());
+  const int t0 = static_cast<int>(__clusterIdx().x), step = static_cast<int>(__clusterGridDimInClusters().x);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->full[s]), 1 + 2 * 4);  // the producer's announcement, four scale warps a CTA
       mbar_init(smem_u32(&ctl->empty[s]), 1);
+      mbar_init(smem_u32(&ctl->sfull[s]), 1);
     }
     mbar_init(smem_u32(&ctl->tfull), 1);
-    mbar_init(smem_u32(&ctl->tempty), kEpiWarps);
+    mbar_init(smem_u32(&ctl->tempty), 2 * kEpiWarps);
     mbar_init(smem_u32(&ctl->drain), 1);
     mbar_init(smem_u32(&ctl->never), 1);
     ctl->abort_flag = 0;
@@ -308,111 +351,181 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->err = 0;
     fence_mbar_init();
   }
+  // (both CTAs of a pair read the same group sizes, so they leave here together)
   if (!build_tables(p.group_sizes, p.E, p.g0, p.El, p.M, &ctl->t)) {
     if (threadIdx.x == 0) raise_error(&g_err, MOE_DEVERR_GROUP_SIZES);
     return;
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&ctl->tmem_base), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish_pair();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
   tc_fence_before();
-  __syncthreads();
+  // the peer's barriers are initialised and its columns allocated before any
+  // operand, commit or release crosses between the two CTAs
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  if (rank == 1 && threadIdx.x == 0 &&
+      ld_shared_cluster_u32(mapa_shared(smem_u32(&ctl->tmem_base), 0)) != tmem)
+    raise_error(&g_err, MOE_DEVERR_TMEM);  // the pair's accumulators would not line up
   const int total = p.El * p.ktiles * p.ntiles;
   volatile int* abort_flag = &ctl->abort_flag;
   bool timed_out = false;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
-        const Tile tl = get_tile(p, ctl, t);
+  if (warp < kCtrlWarps) {
+    setmaxnreg_dec<kCtrlRegs>();
+    if (warp == 0) {
+      const bool leader = elect_one();
+      uint32_t it = 0, s = 0, ph = 1;
+      const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), 0), full_l = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]), sfull0 = smem_u32(&ctl->sfull[0]);
+      for (int t = t0; t < total && !timed_out; t += step) {
+        const Tile tl = get_tile(p, ctl, t, rank);
         const int nkb = (tl.rows + kRB - 1) / kRB;
+        const uint8_t* fa = p.sf_a + (static_cast<int64_t>(tl.kb0) * p.nrb_a + tl.k0 / 128) * kAtom;
+        const uint8_t* fbp = p.sf_b + (static_cast<int64_t>(tl.kb0) * p.nrb_b + tl.n0 / 128) * kAtom;
+        int ya = tl.kb0 * p.K + tl.k0, yb = tl.kb0 * p.N + tl.n0 + rank * (kBN / 2);
         for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+          if (!wait_uniform(empty0 + 8 * s, ph, abort_flag)) {
             timed_out = true;
             break;
           }
-          const uint32_t fb = smem_u32(&ctl->full[s]), sa = base + s * kStageBytes, sf = sf_ring + s * kSfBytes;
-          const int g = tl.kb0 + kb;
-          mbar_arrive_expect_tx(fb, kStageBytes + kSfBytes);
-          // a tile's rows past the operand's last column are the next block's: never stored
-          tma_load_2d(sa, &tmA, 0, g * p.K + tl.k0, fb);
-          tma_load_2d(sa + kABytes, &tmB, 0, g * p.N + tl.n0, fb);
-          bulk_load(sf, p.sf_a + (static_cast<int64_t>(g) * p.nrb_a + tl.k0 / 128) * kAtom, kAtom, fb);
-          bulk_load(sf + kAtom, p.sf_b + (static_cast<int64_t>(g) * p.nrb_b + tl.n0 / 128) * kAtom, 2 * kAtom, fb);
+          if (leader) {
+            const uint32_t sa = base + s * kStageBytes, sf = sf_ring + s * kSfBytes, sb = sfull0 + 8 * s, fb = full0 + 8 * s;
+            mbar_arrive_expect_tx(sb, kSfBytes);
+            if (rank == 0) mbar_arrive_expect_tx(full_l + 8 * s, 2 * kStageBytes);
+            bulk_load(sf, fa, kAtom, sb);
+            bulk_load(sf + kAtom, fbp, 2 * kAtom, sb);
+            tma_load_2d_pair(sa, &tmA, 0, ya, fb);
+            tma_load_2d_pair(sa + kABytes, &tmB, 0, yb, fb);
+          }
+          fa += p.nrb_a * kAtom;
+          fbp += p.nrb_b * kAtom;
+          ya += p.K;
+          yb += p.N;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
-      if (timed_out) {
-        *abort_flag = 1;
-        ctl->err = 2;
-      }
-      // the last loads land before the CTA can exit, whichever role's wait ran out
-      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-        mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, acc = 0;
-      for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
-        const Tile tl = get_tile(p, ctl, t);
-        const int nkb = (tl.rows + kRB - 1) / kRB;
-        if (nkb == 0) continue;
-        if (!mbar_wait_bounded(smem_u32(&ctl->tempty), (acc & 1) ^ 1, abort_flag, kWaitLimitNs)) {
-          timed_out = true;
-          break;
+      __syncwarp();
+      if (lane == 0) {
+        if (timed_out) {
+          *abort_flag = 1;
+          ctl->err = 2;
         }
-        tc_fence_after();
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait_bounded(smem_u32(&ctl->full[s]), (it / kStages) & 1, abort_flag, kWaitLimitNs)) {
+        // The last loads land before the CTAs can exit, whichever role's wait ran out:
+        // the scales of either CTA here; the codes are complete once the MMAs that
+        // read them are, and otherwise (a wait ran out) within microseconds.
+        for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+          mbar_wait_bounded(smem_u32(&ctl->sfull[j % kStages]), (j / kStages) & 1, &ctl->no_abort, kWaitLimitNs);
+        if (*abort_flag) mbar_wait_bounded(smem_u32(&ctl->never), 0, &ctl->no_abort, 1000000ull);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (rank == 0) {
+        const bool leader = elect_one();
+        uint32_t acc = 0, s = 0, ph = 0;
+        const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]);
+        const uint64_t da0 = smem_desc_sw128(base), db0 = smem_desc_sw128(base + kABytes);
+        for (int t = t0; t < total && !timed_out; t += step) {
+          const Tile tl = get_tile(p, ctl, t, rank);
+          const int nkb = (tl.rows + kRB - 1) / kRB;
+          if (nkb == 0) continue;
+          if (!wait_uniform(smem_u32(&ctl->tempty), (acc & 1) ^ 1, abort_flag)) {
             timed_out = true;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + s * kStageBytes, sf = sf_ring + s * kSfBytes, sft = tmem + kSfCol0 + s * kSfCols;
-          const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kABytes);
-          tmem_cp_32x128b_warpx4(sft, smem_desc_plain(sf));
-          tmem_cp_32x128b_warpx4(sft + 4, smem_desc_plain(sf + kAtom));
-          tmem_cp_32x128b_warpx4(sft + 8, smem_desc_plain(sf + 2 * kAtom));
-          const int nsub = min(4, (tl.rows - kb * kRB + 31) / 32);  // 32-row blocks that hold rows
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!wait_uniform(full0 + 8 * s, ph, abort_flag)) {
+              timed_out = true;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sft = tmem + kSfCol0 + s * kSfCols;
+            const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+            const int left = tl.rows - kb * kRB;  // rows of the block: an MMA for each 32
+            if (leader) {
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4)
-            if (k4 < nsub)
-              mma_mx(tmem, da + 2 * k4, db + 2 * k4, idesc_mx_e4m3(kBM, kBN, k4, k4), sft, sft + 4, kb > 0 || k4 > 0);
-          mma_commit(smem_u32(&ctl->empty[s]));
+              for (int k4 = 0; k4 < 4; ++k4)
+                if (k4 == 0 || left > 32 * k4)
+                  mma_mx_pair(tmem, da + 2 * k4, db + 2 * k4, idesc_mx_e4m3(2 * kBM, kBN, k4, k4), sft, sft + 4,
+                              kb > 0 || k4 > 0);
+              mma_commit_pair_mc(empty0 + 8 * s, 0x3);
+            }
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+          if (timed_out) break;
+          if (leader) mma_commit_pair_mc(smem_u32(&ctl->tfull), 0x3);
+          ++acc;
         }
-        if (timed_out) break;
-        mma_commit(smem_u32(&ctl->tfull));
-        ++acc;
+        __syncwarp();
+        if (leader) {
+        mma_commit_pair(smem_u32(&ctl->drain));
+        if (!mbar_wait_bounded(smem_u32(&ctl->drain), 0, &ctl->no_abort, kWaitLimitNs)) timed_out = true;
+        if (timed_out) {
+          *abort_flag = 1;
+          ctl->err = 2;
+        }
+        }
       }
-      mma_commit(smem_u32(&ctl->drain));
-      if (!mbar_wait_bounded(smem_u32(&ctl->drain), 0, &ctl->no_abort, kWaitLimitNs)) timed_out = true;
+      __syncwarp();
+    } else if (warp >= kSfWarp) {
+      // The stage was empty when the producer announced its scales, and so were their
+      // columns: the same MMAs read both.
+      const uint32_t tq = tmem + kSfCol0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      uint32_t s = 0, ph = 0;
+      const uint32_t sfull0 = smem_u32(&ctl->sfull[0]), full0 = mapa_shared(smem_u32(&ctl->full[0]), 0);
+      for (int t = t0; t < total && !timed_out; t += step) {
+        const Tile tl = get_tile(p, ctl, t, rank);
+        const int nkb = (tl.rows + kRB - 1) / kRB;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!wait_uniform(sfull0 + 8 * s, ph, abort_flag)) {
+            timed_out = true;
+            break;
+          }
+          const uint8_t* sf = bp + kStages * kStageBytes + s * kSfBytes + 16 * lane;
+          tmem_st_x4(tq + s * kSfCols, *reinterpret_cast<const uint4*>(sf));
+          tmem_st_x4(tq + s * kSfCols + 4, *reinterpret_cast<const uint4*>(sf + kAtom));
+          tmem_st_x4(tq + s * kSfCols + 8, *reinterpret_cast<const uint4*>(sf + 2 * kAtom));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          // (relaxed: it orders only tensor-memory stores that have completed)
+          if (lane == 0) mbar_arrive_cluster_relaxed(full0 + 8 * s);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
       if (timed_out) {
         *abort_flag = 1;
         ctl->err = 2;
       }
     }
-    __syncwarp();
-  } else if (warp >= kCtrlWarps) {
+  } else {
+    setmaxnreg_inc<kEpiRegs>();
     const int q4 = warp & 3, half = (warp - kCtrlWarps) >> 2;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + half * (kBN / 2);
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     uint32_t acc = 0;
     if (p.stall_ns && !mbar_wait_bounded_warp(smem_u32(&ctl->never), 0, abort_flag, p.stall_ns)) timed_out = true;
-    for (int t = blockIdx.x; t < total && !timed_out; t += gridDim.x) {
-      const Tile tl = get_tile(p, ctl, t);
+    for (int t = t0; t < total && !timed_out; t += step) {
+      const Tile tl = get_tile(p, ctl, t, rank);
       uint32_t v[4][32];
       if (tl.rows > 0) {
-        if (!mbar_wait_bounded_warp(smem_u32(&ctl->tfull), acc & 1, abort_flag, kWaitLimitNs)) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_bounded_idle(smem_u32(&ctl->tfull), acc & 1, abort_flag, kWaitLimitNs))) {
           timed_out = true;
           break;
         }
@@ -423,19 +536,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty));
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctl->tempty), 0));
       } else {  // an expert without rows: zeros
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int c = 0; c < 32; ++c) v[i][c] = 0;
       }
-      const int k = tl.k0 + q4 * 32 + lane, n = tl.n0 + half * (kBN / 2);
-      if (k < p.K) {
-        float* o = p.out + (static_cast<int64_t>(tl.el) * p.K + k) * p.N + n;
+      // Lane 4 a + q has a row's columns; after a transpose of 8-column pieces in each four
+      // lanes it has columns 8 q.. of rows 4 a .. 4 a + 3, so that a store instruction
+      // writes 8 rows x 128 bytes and not 32 rows x 32 (370 -> 331 us on 128 small experts).
+      const int k = tl.k0 + q4 * 32 + (lane & ~3), n = tl.n0 + half * (kBN / 2) + (lane & 3) * 8;
+      const bool odd = lane & 1, high = lane & 2;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (n + 8 * i < p.N) store8(o + 8 * i, &v[i >> 2][8 * (i & 3)], wide);
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t &x0 = v[i][c], &x1 = v[i][8 + c], &x2 = v[i][16 + c], &x3 = v[i][24 + c];
+          const uint32_t s01 = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
+          const uint32_t s23 = __shfl_xor_sync(0xffffffffu, odd ? x2 : x3, 1);
+          if (odd) {
+            x0 = s01;
+            x2 = s23;
+          } else {
+            x1 = s01;
+            x3 = s23;
+          }
+          const uint32_t s02 = __shfl_xor_sync(0xffffffffu, high ? x0 : x2, 2);
+          const uint32_t s13 = __shfl_xor_sync(0xffffffffu, high ? x1 : x3, 2);
+          if (high) {
+            x0 = s02;
+            x1 = s13;
+          } else {
+            x2 = s02;
+            x3 = s13;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k + j < p.K && n + 32 * i < p.N)
+            store8(p.out + (static_cast<int64_t>(tl.el) * p.K + k + j) * p.N + n + 32 * i, &v[i][8 * j], wide);
       }
     }
     if (timed_out) {
@@ -445,10 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  // neither CTA leaves (or frees its columns) while the other may still write its
+  // tensor memory or arrive on its barriers
+  cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
   if (threadIdx.x == 0 && ctl->err) raise_error(&g_err, MOE_DEVERR_TIMEOUT);
 }
@@ -469,8 +611,8 @@ bool make_layout(int64_t M, int64_t K, int64_t N, int El, Layout* l) {
   l->blocks = M == 0 ? 0 : (M - 1) / kRB + El;  // sum of ceil(size / 128), at the most
   const int64_t most = std::max(K, N);
   if (l->blocks > ((1ll << 31) - 1) / most - 1) return false;
-  l->nrb_a = static_cast<int>((K + 127) / 128);
-  l->nrb_b = static_cast<int>((N + 255) / 256) * 2;  // (a tile reads two)
+  l->nrb_a = static_cast<int>((K + 255) / 256) * 2;  // (a tile reads two of either)
+  l->nrb_b = static_cast<int>((N + 255) / 256) * 2;
   l->q_a = 0;
   l->q_b = l->q_a + l->blocks * K * kRB;
   l->sf_a = l->q_b + l->blocks * N * kRB;
@@ -512,7 +654,7 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   MOE_HOST_CHECK(aligned16(lhs) && aligned16(rhs) && aligned16(out) && aligned16(workspace) &&
                      workspace_bytes >= static_cast<size_t>(l.bytes),
                  MOE_ERR_INVALID_ARG);
-  const int64_t ktiles = (K + kBM - 1) / kBM, ntiles = (N + kBN - 1) / kBN, total = E_local * ktiles * ntiles;
+  const int64_t ktiles = (K + 2 * kBM - 1) / (2 * kBM), ntiles = (N + kBN - 1) / kBN, total = E_local * ktiles * ntiles;
   MOE_HOST_CHECK(total < (1ll << 31), MOE_ERR_INVALID_ARG);
   const int sms = sm103_count();
   if (sms <= 0) return MOE_ERR_UNSUPPORTED;
@@ -524,7 +666,7 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   CUtensorMap A, B;
   if (!make_map_u8(&A, ws + l.q_a, kRB, static_cast<uint64_t>(l.blocks) * K, kRB, kBM)) return MOE_ERR_CUDA;
-  if (!make_map_u8(&B, ws + l.q_b, kRB, static_cast<uint64_t>(l.blocks) * N, kRB, kBN)) return MOE_ERR_CUDA;
+  if (!make_map_u8(&B, ws + l.q_b, kRB, static_cast<uint64_t>(l.blocks) * N, kRB, kBN / 2)) return MOE_ERR_CUDA;
   const Operand oa{lhs, lhs_index, k, lhs_rows, static_cast<int>(K), static_cast<int>((K + 127) / 128), l.nrb_a,
                    ws + l.q_a, ws + l.sf_a};
   const Operand ob{rhs, nullptr, 1, M, static_cast<int>(N), static_cast<int>((N + 127) / 128), l.nrb_b,
@@ -538,7 +680,36 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
                  moe_detail_stall_ns()};
   MOE_CUDA_TRY(cudaFuncSetAttribute(tgmm_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(kSmem)));
-  tgmm_mx_kernel<<<static_cast<unsigned>(std::min<int64_t>(total, sms)), kThreads, kSmem, st>>>(A, B, p);
-  MOE_CUDA_TRY(cudaGetLastError());
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // pairs that are resident at once, per device (fewer than half of the SMs where a
+  // cluster of SMs has an odd number: a pair more than that would run after all others)
+  static std::mutex mu;
+  static int resident[kMaxDevices] = {};
+  int dev = 0, pairs = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    pairs = resident[dev];
+  }
+  if (pairs == 0) {
+    cfg.gridDim = dim3(2 * (sms / 2));
+    MOE_CUDA_TRY(cudaOccupancyMaxActiveClusters(&pairs, tgmm_mx_kernel, &cfg));
+    if (pairs <= 0) return MOE_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> lock(mu);
+    resident[dev] = pairs;
+  }
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(total, pairs)));
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, tgmm_mx_kernel, A, B, p));
   return MOE_OK;
 }
