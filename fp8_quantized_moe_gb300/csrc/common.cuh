@@ -510,6 +510,14 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ------------------------------------------------------------------------
+// A kernel launched to overlap the one before it in the stream (programmatic stream
+// serialization): the first lets it start, the second waits until everything before is
+// complete and visible.
+// ------------------------------------------------------------------------
+__device__ __forceinline__ void grid_release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ------------------------------------------------------------------------
 // Thread-block clusters (CTA pairs)
 // ------------------------------------------------------------------------
 // shared::cluster address of the variable at shared::cta address `addr` in

@@ -16,6 +16,7 @@
 //   warp 0      TMA producer: 128 A rows and 256 B rows of 128 bytes per stage, 48 KB,
 //               four stages, 128-byte swizzle.
 //   warp 1      MMA issuer: four M = 128, N = 256, K = 32 tcgen05.mma.kind::f8f6f4 a block.
+//   warps 2, 3  zeros for the rows of no local group.
 //   warps 4..11 epilogue: warp w has tensor-memory lanes 32 (w % 4).. (rows) and
 //               128 of the tile's columns: 128 running sums a thread.
 // The producing and issuing warps run with all lanes (wait_uniform).  Two 256-column accumulators take alternate K blocks.
@@ -190,6 +191,14 @@ __device__ __forceinline__ uint32_t part_offset(int r, int u) {
   return static_cast<uint32_t>(r * (kBN * 4) + ((u ^ (r & 7)) << 4));
 }
 
+// Rows of no local group, zeroed by two warps of every CTA.
+__device__ void zero_outside(const Params& p, const Ctl* c, int cta, int ctas) {
+  const int64_t n16 = p.N / 8, head = c->start[0] * n16, gap = (c->start[p.El] - c->start[0]) * n16;
+  const int64_t all = p.M * n16 - gap, step = 64ll * ctas;
+  uint4* o = reinterpret_cast<uint4*>(p.out);
+  for (int64_t i = 64ll * cta + (threadIdx.x & 63); i < all; i += step) o[i < head ? i : i + gap] = make_uint4(0, 0, 0, 0);
+}
+
 template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     gmm_block_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
@@ -228,7 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) raise_error(&g_err, MOE_DEVERR_GROUP_SIZES);
     return;
   }
-  if (SPLIT && t0 >= ctl->total) return;  // (and here)
+  const bool zeroes = p.El < p.E && (warp == 2 || warp == 3);
+  if (SPLIT) {
+    if (zeroes) zero_outside(p, ctl, blockIdx.x, gridDim.x);
+    if (t0 >= ctl->total) return;  // (and here)
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(&ctl->tmem_base), 512);
     tmem_relinquish();
@@ -320,6 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
+    } else if (!SPLIT && zeroes) {
+      zero_outside(p, ctl, blockIdx.x, gridDim.x);
     }
   } else {
     setmaxnreg_inc<kEpiRegs>();
@@ -510,10 +525,6 @@ extern "C" moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale
     parts *= 2;
   auto kernel = parts > 1 ? gmm_block_kernel<true> : gmm_block_kernel<false>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
-  if (E_local < E) {
-    zero_outside_rows_kernel<<<sms * 4, 256, 0, st>>>(out, M, N, group_sizes, E, group_offset, E_local);
-    MOE_CUDA_TRY(cudaGetLastError());
-  }
   if (parts == 1) {
     kernel<<<static_cast<unsigned>(most < sms ? most : sms), kThreads, kSmem, st>>>(A, B, p);
     MOE_CUDA_TRY(cudaGetLastError());

@@ -1,5 +1,5 @@
 // What the grouped kernels on block-scaled 8-bit operands share: tensor maps,
-// device queries, and the rows that belong to no local group.  (Included by several translation units; everything is local to each.)
+// device queries and the waits of issuing warps.  (Included by several translation units; everything is local to each.)
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -42,35 +42,6 @@ __device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, cons
       : "memory");
   if (__all_sync(0xffffffffu, ok != 0)) return true;
   return __all_sync(0xffffffffu, mbar_wait_bounded_idle(bar, parity, abort_flag, kWaitLimitNs));
-}
-
-// Rows of out (bf16 [M, N]) before the first and after the last local group: zeros.
-__global__ void __launch_bounds__(256) zero_outside_rows_kernel(uint16_t* out, int64_t M, int64_t N,
-                                                                const int32_t* sizes, int E, int g0, int El) {
-  __shared__ int64_t bound[2];
-  if (threadIdx.x < 32) {
-    int64_t lo = 0, hi = 0;
-    for (int g = threadIdx.x; g < E; g += 32) {
-      const int64_t sz = __ldg(sizes + g);
-      lo += g < g0 ? sz : 0;
-      hi += g < g0 + El ? sz : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      lo += __shfl_xor_sync(0xffffffffu, lo, o);
-      hi += __shfl_xor_sync(0xffffffffu, hi, o);
-    }
-    if (threadIdx.x == 0) {  // (sizes that do not add up to M: an error of the product's kernel)
-      bound[0] = min(max(lo, static_cast<int64_t>(0)), M);
-      bound[1] = min(max(hi, bound[0]), M);
-    }
-  }
-  __syncthreads();
-  const int64_t n16 = N / 8, head = bound[0] * n16, gap = (bound[1] - bound[0]) * n16;
-  const int64_t all = M * n16 - gap, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  uint4* o = reinterpret_cast<uint4*>(out);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step)
-    o[i < head ? i : i + gap] = make_uint4(0, 0, 0, 0);
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -155,10 +155,11 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float& inv) 
   return static_cast<uint32_t>(code);
 }
 
-__global__ void __launch_bounds__(256, 3) round_rows_kernel(const Operand oa, const Operand ob, const int32_t* sizes,
+__global__ void __launch_bounds__(256, 4) round_rows_kernel(const Operand oa, const Operand ob, const int32_t* sizes,
                                                             int E, int g0, int El, int64_t M) {
   __shared__ Tables t;
   __shared__ __align__(16) uint8_t sfs[2][kAtom];
+  grid_release_next();  // (the product's kernel takes over the SMs as they come free)
   if (!build_tables(sizes, E, g0, El, M, &t)) return;  // (the product's kernel raises the error)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // warp: 32 rows (warp & 3) of 64 columns (warp >> 2); lane: 8 rows, 8 columns
@@ -180,22 +181,24 @@ __global__ void __launch_bounds__(256, 3) round_rows_kernel(const Operand oa, co
     const int r0 = t.start[lo] + (kb - t.kstart[lo]) * kRB + 32 * j + 8 * rl;  // this thread's first row
     const int nr = t.start[lo + 1] - r0;                                       // rows of the group from there on
     const int c0 = cb * 128 + cu;
+    // lane (rl, i) finds the source of row i of its eight, the others take it from there
+    int src = r0 + (lane & 7);
+    if (o.idx && (lane & 7) < nr) {
+      const int pick = __ldg(o.idx + src);
+      const uint32_t row = static_cast<uint32_t>(pick) / static_cast<uint32_t>(o.k);
+      src = static_cast<int>(row);
+      if (pick < 0 || row >= o.src_rows) {
+        raise_error(&g_err, MOE_DEVERR_BAD_POSITION);
+        src = -1;
+      }
+    }
     uint4 d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      const int row = __shfl_sync(0xffffffffu, src, (lane & 24) + i);
       d[i] = make_uint4(0, 0, 0, 0);
-      if (i < nr && c0 < o.C) {
-        int64_t row = r0 + i;
-        if (o.idx) {
-          const int p = __ldg(o.idx + row);
-          row = static_cast<int64_t>(static_cast<uint32_t>(p) / static_cast<uint32_t>(o.k));
-          if (p < 0 || row >= o.src_rows) {
-            raise_error(&g_err, MOE_DEVERR_BAD_POSITION);
-            continue;
-          }
-        }
-        d[i] = __ldg(reinterpret_cast<const uint4*>(o.x + row * o.C + c0));
-      }
+      if (i < nr && row >= 0 && c0 < o.C)
+        d[i] = __ldg(reinterpret_cast<const uint4*>(o.x + static_cast<int64_t>(row) * o.C + c0));
     }
     // largest magnitude of each column over the 32 rows: bf16 magnitudes order
     // like their bits
@@ -369,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // operand, commit or release crosses between the two CTAs
   cluster_sync_all();
   tc_fence_after();
+  grid_wait_previous();  // the codes are complete (all but the group sizes, which round_rows_kernel did not write)
   const uint32_t tmem = ctl->tmem_base;
   if (rank == 1 && threadIdx.x == 0 &&
       ld_shared_cluster_u32(mapa_shared(smem_u32(&ctl->tmem_base), 0)) != tmem)
@@ -672,7 +676,7 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   const Operand ob{rhs, nullptr, 1, M, static_cast<int>(N), static_cast<int>((N + 127) / 128), l.nrb_b,
                    ws + l.q_b, ws + l.sf_b};
   const int64_t rounds = l.blocks * (oa.ncb + ob.ncb);
-  round_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(rounds, sms * 3)), 256, 0, st>>>(
+  round_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(rounds, sms * 4)), 256, 0, st>>>(
       oa, ob, group_sizes, E, group_offset, E_local, M);
   MOE_CUDA_TRY(cudaGetLastError());
   const Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(K), static_cast<int>(N),
@@ -681,11 +685,13 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   MOE_CUDA_TRY(cudaFuncSetAttribute(tgmm_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(kSmem)));
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -710,6 +716,7 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
     resident[dev] = pairs;
   }
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(total, pairs)));
+  cfg.numAttrs = 2;
   MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, tgmm_mx_kernel, A, B, p));
   return MOE_OK;
 }

@@ -1,8 +1,8 @@
 """GPU tests of the router's balance loss and its gradient against 64-bit forms.
 
-Counts are exact.  With R the logits' range in a row, e^(x - max) is off by (R + 2)
-half steps of fp32 relative (the subtraction, the exponential), their sum by E more, the
-reciprocal and the product by 2: a probability by u = (2 R + E + 8) 2^-24, a mean over n
+Counts are exact.  With R the logits' range in a row, e^(x - max) is off by R + 5 half
+steps of fp32 relative (the subtraction; the exponential's 2^-22 and a rounding), their sum
+by E more, the reciprocal and the product by 2: a probability by u = (2 R + E + 8) 2^-24 at the most, a mean over n
 rows by u + n 2^-24 (sums in order, at the worst), the loss likewise."""
 
 import pytest
