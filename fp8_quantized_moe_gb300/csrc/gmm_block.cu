@@ -505,8 +505,9 @@ extern "C" moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale
   const int64_t ntiles = (N + kBN - 1) / kBN;
   const int64_t most = ((M + kBM - 1) / kBM + E_local) * ntiles;  // tiles, at the most
   MOE_HOST_CHECK(most < (1ll << 31), MOE_ERR_INVALID_ARG);
-  const int sms = sm103_count();
-  if (sms <= 0) return MOE_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int dev = sm103_device(&sms);
+  if (dev < 0) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   cudaStream_t st = as_stream(stream);
   CUtensorMap A, B;
@@ -524,7 +525,8 @@ extern "C" moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale
   while (parts < 8 && 2 * parts * most <= sms && 128ll * p.nkb > 2 * parts * ((parts == 1 ? 512 : 128) + 6 * rows))
     parts *= 2;
   auto kernel = parts > 1 ? gmm_block_kernel<true> : gmm_block_kernel<false>;
-  MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
+  static SmemLimit limit[2];
+  MOE_CUDA_TRY(limit[parts > 1].set(kernel, kSmem, dev));
   if (parts == 1) {
     kernel<<<static_cast<unsigned>(most < sms ? most : sms), kThreads, kSmem, st>>>(A, B, p);
     MOE_CUDA_TRY(cudaGetLastError());

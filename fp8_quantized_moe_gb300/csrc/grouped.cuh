@@ -4,6 +4,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -70,16 +71,38 @@ inline bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The current device's SMs, or 0 when it is not an sm_103 (or on an error).
-inline int sm103_count() {
-  int dev = 0, major = 0, minor = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return major == 10 && minor == 3 ? sms : 0;
+// The current device, or -1 where it is not an sm_103 (or on an error), and its SMs; asked
+// of the runtime once a device (half a microsecond a call otherwise).
+inline int sm103_device(int* sms) {
+  static std::atomic<int> known[kMaxDevices];  // 0: not asked yet; -1: another device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      return -1;
+    if (major != 10 || minor != 3) n = -1;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  *sms = n;
+  return n > 0 ? dev : -1;
 }
+
+// Let `kernel` have `bytes` of dynamic shared memory on device `dev`: once a device.
+struct SmemLimit {
+  std::atomic<bool> done[kMaxDevices];
+  template <class K>
+  cudaError_t set(K kernel, size_t bytes, int dev) {
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
 
 }  // namespace
 }  // namespace moe

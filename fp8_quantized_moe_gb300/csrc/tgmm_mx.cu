@@ -660,8 +660,9 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
                  MOE_ERR_INVALID_ARG);
   const int64_t ktiles = (K + 2 * kBM - 1) / (2 * kBM), ntiles = (N + kBN - 1) / kBN, total = E_local * ktiles * ntiles;
   MOE_HOST_CHECK(total < (1ll << 31), MOE_ERR_INVALID_ARG);
-  const int sms = sm103_count();
-  if (sms <= 0) return MOE_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int dev = sm103_device(&sms);
+  if (dev < 0) return MOE_ERR_UNSUPPORTED;
   cudaStream_t st = as_stream(stream);
   if (M == 0) {
     MOE_CUDA_TRY(cudaMemsetAsync(out, 0, static_cast<size_t>(E_local) * K * N * 4, st));
@@ -682,8 +683,8 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   const Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(K), static_cast<int>(N),
                  static_cast<int>(ktiles), static_cast<int>(ntiles), l.nrb_a, l.nrb_b, ws + l.sf_a, ws + l.sf_b, out,
                  moe_detail_stall_ns()};
-  MOE_CUDA_TRY(cudaFuncSetAttribute(tgmm_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kSmem)));
+  static SmemLimit limit;
+  MOE_CUDA_TRY(limit.set(tgmm_mx_kernel, kSmem, dev));
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -699,21 +700,13 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   cfg.numAttrs = 1;
   // pairs that are resident at once, per device (fewer than half of the SMs where a
   // cluster of SMs has an odd number: a pair more than that would run after all others)
-  static std::mutex mu;
-  static int resident[kMaxDevices] = {};
-  int dev = 0, pairs = 0;
-  MOE_CUDA_TRY(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    pairs = resident[dev];
-  }
+  static std::atomic<int> resident[kMaxDevices];
+  int pairs = resident[dev].load(std::memory_order_relaxed);
   if (pairs == 0) {
     cfg.gridDim = dim3(2 * (sms / 2));
     MOE_CUDA_TRY(cudaOccupancyMaxActiveClusters(&pairs, tgmm_mx_kernel, &cfg));
     if (pairs <= 0) return MOE_ERR_UNSUPPORTED;
-    std::lock_guard<std::mutex> lock(mu);
-    resident[dev] = pairs;
+    resident[dev].store(pairs, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(total, pairs)));
   cfg.numAttrs = 2;
