@@ -658,7 +658,9 @@ def gather_scale_quant_block(G: torch.Tensor, w: Optional[torch.Tensor], sorted_
     T, D = _arg(what, G, torch.bfloat16, 2).shape
     R, dev, at = T * k, _dev(what, G), G.device
     pG = _ptr(what, G, torch.bfloat16, (T, D), dev)
-    pw = None if w is None else _ptr(what + " w", w.view(-1), torch.float32, (R,), dev)
+    if w is not None and w.numel() != R:
+        raise MoEError(f"{what} w: expected {R} values, got {list(w.shape)}")
+    pw = None if w is None else _ptr(what + " w", w, torch.float32, w.shape, dev)
     ps = _ptr(what + " sorted_src", sorted_src, torch.int32, (R,), dev)
     dO = torch.empty(R, D, dtype=torch.bfloat16, device=at)
     dO_q = torch.empty(R, D, dtype=torch.uint8, device=at)
@@ -1159,6 +1161,8 @@ def ffn_backward(dY: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, buf: 
     if W.in_mode == PER_BLOCK128:
         if W.w_in_t is None or x is None:
             raise MoEError("ffn_backward: PER_BLOCK128 weights made with for_backward, and x, are needed")
+        if not buf.keep_a:
+            raise MoEError("ffn_backward: buffers made with backward=True are needed")
         sizes, ws = s["group_sizes"], buf.tgmm_workspace(W.w_in.shape[0])
         dO, dO_q, dO_s = gather_scale_quant_block(dY, topk_w, s["sorted_src"], k)
         gmm_block(dO_q, dO_s, W.w_out_t, W.s_out_t, sizes, out=buf.dH)

@@ -208,3 +208,21 @@ def test_router_backward_adds_the_loss_gradient():
     assert (gg.double() - want).norm() <= 2e-3 * want.norm()
     want = dl.double() @ wg.double()
     assert (sg.double() - want).norm() <= (2.0 ** -8 + 1e-5) * want.norm()
+
+
+def test_offsets_past_32_bits():
+    T, E = 2_200_000, 1000
+    g = torch.Generator(device="cuda").manual_seed(11)
+    logits = torch.empty(T, E, device="cuda")
+    for part in logits.split(200_000):
+        part.normal_(generator=g)
+    ids = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    b = moe.router_balance_loss(logits, ids, 1.0, seqs=11)
+    d = moe.router_balance_loss_backward(logits, b)
+    assert moe.device_error() == 0 and int(b.counts.sum()) == T
+    p = torch.softmax(logits[-200_000:].double(), 1)
+    mean = p.mean(0)
+    assert ((b.mean[10].double() - mean).abs() <= 1e-5 * mean).all()
+    c = b.counts[10].double() * E / 11 / 200_000 / 200_000
+    want = p[-100:] * (c - (p[-100:] @ c).unsqueeze(1))
+    assert ((d[-100:].double() - want).abs() <= 1e-5 * want.abs().amax()).all()

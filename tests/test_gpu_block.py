@@ -330,18 +330,72 @@ def test_on_two_streams_at_once():
     assert moe.device_error() == 0
 
 
-def test_a_wait_that_runs_out_is_reported():
-    a = product_case(25, 300, 256, 272, 1)
-    x, d = gradient_case(26, 300, 300, 64, 272)
-    sizes = sizes_tensor([300])
-    y, dw = moe.gmm_block(*a), moe.tgmm_mx(x, d, sizes)
+@pytest.mark.parametrize("M,K,N,E", [
+    (300, 256, 272, 1),     # the producer has issued all it has and is done
+    (4096, 512, 1024, 8),   # several tiles a CTA: every role waits
+    (1, 4096, 512, 1),      # a tile shared by eight CTAs
+    (65, 2048, 48, 1),      # by two, an N tail
+])
+def test_a_wait_that_runs_out_is_reported(M, K, N, E):
+    a = product_case(25, M, K, N, E)
+    x, d = gradient_case(26, M, M, K, N)
+    sizes = sizes_tensor(ragged_sizes(np.random.default_rng(M), E, M))
+    y, dw = moe.gmm_block(*a, sizes), moe.tgmm_mx(x, d, sizes)
     assert moe.device_error() == 0
-    for call in (lambda: moe.gmm_block(*a), lambda: moe.tgmm_mx(x, d, sizes)):
-        moe.lib().moe_test_stall_consumers(20_000_000)
+    for call in (lambda: moe.gmm_block(*a, sizes), lambda: moe.tgmm_mx(x, d, sizes)):
+        moe.lib().moe_test_stall_consumers(200_000)
         try:
             call()
             assert moe.device_error() == 0x4
         finally:
             moe.lib().moe_test_stall_consumers(0)
-    assert torch.equal(moe.gmm_block(*a), y) and torch.equal(moe.tgmm_mx(x, d, sizes), dw)
+    assert torch.equal(moe.gmm_block(*a, sizes), y) and torch.equal(moe.tgmm_mx(x, d, sizes), dw)
     assert moe.device_error() == 0
+
+
+@pytest.mark.parametrize("M", [1, 3, 40, 64, 100, 128, 129])
+@pytest.mark.parametrize("K", [1024, 2048, 4096, 7168])
+def test_tiles_shared_by_several_ctas(M, K):
+    """Few tiles and many K blocks: one, two, four and eight CTAs a tile."""
+    a = product_case(M + K, M, K, 528, 1)
+    check_product(moe.gmm_block(*a), *ref.gmm(*a, [M]), K)
+    assert moe.device_error() == 0
+    a = product_case(M + K + 1, M, K, 272, 2)
+    for sizes in ([M, 0], [0, M], [M // 2, M - M // 2]):
+        out = moe.gmm_block(*a, sizes_tensor(sizes))
+        check_product(out, *ref.gmm(*a, sizes), K)
+    # and as the only local one of three groups, the others' rows zeroed
+    a = product_case(M + K + 2, M + 50, K, 144, 1)
+    out = torch.full((M + 50, 144), 5.0, dtype=torch.bfloat16, device="cuda")
+    moe.gmm_block(*a, sizes_tensor([20, M, 30]), group_offset=1, out=out)
+    check_product(out, *ref.gmm(*a, [20, M, 30], 1), K)
+    assert moe.device_error() == 0
+
+
+def test_offsets_past_32_bits():
+    # 2.4e9 outputs and 2.2e9 lhs codes of a product
+    M, K, N = 300_000, 7296, 8192
+    g = gen(30)
+    a = torch.randint(0, 0x70, (M, K), generator=g, device="cuda", dtype=torch.uint8)
+    sa = rand_scales(g, M, K // 128)
+    w, sw = rand_codes(g, 1, N, K), rand_scales(g, 1, N // 128, K // 128)
+    out = moe.gmm_block(a, sa, w, sw)
+    rows = torch.tensor([0, 131_071, 262_143, 262_144, 294_000, 299_999], device="cuda")
+    check_product(out[rows], *ref.gmm(a[rows].contiguous(), sa[rows].contiguous(), w, sw, [len(rows)]), K)
+    del a, out
+    # 2.3e9 gradients, and 2.6e9 weight codes
+    El, K, N = 9, 16384, 15680
+    x, d = gradient_case(31, 70, 70, K, N)
+    out = moe.tgmm_mx(x, d, sizes_tensor([5, 0, 30, 0, 0, 0, 0, 0, 35]))
+    assert moe.device_error() == 0
+    last = ref.round_rows(x[35:]).t()[-200:] @ ref.round_rows(d[35:])
+    assert ((out[8, -200:].double() - last).abs() <= 1e-5 * last.abs() + 1e-5 * last.abs().amax()).all()
+    assert not out[1].any() and not out[7].any()
+    del out
+    E, N, K = 10, 16000, 16384
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    w[9, 15872:] = torch.randn(128, K, generator=g, device="cuda").bfloat16()
+    q, s, q_t, s_t = moe.quantize_weights_block(w, transposed=True)
+    vq, vs = ref.quantise_blocks(w[9:, 15872:].contiguous())
+    assert torch.equal(ref.e4m3(q[9, 15872:])[None], vq) and torch.equal(s[9, 124:].double()[None], vs)
+    assert torch.equal(q_t[9, :, 15872:], q[9, 15872:].t()) and torch.equal(s_t[9, :, 124], s[9, 124])

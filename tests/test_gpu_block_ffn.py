@@ -171,6 +171,14 @@ def test_refusals():
     W = moe.prepare_weights(w_in, w_out, moe.PER_BLOCK128, for_backward=True)
     with pytest.raises(moe.MoEError, match="and x"):
         moe.ffn_backward(dY, w, W, buf)
+    small = moe.FFNBuffers(T, D, E, k, F, moe.PER_ROW_BLOCK128, "cuda")
+    moe.ffn_forward(x, ids, w, W, moe.PER_ROW_BLOCK128, small)
+    with pytest.raises(moe.MoEError, match="backward=True"):
+        moe.ffn_backward(dY, w, W, small, x=x)
+    with pytest.raises(moe.MoEError, match="static"):
+        moe.ffn_backward(dY, w, moe.prepare_weights(w_in, w_out, moe.PER_ROW), buf)
+    with pytest.raises(moe.MoEError, match="expected 4 values"):
+        moe.gather_scale_quant_block(dY, w[:2], torch.zeros(T, dtype=torch.int32, device="cuda"), 1)
     with pytest.raises(moe.MoEError, match="decode_weights"):
         moe.ffn_decode(x, ids, w, W)
     with pytest.raises(moe.MoEError):
