@@ -759,10 +759,15 @@ class BalanceLoss:
     loss: torch.Tensor    # fp32 [1]
     counts: torch.Tensor  # int32 [seqs, E]: pairs of valid rows routed to each expert
     mean: torch.Tensor    # fp32 [seqs, E]: mean probability over valid rows
-    tokens: torch.Tensor  # int32 [seqs]: valid rows
+    state: torch.Tensor   # the call's workspace, its last words the sequences' valid rows
     k: int
     coef: float
     valid: Optional[torch.Tensor] = None
+
+    @property
+    def tokens(self) -> torch.Tensor:
+        """int32 [seqs]: valid rows."""
+        return self.state.view(torch.int32)[-self.counts.shape[0]:]
 
 
 def router_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, coef: float = 1.0, seqs: int = 1,
@@ -784,11 +789,11 @@ def router_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, coef: floa
     loss = torch.empty(1, dtype=torch.float32, device=at)
     counts = torch.empty(seqs, E, dtype=torch.int32, device=at)
     mean = torch.empty(seqs, E, dtype=torch.float32, device=at)
-    tokens = torch.empty(seqs, dtype=torch.int32, device=at)
-    ws = torch.empty(nws, dtype=torch.uint8, device=at)
+    state = torch.empty(nws + 4 * seqs, dtype=torch.uint8, device=at)
+    ws = state.data_ptr()
     check(L.moe_router_balance(pl, pi, pv, T, E, k, seqs, coef, loss.data_ptr(), counts.data_ptr(), mean.data_ptr(),
-                               tokens.data_ptr(), ws.data_ptr(), nws, _s()), "moe_router_balance")
-    return BalanceLoss(loss, counts, mean, tokens, k, coef, valid)
+                               ws + nws, ws, nws, _s()), "moe_router_balance")
+    return BalanceLoss(loss, counts, mean, state, k, coef, valid)
 
 
 def router_balance_loss_backward(logits: torch.Tensor, b: BalanceLoss, grad: Optional[torch.Tensor] = None,
@@ -798,10 +803,11 @@ def router_balance_loss_backward(logits: torch.Tensor, b: BalanceLoss, grad: Opt
     dlogits_aux."""
     what = "router_balance_loss_backward"
     T, E = _arg("router_balance_loss_backward logits", logits, torch.float32, 2).shape
-    seqs, dev = b.tokens.shape[0], _dev(what, logits)
+    seqs, dev = b.counts.shape[0], _dev(what, logits)
     pl = _ptr("router_balance_loss_backward logits", logits, torch.float32, (T, E), dev)
     pc = _ptr("router_balance_loss_backward counts", b.counts, torch.int32, (seqs, E), dev)
-    pt = _ptr("router_balance_loss_backward tokens", b.tokens, torch.int32, (seqs,), dev)
+    ns = b.state.numel()
+    pt = _ptr(what + " state", b.state, torch.uint8, (ns,), dev) + ns - 4 * seqs
     pv = None if b.valid is None else _ptr("router_balance_loss_backward valid", b.valid, torch.bool, (T,), dev)
     pg = None if grad is None else _ptr("router_balance_loss_backward grad", grad, torch.float32, (1,), dev)
     out = torch.empty(T, E, dtype=torch.float32, device=logits.device) if out is None else out

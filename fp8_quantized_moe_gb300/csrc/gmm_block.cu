@@ -300,9 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tfull0 = smem_u32(&ctl->tfull[0]), tempty0 = smem_u32(&ctl->tempty[0]);
       const uint64_t da0 = smem_desc_sw128(base), db0 = smem_desc_sw128(base + kABytes);
       uint32_t s = 0, ph = 0, a = 0, aph = 1;
+      bool ready = false;  // the next stage is full: asked while a block's products are queued (1.59 -> 1.54 ms)
       for (int t = t0; t < total && !timed_out; t += step) {
         for (int kb = kb_lo; kb < kb_hi; ++kb) {
-          if (!wait_uniform(full0 + 8 * s, ph, abort_flag) || !wait_uniform(tempty0 + 8 * a, aph, abort_flag)) {
+          if ((!ready && !wait_uniform(full0 + 8 * s, ph, abort_flag)) ||
+              !wait_uniform(tempty0 + 8 * a, aph, abort_flag)) {
             timed_out = true;
             break;
           }
@@ -319,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s = 0;
             ph ^= 1;
           }
+          ready = __all_sync(0xffffffffu, mbar_test(full0 + 8 * s, ph));
           a ^= 1;
           aph ^= a == 0;
         }
@@ -351,12 +354,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      // the next block's scale is asked for a block ahead
-      float next = __fmul_rn(__ldg(sa + kb_lo), __ldg(sb + kb_lo));
+      // a block's scales are asked for two blocks ahead (one ahead: 1.69 instead of 1.59 ms on
+      // the large groups)
+      float next = __fmul_rn(__ldg(sa + kb_lo), __ldg(sb + kb_lo)), na = 0.f, nw = 0.f;
+      if (kb_lo + 1 < kb_hi) {
+        na = __ldg(sa + kb_lo + 1);
+        nw = __ldg(sb + kb_lo + 1);
+      }
 #pragma unroll 1
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         const uint64_t s2 = f2_pack(next, next);
-        if (kb + 1 < kb_hi) next = __fmul_rn(__ldg(sa + kb + 1), __ldg(sb + kb + 1));
+        const float ma = na, mw = nw;
+        if (kb + 2 < kb_hi) {
+          na = __ldg(sa + kb + 2);
+          nw = __ldg(sb + kb + 2);
+        }
+        next = __fmul_rn(ma, mw);
         const uint32_t a = it & 1;
         if (!wait_warp(smem_u32(&ctl->tfull[a]), (it >> 1) & 1, abort_flag)) {
           timed_out = true;

@@ -22,6 +22,19 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Whether the phase has completed, asked without waiting (try_wait may wait microseconds).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait of a whole warp that issues loads or MMAs.  Such a warp runs its loop with
 // all lanes, and only the issuing instructions are one lane's: what they take (addresses,
 // descriptors) is then the warp's, in uniform registers, and a stage costs half the clocks

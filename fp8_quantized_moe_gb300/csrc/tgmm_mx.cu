@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rank == 0) {
         const bool leader = elect_one();
         uint32_t acc = 0, s = 0, ph = 0;
+        bool ready = false;  // the next stage is full: asked while a block's products are queued
         const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]);
         const uint64_t da0 = smem_desc_sw128(base), db0 = smem_desc_sw128(base + kABytes);
         for (int t = t0; t < total && !timed_out; t += step) {
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           for (int kb = 0; kb < nkb; ++kb) {
-            if (!wait_uniform(full0 + 8 * s, ph, abort_flag)) {
+            if (!ready && !wait_uniform(full0 + 8 * s, ph, abort_flag)) {
               timed_out = true;
               break;
             }
@@ -467,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               s = 0;
               ph ^= 1;
             }
+            ready = __all_sync(0xffffffffu, mbar_test(full0 + 8 * s, ph));
           }
           if (timed_out) break;
           if (leader) mma_commit_pair_mc(smem_u32(&ctl->tfull), 0x3);
