@@ -15,6 +15,11 @@
 // and then over the blocks of a sequence in a fixed order (no floating-point atomics:
 // the result does not depend on timing); counts are integers.
 //
+// Measured, both passes: 24 rows of 128 experts 6.8 us, 4 x 4096 of 256 experts 19 us (8, 8 and
+// 10 for the three kernels; bytes 5), 32 x 8192 of 64 experts 57 us (23, 6, 25; bytes 21): the
+// small ones are launches and round trips, the last one shuffles and exponentials beside
+// the memory.  (exp_f32 and one load a lane: 84 us.)
+//
 // The gradient takes counts relative to the row's most probable expert e*: with
 // c'_e = c_e - c_{e*} the formula is the same, and where p_{e*} is near 1 the two terms
 // of the difference no longer cancel (the integers' difference is exact).
@@ -368,8 +373,8 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const float* log
 }
 
 // Lanes a row and loads a lane.  Two loads a lane where they do: half the lanes, so fewer
-// shuffles a row and more rows an instruction than with one (262144 rows of 64 experts:
-// 59 against 53 us for both passes).
+// shuffles a row and more rows an instruction than with one (262144 rows of 64 experts: 23
+// against 26.7 us for the sums, 25 against 32 for the gradient).
 template <class F>
 cudaError_t by_width(int E, F&& f) {
   if (E <= 32) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});

@@ -30,22 +30,27 @@
 // memory (the stages', which are done with) and every CTA adds up and stores a slice of
 // the columns, in the order of the CTAs.
 //
-// Bound and measurements.  A block is 554 clocks of MMA at the measured rate; the same
-// loop without any fold takes 730-760 (both accumulators handed back and forth: the two
-// are not enough to hide the way from commit to epilogue and back), with it 860-870, 2.4 to
-// 2.6 PFLOP/s where the plain product of gmm_fp8 (one accumulator a tile) has 3.1 to 3.4.
-// Measured on 49152 x 4096 x 7168, 64 of 96 groups: 851 us; 16384 x 4096 x 28672, 8 groups:
-// 1.50 ms; 16384 x 1536 x 2048 over 128 groups 109 us (floor of its bytes: 72).  On the way there:
+// Bound and measurements.  A block is 554 clocks of MMA at the measured rate, and 768 of
+// loads (48 KB at the 64 bytes a clock that an SM takes in).  On 16384 x 4096 x 28672 over
+// 8 groups in bursts: 1.38 ms; the same loop without any fold 1.29 (both accumulators handed
+// back and forth), without fold and MMAs 1.03, the hand-over alone 0.81: what is left is
+// loads, MMAs and hand-over in turn.  Run back to back the power limit lowers the clock and it
+// takes 1.53 ms, 2.5 PFLOP/s; the plain product of gmm_fp8 (one accumulator a tile, no fold)
+// 1.40.  64 of 96 groups of 49152 x 4096 x 7168: 956 us (a last tile of some 60 of 128
+// rows in each group of 512); 16384 x 1536 x 2048 over 128 groups: 91 us, its bytes 72.
+// On the way there (burst or back to back alike):
 //   - tensor-memory loads of 16 columns, two at a time, against 32 columns: 2.4 against
 //     1.7 PFLOP/s (32 registers in a row cost moves and spills);
 //   - the epilogue's waits sleeping in the barrier (a suspend-time hint) against polling:
 //     5 %; polling without pause made even the loop without a fold 20 % slower: the
 //     polls take shared memory's time from the MMA's operands;
-//   - pairs of CTAs on 256 x 256 tiles (half of B each): 1.55 against 1.50 ms on the large groups,
-//     906 against 851 us on ragged ones (256-row tiles leave more rows empty);
-//   - four accumulators of 128 columns (N = 128 MMAs read A twice as often): 1.93 ms;
-//   - 16 epilogue warps of 64 columns: 1.69 ms; the next block's first columns loaded
-//     before a block's last sums: 1.74 ms.
+//   - scales two blocks ahead against one, and the issuing warp's early look at the next
+//     stage: 6 and 3 %;
+//   - pairs of CTAs on 256 x 256 tiles (half of B each): 5 to 8 % slower on ragged groups
+//     (256-row tiles leave more rows empty), level on the large ones;
+//   - four accumulators of 128 columns (N = 128 MMAs read A twice as often): 25 % slower;
+//   - 16 epilogue warps of 64 columns: 10 % slower; the next block's first columns loaded
+//     before a block's last sums: 12 %.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets what
 // it issued finish and returns.

@@ -35,13 +35,14 @@
 //     Tiles run expert-major, then n tile, then k tile.
 //     One CTA per 128 x 256 tile needs 48 KB a block and SM, 768 clocks at the 64 bytes a
 //     clock that an SM takes in; a pair needs 32 KB.
-//     Measured: 16384 rows, 4096 x 28672, 8 experts 1.60 ms with the rounding (0.30);
-//     without the stores 1.33, without the MMAs 1.35, with neither 0.96: loads, MMAs and
-//     stores (3.8 GB) overlap only in part.  One CTA a 128 x 256 tile, its issuing loops run by
-//     one lane and its scales by tcgen05.cp: 1.87; the pair with such loops: 1.75.  49152
-//     rows, 4096 x 2816, 64 experts: 835 us; 16384 rows, 2048 x 1536, 128 experts: 331 us
-//     (1.6 GB of gradients; stores alone 260).  Stores by TMA from shared memory: 855 us and
-//     1.69 ms on the first two.
+//     Measured with the rounding, back to back: 16384 rows, 4096 x 28672, 8 experts 1.70 ms
+//     (rounding 0.28; in bursts 1.58: the power limit lowers the clock); there without the
+//     stores 1.33, without the MMAs 1.35, with neither 0.96: loads, MMAs and stores (3.8 GB)
+//     overlap only in part.  49152 rows, 4096 x 2816, 64 experts: 800 to 840 us (rounding 187,
+//     stores alone 475); 16384 rows, 2048 x 1536, 128 experts: 312 us (47, 260).  One CTA a
+//     128 x 256 tile, its issuing loops run by one lane and its scales by tcgen05.cp: 1.87 ms,
+//     980, 376 us; the pair with such loops: 1.75 ms.  Stores by TMA from shared memory instead
+//     of the transpose: 1.69 ms, 855 us.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets what
 // it issued finish and returns.
