@@ -476,6 +476,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// Contiguous copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from
+// this CTA's shared to global memory, tracked by bulk async-groups.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+               "r"(src), "r"(bytes)
+               : "memory");
+}
+
 // 4-byte asynchronous copy global -> shared through L1 (cp.async); with
 // src_bytes 0 nothing is read and the destination is zero-filled.
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {

@@ -46,8 +46,8 @@
 //     polls take shared memory's time from the MMA's operands;
 //   - scales two blocks ahead against one, and the issuing warp's early look at the next
 //     stage: 6 and 3 %;
-//   - pairs of CTAs on 256 x 256 tiles (half of B each): 5 to 8 % slower on ragged groups
-//     (256-row tiles leave more rows empty), level on the large ones;
+//   - pairs of CTAs on 256 x 256 tiles (half of B each): 3 % slower on the large groups and on
+//     64 of 96, 22 % on 128 small ones (256-row tiles leave more rows empty);
 //   - four accumulators of 128 columns (N = 128 MMAs read A twice as often): 25 % slower;
 //   - 16 epilogue warps of 64 columns: 10 % slower; the next block's first columns loaded
 //     before a block's last sums: 12 %.

@@ -72,15 +72,15 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // A byte matrix [rows, cols] of row pitch `pitch` for boxes of box_rows x 128
-// bytes in the 128-byte swizzle; reads past the extents return zeros.
+// bytes in the 128-byte swizzle, or as they lie; reads past the extents return zeros.
 inline bool make_map_u8(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t pitch,
-                        uint32_t box_rows) {
+                        uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
   cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -13,13 +13,14 @@
 // value alone.
 //
 // Two kernels:
-//   round_rows_kernel  both operands to codes in the workspace, transposed to
-//     [128-row block][column][128 rows], every expert padded to whole blocks with
-//     zeros; the scale codes as the atoms that tcgen05.cp copies (32 x 16 bytes for 128
-//     columns: byte 16 l + 4 c + j holds column 32 c + l, rows 32 j..).  Bound by memory
-//     (2 bytes read, 1 written): a thread holds 8 columns of 8 consecutive rows, so
-//     that a column's codes are 8 bytes of its own registers and a warp's stores fill
-//     whole sectors; maxima of 32 rows are among 4 lanes.
+//   round_rows_kernel  both operands to codes in the workspace, transposed: for 128 rows
+//     of an expert (padded with zeros) and 128 columns a 16 KB tile, the image that the MMA
+//     reads from shared memory (128 lines of 128 rows' codes, 128-byte swizzle); the scale
+//     codes as the 32 x 16-byte atoms that go to tensor memory.  Line p of a tile holds column
+//     64 (p / 8 % 2) + 8 (p % 8) + p / 16: a lane has 8 columns of 8 consecutive rows, and in
+//     this order the 8-byte pieces of a warp's lanes fall on different banks.  A tile goes out
+//     as one bulk copy (stored by the lanes, 8 bytes each, L1 was the busiest unit).  Maxima
+//     of 32 rows are among 4 lanes.  Bound by memory: 2 bytes read, 1 written.
 //   tgmm_mx_kernel  persistent pairs of CTAs, 256 (k) x 256 (n) tiles, 128 rows of
 //     k and half of B a CTA (16 warps, one CTA per SM):
 //     warp 0       TMA producer: per stage one block of 128 rows, A 16 KB and half of B
@@ -35,14 +36,15 @@
 //     Tiles run expert-major, then n tile, then k tile.
 //     One CTA per 128 x 256 tile needs 48 KB a block and SM, 768 clocks at the 64 bytes a
 //     clock that an SM takes in; a pair needs 32 KB.
-//     Measured with the rounding, back to back: 16384 rows, 4096 x 28672, 8 experts 1.70 ms
-//     (rounding 0.28; in bursts 1.58: the power limit lowers the clock); there without the
+//     Measured with the rounding, back to back: 16384 rows, 4096 x 28672, 8 experts 1.68 ms
+//     (rounding 0.26; in bursts 1.55: the power limit lowers the clock); there without the
 //     stores 1.33, without the MMAs 1.35, with neither 0.96: loads, MMAs and stores (3.8 GB)
-//     overlap only in part.  49152 rows, 4096 x 2816, 64 experts: 800 to 840 us (rounding 187,
-//     stores alone 475); 16384 rows, 2048 x 1536, 128 experts: 312 us (47, 260).  One CTA a
+//     overlap only in part.  49152 rows, 4096 x 2816, 64 experts: 790 us (rounding 166,
+//     stores alone 475); 16384 rows, 2048 x 1536, 128 experts: 306 us (39, 260).  One CTA a
 //     128 x 256 tile, its issuing loops run by one lane and its scales by tcgen05.cp: 1.87 ms,
-//     980, 376 us; the pair with such loops: 1.75 ms.  Stores by TMA from shared memory instead
-//     of the transpose: 1.69 ms, 855 us.
+//     980, 376 us; the pair with such loops: 1.75 ms; tiles stored by the lanes 3 % more
+//     (rounding 0.28 ms, 187, 47 us).  Gradients by TMA from shared memory instead of the
+//     transpose: 1.69 ms and 855 us where it gave 1.60 and 835.
 //
 // Every wait is bounded; on expiry the kernel raises MOE_DEVERR_TIMEOUT, lets what
 // it issued finish and returns.
@@ -57,6 +59,7 @@ __device__ unsigned int g_err;
 
 constexpr int kRB = 128;  // rows of a block (four scales a column)
 constexpr int kAtom = 512;
+constexpr int kTileBytes = 128 * kRB;
 
 // ---- local groups --------------------------------------------------------
 struct Tables {
@@ -143,7 +146,7 @@ struct Operand {
   int k;
   int64_t src_rows;
   int C, ncb, nrb;     // columns; 128-column blocks; atoms a row block (a multiple of what a tile reads)
-  uint8_t* q;          // [row blocks][C][128]
+  uint8_t* q;          // [row blocks][ncb][kTileBytes]
   uint8_t* sf;         // [row blocks][nrb][512]
 };
 
@@ -160,6 +163,7 @@ __global__ void __launch_bounds__(256, 4) round_rows_kernel(const Operand oa, co
                                                             int E, int g0, int El, int64_t M) {
   __shared__ Tables t;
   __shared__ __align__(16) uint8_t sfs[2][kAtom];
+  __shared__ __align__(128) uint8_t tile[2][kTileBytes];
   grid_release_next();  // (the product's kernel takes over the SMs as they come free)
   if (!build_tables(sizes, E, g0, El, M, &t)) return;  // (the product's kernel raises the error)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -216,28 +220,35 @@ __global__ void __launch_bounds__(256, 4) round_rows_kernel(const Operand oa, co
       m[c] = __vmaxu2(m[c], __shfl_xor_sync(0xffffffffu, m[c], 8));
       m[c] = __vmaxu2(m[c], __shfl_xor_sync(0xffffffffu, m[c], 16));
     }
-    uint8_t* q = o.q + (static_cast<int64_t>(kb) * o.C + c0) * kRB + 32 * j + 8 * rl;
+    // column 64 (warp / 4) + 8 (lane % 8) + c is line 16 c + 8 (warp / 4) + lane % 8
+    const int line0 = 8 * (warp >> 2) + (lane & 7);
+    uint8_t* t0 = tile[sel] + line0 * 128 + (((2 * j + (rl >> 1)) ^ (lane & 7)) << 4) + 8 * (rl & 1);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       float inv;
       const uint32_t code = block_scale((c & 1) ? m[c >> 1] >> 16 : m[c >> 1] & 0xFFFFu, inv);
-      if (rl == 0) {
-        const int cc = cu + c;  // column of the 128
-        sfs[sel][16 * (cc & 31) + 4 * (cc >> 5) + j] = static_cast<uint8_t>(code);
-      }
+      const int line = 16 * c + line0;
+      if (rl == 0) sfs[sel][16 * (line & 31) + 4 * (line >> 5) + j] = static_cast<uint8_t>(code);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t x = (c >> 1) == 0 ? d[i].x : (c >> 1) == 1 ? d[i].y : (c >> 1) == 2 ? d[i].z : d[i].w;
         v[i] = __fmul_rn((c & 1) ? bf16hi(x) : bf16lo(x), inv);  // exact: a power of two
       }
-      if (c0 < o.C) *reinterpret_cast<uint2*>(q + c * kRB) = pack_e4m3x8(v);
+      *reinterpret_cast<uint2*>(t0 + 16 * 128 * c) = pack_e4m3x8(v);
     }
-    __syncthreads();  // (the two buffers alternate: one barrier a tile)
+    fence_proxy_async_smem();
+    if (tid == 0) bulk_wait_read<0>();  // the last tile's copy has read the other buffer, which is written next
+    __syncthreads();                    // (one barrier a tile: the buffers alternate)
+    if (tid == 0) {
+      bulk_store(o.q + (static_cast<int64_t>(kb) * o.ncb + cb) * kTileBytes, smem_u32(tile[sel]), kTileBytes);
+      bulk_commit();
+    }
     if (tid < 32)
       *reinterpret_cast<uint4*>(o.sf + (static_cast<int64_t>(kb) * o.nrb + cb) * kAtom + 16 * tid) =
           *reinterpret_cast<const uint4*>(&sfs[sel][16 * tid]);
   }
+  if (tid == 0) bulk_wait_all();
 }
 
 // ---- product -------------------------------------------------------------
@@ -261,6 +272,7 @@ struct Params {
   int E, g0, El;
   int64_t M;
   int K, N, ktiles, ntiles;
+  int ncb_a, ncb_b;  // 128-column blocks
   int nrb_a, nrb_b;
   const uint8_t* sf_a;
   const uint8_t* sf_b;
@@ -393,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nkb = (tl.rows + kRB - 1) / kRB;
         const uint8_t* fa = p.sf_a + (static_cast<int64_t>(tl.kb0) * p.nrb_a + tl.k0 / 128) * kAtom;
         const uint8_t* fbp = p.sf_b + (static_cast<int64_t>(tl.kb0) * p.nrb_b + tl.n0 / 128) * kAtom;
-        int ya = tl.kb0 * p.K + tl.k0, yb = tl.kb0 * p.N + tl.n0 + rank * (kBN / 2);
+        // lines of the tiles (past an operand's last block: the next row block's, never stored)
+        int ya = (tl.kb0 * p.ncb_a + tl.k0 / 128) * 128, yb = (tl.kb0 * p.ncb_b + tl.n0 / 128 + rank) * 128;
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           if (!wait_uniform(empty0 + 8 * s, ph, abort_flag)) {
             timed_out = true;
@@ -410,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fa += p.nrb_a * kAtom;
           fbp += p.nrb_b * kAtom;
-          ya += p.K;
-          yb += p.N;
+          ya += p.ncb_a * 128;
+          yb += p.ncb_b * 128;
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
@@ -550,39 +563,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c) v[i][c] = 0;
       }
-      // Lane 4 a + q has a row's columns; after a transpose of 8-column pieces in each four
-      // lanes it has columns 8 q.. of rows 4 a .. 4 a + 3, so that a store instruction
-      // writes 8 rows x 128 bytes and not 32 rows x 32 (370 -> 331 us on 128 small experts).
-      const int k = tl.k0 + q4 * 32 + (lane & ~3), n = tl.n0 + half * (kBN / 2) + (lane & 3) * 8;
+      // The accumulator's rows and columns are lines of the operands' tiles: column 16 c + b of
+      // this warp's 128 is n = 8 b + c, lane l of the warp k = 64 (l / 8 % 2) + 8 (l % 8) +
+      // l / 16 + 2 q4.  A lane has a row; after a transpose of 8-column pieces in each four lanes it
+      // has columns 8 q.. (q = l % 4) of four rows 8 apart, so that a store instruction writes
+      // 8 rows x 128 bytes and not 32 rows x 32 (370 -> 331 us on 128 small experts).
+      const int k = tl.k0 + 64 * ((lane >> 3) & 1) + 8 * (lane & 4) + (lane >> 4) + 2 * q4;
+      const int n = tl.n0 + half * (kBN / 2) + (lane & 3) * 8;
       const bool odd = lane & 1, high = lane & 2;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        uint32_t y[4][8];  // pieces 4 i + j of the lane's row
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t &x0 = v[i][c], &x1 = v[i][8 + c], &x2 = v[i][16 + c], &x3 = v[i][24 + c];
-          const uint32_t s01 = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
-          const uint32_t s23 = __shfl_xor_sync(0xffffffffu, odd ? x2 : x3, 1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j][c] = v[(16 * c + 4 * i + j) >> 5][(16 * c + 4 * i + j) & 31];
+          const uint32_t s01 = __shfl_xor_sync(0xffffffffu, odd ? y[0][c] : y[1][c], 1);
+          const uint32_t s23 = __shfl_xor_sync(0xffffffffu, odd ? y[2][c] : y[3][c], 1);
           if (odd) {
-            x0 = s01;
-            x2 = s23;
+            y[0][c] = s01;
+            y[2][c] = s23;
           } else {
-            x1 = s01;
-            x3 = s23;
+            y[1][c] = s01;
+            y[3][c] = s23;
           }
-          const uint32_t s02 = __shfl_xor_sync(0xffffffffu, high ? x0 : x2, 2);
-          const uint32_t s13 = __shfl_xor_sync(0xffffffffu, high ? x1 : x3, 2);
+          const uint32_t s02 = __shfl_xor_sync(0xffffffffu, high ? y[0][c] : y[2][c], 2);
+          const uint32_t s13 = __shfl_xor_sync(0xffffffffu, high ? y[1][c] : y[3][c], 2);
           if (high) {
-            x0 = s02;
-            x1 = s13;
+            y[0][c] = s02;
+            y[1][c] = s13;
           } else {
-            x2 = s02;
-            x3 = s13;
+            y[2][c] = s02;
+            y[3][c] = s13;
           }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (k + j < p.K && n + 32 * i < p.N)
-            store8(p.out + (static_cast<int64_t>(tl.el) * p.K + k + j) * p.N + n + 32 * i, &v[i][8 * j], wide);
+          if (k + 8 * j < p.K && n + 32 * i < p.N)
+            store8(p.out + (static_cast<int64_t>(tl.el) * p.K + k + 8 * j) * p.N + n + 32 * i, y[j], wide);
       }
     }
     if (timed_out) {
@@ -607,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // and scale atoms.
 struct Layout {
   int64_t blocks;
-  int nrb_a, nrb_b;
+  int ncb_a, ncb_b, nrb_a, nrb_b;
   int64_t q_a, q_b, sf_a, sf_b, bytes;
 };
 
@@ -616,13 +634,15 @@ bool make_layout(int64_t M, int64_t K, int64_t N, int El, Layout* l) {
       N >= (1 << 30) || El <= 0 || El > kMaxGroups)
     return false;
   l->blocks = M == 0 ? 0 : (M - 1) / kRB + El;  // sum of ceil(size / 128), at the most
-  const int64_t most = std::max(K, N);
-  if (l->blocks > ((1ll << 31) - 1) / most - 1) return false;
+  l->ncb_a = static_cast<int>((K + 127) / 128);
+  l->ncb_b = static_cast<int>((N + 127) / 128);
+  const int64_t most = 128ll * std::max(l->ncb_a, l->ncb_b);
+  if (l->blocks > ((1ll << 31) - 1) / most - 2) return false;  // (a tile's lines are counted in 32 bits)
   l->nrb_a = static_cast<int>((K + 255) / 256) * 2;  // (a tile reads two of either)
   l->nrb_b = static_cast<int>((N + 255) / 256) * 2;
   l->q_a = 0;
-  l->q_b = l->q_a + l->blocks * K * kRB;
-  l->sf_a = l->q_b + l->blocks * N * kRB;
+  l->q_b = l->q_a + l->blocks * l->ncb_a * kTileBytes;
+  l->sf_a = l->q_b + l->blocks * l->ncb_b * kTileBytes;
   l->sf_b = l->sf_a + l->blocks * l->nrb_a * kAtom;
   l->bytes = l->sf_b + l->blocks * l->nrb_b * kAtom;
   return true;
@@ -673,18 +693,20 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   CUtensorMap A, B;
-  if (!make_map_u8(&A, ws + l.q_a, kRB, static_cast<uint64_t>(l.blocks) * K, kRB, kBM)) return MOE_ERR_CUDA;
-  if (!make_map_u8(&B, ws + l.q_b, kRB, static_cast<uint64_t>(l.blocks) * N, kRB, kBN / 2)) return MOE_ERR_CUDA;
-  const Operand oa{lhs, lhs_index, k, lhs_rows, static_cast<int>(K), static_cast<int>((K + 127) / 128), l.nrb_a,
+  constexpr auto plain = CU_TENSOR_MAP_SWIZZLE_NONE;  // (a tile is the swizzled image already)
+  if (!make_map_u8(&A, ws + l.q_a, kRB, static_cast<uint64_t>(l.blocks) * l.ncb_a * 128, kRB, kBM, plain) ||
+      !make_map_u8(&B, ws + l.q_b, kRB, static_cast<uint64_t>(l.blocks) * l.ncb_b * 128, kRB, kBN / 2, plain))
+    return MOE_ERR_CUDA;
+  const Operand oa{lhs, lhs_index, k, lhs_rows, static_cast<int>(K), l.ncb_a, l.nrb_a,
                    ws + l.q_a, ws + l.sf_a};
-  const Operand ob{rhs, nullptr, 1, M, static_cast<int>(N), static_cast<int>((N + 127) / 128), l.nrb_b,
+  const Operand ob{rhs, nullptr, 1, M, static_cast<int>(N), l.ncb_b, l.nrb_b,
                    ws + l.q_b, ws + l.sf_b};
   const int64_t rounds = l.blocks * (oa.ncb + ob.ncb);
   round_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(rounds, sms * 4)), 256, 0, st>>>(
       oa, ob, group_sizes, E, group_offset, E_local, M);
   MOE_CUDA_TRY(cudaGetLastError());
   const Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(K), static_cast<int>(N),
-                 static_cast<int>(ktiles), static_cast<int>(ntiles), l.nrb_a, l.nrb_b, ws + l.sf_a, ws + l.sf_b, out,
+                 static_cast<int>(ktiles), static_cast<int>(ntiles), l.ncb_a, l.ncb_b, l.nrb_a, l.nrb_b, ws + l.sf_a, ws + l.sf_b, out,
                  moe_detail_stall_ns()};
   static SmemLimit limit;
   MOE_CUDA_TRY(limit.set(tgmm_mx_kernel, kSmem, dev));

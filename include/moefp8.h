@@ -674,11 +674,12 @@ moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale, const uin
  *             group's row stands for a row of zeros and sets MOE_DEVERR_BAD_POSITION.
  *   rhs       bf16 [M, N]; out fp32 [E_local, K, N]; a group without rows gets zeros
  *   workspace tgmm_fp8_mx_workspace_bytes(M, K, N, E_local) bytes, 16-byte aligned (no
- *             initialisation needed): about M (K + N), each group padded to 128 rows;
- *             calls that may overlap on the GPU need workspaces of their own.
+ *             initialisation needed): about M (K + N), each group padded to 128 rows, K
+ *             and N to 128; calls that may overlap on the GPU need workspaces of their own.
  * An infinity stands for 448 * 2^120, above fp32's range, and the finite values of its
- * block round to zero beside it; a NaN makes every product it enters NaN.  K % 16 == 0, N % 16 == 0, E <= 1024; every pointer but lhs_index and
- * group_sizes 16-byte aligned.  MOE_ERR_UNSUPPORTED off sm_103. */
+ * block round to zero beside it; a NaN makes every product it enters NaN.
+ * K % 16 == 0, N % 16 == 0, E <= 1024; every pointer but lhs_index and group_sizes
+ * 16-byte aligned.  MOE_ERR_UNSUPPORTED off sm_103. */
 size_t tgmm_fp8_mx_workspace_bytes(int64_t M, int64_t K, int64_t N, int E_local);
 moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const int32_t* lhs_index, int k, const uint16_t* rhs,
                        const int32_t* group_sizes, int E, int group_offset, int E_local, int64_t M, int64_t K,
