@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // (both CTAs of a pair read the same group sizes, so they leave here together)
   if (!build_tables(p.group_sizes, p.E, p.g0, p.El, p.M, &ctl->t)) {
+    grid_wait_previous();  // (this kernel never ends before the one it overlaps)
     if (threadIdx.x == 0) raise_error(&g_err, MOE_DEVERR_GROUP_SIZES);
     return;
   }

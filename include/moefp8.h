@@ -75,11 +75,11 @@ typedef enum {
 } moe_scale_mode;
 
 /* Device error word bits. */
-#define MOE_DEVERR_BAD_EXPERT_ID 0x1u /* moe_ragged_sort: id outside [0, E) */
+#define MOE_DEVERR_BAD_EXPERT_ID 0x1u /* moe_ragged_sort, moe_router_balance: id outside [0, E) */
 #define MOE_DEVERR_GROUP_SIZES 0x2u   /* gmm/tgmm: negative size or sum != M */
 #define MOE_DEVERR_TIMEOUT 0x4u       /* a bounded wait in a tcgen05 kernel ran out */
 #define MOE_DEVERR_TMEM 0x8u          /* tensor-memory allocation returned no columns */
-#define MOE_DEVERR_BAD_POSITION 0x10u /* ragged_gather_reduce: a pos entry outside [0, T*k) */
+#define MOE_DEVERR_BAD_POSITION 0x10u /* ragged_gather_reduce: a pos entry outside [0, T*k); tgmm_fp8_mx: an index */
 
 const char* moe_status_string(moe_status s);
 

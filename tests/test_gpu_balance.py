@@ -210,6 +210,25 @@ def test_router_backward_adds_the_loss_gradient():
     assert (sg.double() - want).norm() <= (2.0 ** -8 + 1e-5) * want.norm()
 
 
+def test_on_two_streams_at_once():
+    a, b = case(12, 6000, 64, 4), case(13, 3000, 300, 8)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for x, ids in (a, b):
+        r = moe.router_balance_loss(x, ids, 0.1, seqs=3)
+        want.append((r, moe.router_balance_loss_backward(x, r)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for (x, ids), st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                r = moe.router_balance_loss(x, ids, 0.1, seqs=3)
+                got.append((r, moe.router_balance_loss_backward(x, r)))
+        torch.cuda.synchronize()
+        for (r, d), (r0, d0) in zip(got, want):
+            assert torch.equal(r.loss, r0.loss) and torch.equal(r.counts, r0.counts) and torch.equal(d, d0)
+
+
 def test_offsets_past_32_bits():
     T, E = 2_200_000, 1000
     g = torch.Generator(device="cuda").manual_seed(11)

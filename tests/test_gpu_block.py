@@ -369,7 +369,37 @@ def test_tiles_shared_by_several_ctas(M, K):
     out = torch.full((M + 50, 144), 5.0, dtype=torch.bfloat16, device="cuda")
     moe.gmm_block(*a, sizes_tensor([20, M, 30]), group_offset=1, out=out)
     check_product(out, *ref.gmm(*a, [20, M, 30], 1), K)
+    # or with no row at all
+    out.fill_(5)
+    moe.gmm_block(*a, sizes_tensor([M + 20, 0, 30]), group_offset=1, out=out)
+    assert not out.any() and moe.device_error() == 0
+
+
+def test_shared_tiles_with_sizes_that_do_not_add_up():
+    a = product_case(40, 8, 7168, 272, 2)
+    for sizes in ([4, 3], [9, -1], [8, 1]):
+        moe.gmm_block(*a, sizes_tensor(sizes))
+        assert moe.device_error() & 0x2
     assert moe.device_error() == 0
+
+
+def test_two_graphs_at_once():
+    """Two captured steps with workspaces of their own, replayed on two streams."""
+    cases = [gradient_case(41 + i, 500, 500, 128, 272) for i in range(2)]
+    sizes = [sizes_tensor([300, 0, 200]), sizes_tensor([0, 499, 1])]
+    want = [moe.tgmm_mx(x, d, s) for (x, d), s in zip(cases, sizes)]
+    graphs, outs = [], []
+    for (x, d), s in zip(cases, sizes):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(moe.tgmm_mx(x, d, s))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want)) and moe.device_error() == 0
 
 
 def test_offsets_past_32_bits():
