@@ -16,7 +16,7 @@
 // the result does not depend on timing); counts are integers.
 //
 // Measured, both passes: 24 rows of 128 experts 6.8 us, 4 x 4096 of 256 experts 19 us (8, 8 and
-// 10 for the three kernels; bytes 5), 32 x 8192 of 64 experts 57 us (23, 6, 25; bytes 21): the
+// 10 for the three kernels; bytes 5), 32 x 8192 of 64 experts 55 us (21, 6, 25; bytes 21): the
 // small ones are launches and round trips, the last one shuffles and exponentials beside
 // the memory.  (exp_f32 and one load a lane: 84 us.)
 //
@@ -142,13 +142,24 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const float* log
   // pairs
   int mine = 0;
   const uint32_t pairs = hi > lo ? static_cast<uint32_t>((hi - lo) * s.k) : 0u, k = static_cast<uint32_t>(s.k);
-  for (uint32_t i = tid; i < pairs; i += kThreads) {
-    const uint32_t r = i / k;
-    if (valid && !__ldg(valid + row0 + lo + r)) continue;
-    mine += i - r * k == 0;
-    const int e = __ldg(ids + (row0 + lo) * s.k + i);
-    if (e >= 0 && e < s.E) atomicAdd(cnt + e, 1);
-    else raise_error(&g_err, MOE_DEVERR_BAD_EXPERT_ID);
+  constexpr int P = 4;  // pairs whose loads are in flight together
+  for (uint32_t i0 = tid; i0 < pairs; i0 += kThreads * P) {
+    int e[P];
+    bool on[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const uint32_t i = i0 + q * kThreads, r = i / k;
+      on[q] = i < pairs && (!valid || __ldg(valid + row0 + lo + r));
+      mine += on[q] && i - r * k == 0;
+    }
+#pragma unroll
+    for (int q = 0; q < P; ++q) e[q] = on[q] ? __ldg(ids + (row0 + lo) * s.k + i0 + q * kThreads) : 0;
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      if (!on[q]) continue;
+      if (e[q] >= 0 && e[q] < s.E) atomicAdd(cnt + e[q], 1);
+      else raise_error(&g_err, MOE_DEVERR_BAD_EXPERT_ID);
+    }
   }
   if (mine) atomicAdd(&n_tok, mine);
   // probabilities
