@@ -35,6 +35,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 from typing import Optional
 
 import torch
@@ -69,6 +70,11 @@ def lib():
     return _native.load()
 
 
+def _lib():
+    """lib() without its lock once the library is loaded."""
+    return _native._lib or _native.load()
+
+
 def _p(t: Optional[torch.Tensor]):
     if t is None:
         return None
@@ -82,6 +88,11 @@ def _p(t: Optional[torch.Tensor]):
 def _s():
     # (the raw handle: building a torch.cuda.Stream object takes longer than a launch)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _stream(dev: int) -> int:
+    """The raw handle of the current stream of `dev`, the current CUDA device."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _arg(what: str, t, dtype, ndim: int):
@@ -460,10 +471,13 @@ def gmm_block(lhs_q: torch.Tensor, lhs_s: torch.Tensor, rhs_q: torch.Tensor, rhs
     pls = _ptr("gmm_block lhs_s", lhs_s, torch.float32, (M, K // 128), dev)
     pr = _ptr("gmm_block rhs_q", rhs_q, torch.uint8, (El, N, K), dev)
     prs = _ptr("gmm_block rhs_s", rhs_s, torch.float32, (El, _nb(N), K // 128), dev)
-    out = torch.empty(M, N, dtype=torch.bfloat16, device=lhs_q.device) if out is None else out
-    po = _ptr("gmm_block out", out, torch.bfloat16, (M, N), dev)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _ptr("gmm_block out", out, torch.bfloat16, (M, N), dev)
     if M:
-        check(lib().gmm_fp8_block(pl, pls, pr, prs, pg, E, group_offset, El, M, K, N, po, _s()), "gmm_fp8_block")
+        check(_lib().gmm_fp8_block(pl, pls, pr, prs, pg, E, group_offset, El, M, K, N, po, _stream(dev)), "gmm_fp8_block")
     return out
 
 
@@ -484,7 +498,7 @@ def tgmm_mx(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Tensor, gro
     L, K = _arg("tgmm_mx lhs", lhs, torch.bfloat16, 2).shape
     M, N = _arg("tgmm_mx rhs", rhs, torch.bfloat16, 2).shape
     E = _arg("tgmm_mx group_sizes", group_sizes, torch.int32, 1).shape[0]
-    dev, at = _dev(what, lhs), lhs.device
+    dev = _dev(what, lhs)
     El = E - group_offset if E_local is None else E_local
     if lhs_rows is None and (k != 1 or L != M):
         raise MoEError(f"tgmm_mx: lhs has {L} rows and rhs {M}; lhs_rows picks rows of lhs, k at a time")
@@ -494,16 +508,19 @@ def tgmm_mx(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Tensor, gro
     pi = None if lhs_rows is None else _ptr("tgmm_mx lhs_rows", lhs_rows, torch.int32, (M,), dev)
     if El <= 0:
         raise MoEError(f"tgmm_mx: E_local is {El}")
-    out = torch.empty(El, K, N, dtype=torch.float32, device=at) if out is None else out
-    po = _ptr("tgmm_mx out", out, torch.float32, (El, K, N), dev)
+    if out is None:
+        out = torch.empty(El, K, N, dtype=torch.float32, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _ptr("tgmm_mx out", out, torch.float32, (El, K, N), dev)
     if not M:
         return out.zero_()
-    L_ = lib()
+    L_ = _lib()
     if workspace is None:
-        workspace = torch.empty(max(16, L_.tgmm_fp8_mx_workspace_bytes(M, K, N, El)), dtype=torch.uint8, device=at)
+        workspace = torch.empty(max(16, L_.tgmm_fp8_mx_workspace_bytes(M, K, N, El)), dtype=torch.uint8, device=dev)
     pw = _ptr("tgmm_mx workspace", workspace, torch.uint8, (workspace.numel(),), dev)
-    check(L_.tgmm_fp8_mx(px, L, pi, k, pd, pg, E, group_offset, El, M, K, N, po, pw, workspace.numel(), _s()),
-          "tgmm_fp8_mx")
+    check(L_.tgmm_fp8_mx(px, L, pi, k, pd, pg, E, group_offset, El, M, K, N, po, pw, workspace.numel(),
+                         _stream(dev)), "tgmm_fp8_mx")
     return out
 
 
@@ -770,6 +787,11 @@ class BalanceLoss:
         return self.state.view(torch.int32)[-self.counts.shape[0]:]
 
 
+@functools.lru_cache(maxsize=256)
+def _balance_workspace(T: int, E: int, k: int, seqs: int) -> int:
+    return int(lib().moe_router_balance_workspace_bytes(T, E, k, seqs))
+
+
 def router_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, coef: float = 1.0, seqs: int = 1,
                         valid: Optional[torch.Tensor] = None) -> BalanceLoss:
     """Balance loss of router logits fp32 [T, E] and their choices int32 [T, k], the T rows being `seqs` sequences
@@ -778,21 +800,20 @@ def router_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, coef: floa
     what = "router_balance_loss"
     T, E = _arg("router_balance_loss logits", logits, torch.float32, 2).shape
     k = _arg("router_balance_loss topk_ids", topk_ids, torch.int32, 2).shape[1]
-    dev, at = _dev(what, logits), logits.device
+    dev = _dev(what, logits)
     pl = _ptr("router_balance_loss logits", logits, torch.float32, (T, E), dev)
     pi = _ptr("router_balance_loss topk_ids", topk_ids, torch.int32, (T, k), dev)
     pv = None if valid is None else _ptr("router_balance_loss valid", valid, torch.bool, (T,), dev)
-    L = lib()
-    nws = L.moe_router_balance_workspace_bytes(T, E, k, seqs)
+    nws = _balance_workspace(T, E, k, seqs)
     if not nws:
         raise MoEError(f"router_balance_loss does not take T = {T}, E = {E}, k = {k}, seqs = {seqs}")
-    loss = torch.empty(1, dtype=torch.float32, device=at)
-    counts = torch.empty(seqs, E, dtype=torch.int32, device=at)
-    mean = torch.empty(seqs, E, dtype=torch.float32, device=at)
-    state = torch.empty(nws + 4 * seqs, dtype=torch.uint8, device=at)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    counts = torch.empty(seqs, E, dtype=torch.int32, device=dev)
+    mean = torch.empty(seqs, E, dtype=torch.float32, device=dev)
+    state = torch.empty(nws + 4 * seqs, dtype=torch.uint8, device=dev)
     ws = state.data_ptr()
-    check(L.moe_router_balance(pl, pi, pv, T, E, k, seqs, coef, loss.data_ptr(), counts.data_ptr(), mean.data_ptr(),
-                               ws + nws, ws, nws, _s()), "moe_router_balance")
+    check(_lib().moe_router_balance(pl, pi, pv, T, E, k, seqs, coef, loss.data_ptr(), counts.data_ptr(),
+                                    mean.data_ptr(), ws + nws, ws, nws, _stream(dev)), "moe_router_balance")
     return BalanceLoss(loss, counts, mean, state, k, coef, valid)
 
 
@@ -810,9 +831,12 @@ def router_balance_loss_backward(logits: torch.Tensor, b: BalanceLoss, grad: Opt
     pt = _ptr(what + " state", b.state, torch.uint8, (ns,), dev) + ns - 4 * seqs
     pv = None if b.valid is None else _ptr("router_balance_loss_backward valid", b.valid, torch.bool, (T,), dev)
     pg = None if grad is None else _ptr("router_balance_loss_backward grad", grad, torch.float32, (1,), dev)
-    out = torch.empty(T, E, dtype=torch.float32, device=logits.device) if out is None else out
-    po = _ptr("router_balance_loss_backward out", out, torch.float32, (T, E), dev)
-    check(lib().moe_router_balance_backward(pl, pv, T, E, b.k, seqs, b.coef, pc, pt, pg, po, _s()),
+    if out is None:
+        out = torch.empty(T, E, dtype=torch.float32, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _ptr("router_balance_loss_backward out", out, torch.float32, (T, E), dev)
+    check(_lib().moe_router_balance_backward(pl, pv, T, E, b.k, seqs, b.coef, pc, pt, pg, po, _stream(dev)),
           "moe_router_balance_backward")
     return out
 
