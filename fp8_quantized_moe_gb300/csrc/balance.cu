@@ -304,10 +304,12 @@ __global__ void __launch_bounds__(32 * kFinishWarps) balance_finish_kernel(Shape
   }
 }
 
+// (NV == 6: 80 registers, so that three blocks are resident as in the other pass; 67 us for 90
+// at 65536 rows of 768 experts.)
 template <int LPR, int NV>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const float* logits, const uint8_t* valid, Shape s,
-                                                                const int* counts, const int* tokens,
-                                                                const float* grad, float coef, float* dlogits) {
+__global__ void __launch_bounds__(kThreads, NV == 6 ? 3 : 1)
+    balance_grad_kernel(const float* logits, const uint8_t* valid, Shape s, const int* counts, const int* tokens,
+                        const float* grad, float coef, float* dlogits) {
   constexpr int RPW = 32 / LPR, N = 4 * NV;
   constexpr int U = NV > 2 ? 1 : 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (LPR - 1);
@@ -385,18 +387,28 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const float* log
 
 // Lanes a row and loads a lane.  Two loads a lane where they do: half the lanes, so fewer
 // shuffles a row and more rows an instruction than with one (262144 rows of 64 experts: 23
-// against 26.7 us for the sums, 25 against 32 for the gradient).
+// against 26.7 us for the sums, 25 against 32 for the gradient).  Three between the powers of
+// two, for lanes past the last expert do all the work of the others (sums and gradient, 65536
+// rows of 192 experts: 34 against 44.5 us; 131072 of 96: 40 against 49; 32768 of 384: 34
+// against 48; six loads, 65536 of 768: 122 against 140).
 template <class F>
 cudaError_t by_width(int E, F&& f) {
   if (E <= 32) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
   if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+  if (E <= 96) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 3>{});
   if (E <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+  if (E <= 192) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 3>{});
   if (E <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
+  if (E <= 384) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 3>{});
   if (E <= 512) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+  if (E <= 768) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 6>{});
   return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
 }
 
-constexpr int kBlocks = 608;  // four a streaming multiprocessor
+// Blocks at most: those that the streaming multiprocessors hold at once, by the registers of
+// a row's columns (32768 rows of 512 experts, both passes: 44 us with three a multiprocessor,
+// 56 with four; 65536 of 1000: 155 with two, 166 with four).
+int blocks_for(int E) { return 152 * (E <= 384 ? 4 : E <= 768 ? 3 : 2); }
 constexpr int kMinChunk = 32;
 
 bool make_shape(int64_t T, int E, int k, int64_t S, Shape* s) {
@@ -405,7 +417,7 @@ bool make_shape(int64_t T, int E, int k, int64_t S, Shape* s) {
   s->S = static_cast<int>(S);
   s->E = E;
   s->k = k;
-  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(kBlocks / S, (s->L + kMinChunk - 1) / kMinChunk));
+  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(blocks_for(E) / S, (s->L + kMinChunk - 1) / kMinChunk));
   s->chunk = static_cast<int>(std::max<int64_t>(1, (s->L + per - 1) / per));
   s->per = static_cast<int>(std::max<int64_t>(1, (s->L + s->chunk - 1) / s->chunk));
   return true;

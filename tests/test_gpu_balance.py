@@ -64,6 +64,16 @@ def test_loss_and_gradient(T, E, k, seqs):
     assert moe.device_error() == 0
 
 
+@pytest.mark.parametrize("E", [31, 65, 95, 96, 97, 129, 191, 192, 193, 257, 320, 384, 385, 513, 701, 768, 769, 1024])
+def test_every_width_at_its_edges(E):
+    for T, seqs in ((6, 2), (3 * 701, 3)):
+        logits, ids = case(E, T, E, 4)
+        valid = torch.arange(T, device="cuda") % 5 != 2
+        check(logits, ids, seqs=seqs)
+        check(logits, ids, seqs=seqs, valid=valid)
+    assert moe.device_error() == 0
+
+
 def test_padded_rows_count_nowhere_whatever_they_hold():
     S, L, E = 5, 70, 40
     logits, ids = case(1, S * L, E, 4)
