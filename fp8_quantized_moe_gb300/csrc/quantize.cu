@@ -233,6 +233,25 @@ struct SwigluBwdOp {  // dA0 = (dH a1) silu'(a0), dA1 = dH silu(a0); also stores
   __device__ __forceinline__ int64_t col(int u, int uu) const { return 8 * static_cast<int64_t>(u) + uu * F; }
 };
 
+// quant_n for any scale: below 2^-125 its reciprocal may overflow, so that all are divided.
+// One test for all N values, joined without branches: with a branch a value, quantising weights
+// by 128 x 128 blocks takes a quarter longer.
+template <int N>
+__device__ __forceinline__ void quant_any(const float* x, float s, float inv, float* out) {
+  const bool tiny = s < 0x1p-125f;
+  bool slow = tiny;
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(inv, inv)), out[j], out[j + 1]);
+    slow = slow | quant_needs_division(out[j]) | quant_needs_division(out[j + 1]);
+  }
+  if (slow) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (tiny || quant_needs_division(out[j])) out[j] = __fdiv_rn(x[j], s);
+  }
+}
+
 // ---- the row kernel ------------------------------------------------------
 // MODE: MOE_SCALE_PER_ROW, MOE_SCALE_PER_ROW_BLOCK128, MOE_SCALE_PER_TENSOR
 // or kModeMx32 (MXFP8, OCP MX v1.0: per 32-column block the shared exponent
@@ -345,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) rowquant_kernel(Op op, int nunits, i
           for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(x8[j], s);
           codes[i][uu] = pack_i8x8(v);
         } else {
-          quant_n<8>(x8, s, inv, v);
+          quant_any<8>(x8, s, inv, v);
           codes[i][uu] = pack_e4m3x8(v);
         }
       }
@@ -560,27 +579,18 @@ __global__ void finalize_scales_kernel(float* scale, int64_t n) {
   if (i < n) scale[i] = absmax_scale(scale[i]);
 }
 
-// quant_n for any scale: below 2^-125 its reciprocal overflows.
-template <int N>
-__device__ __forceinline__ void quant_any(const float* x, float s, float* out) {
-  if (s < 0x1p-125f) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) out[j] = __fdiv_rn(x[j], s);
-  } else {
-    quant_n<N>(x, s, __frcp_rn(s), out);
-  }
-}
-
 // ---- 128 x 128 blocks ------------------------------------------------------
 // Expert weights w [E, N, K] to e4m3 codes with one scale (amax / 448) for each 128 x
 // 128 block of an expert, and the codes of the transposed weights (the same ones).
 // One block of the matrix a CTA, read once: a warp holds 32 rows of 64 columns, a lane
 // 8 consecutive rows of 8 columns, so that a row's codes (8 bytes) and a transposed
-// row's are both in one lane's registers; four lanes fill a 32-byte sector of either.
-// 64 experts of 2 x 1408 x 4096 and 4096 x 1408 with their transposes: 1.20 ms, the bytes 0.65.
+// row's are both in one lane's registers; through shared memory they leave as whole 128-byte
+// lines.  64 experts of 2 x 1408 x 4096 and 4096 x 1408 with their transposes: 0.89 ms, the
+// bytes 0.65 (stores of 8 bytes from the registers: 0.93).
 __global__ void __launch_bounds__(256, 3) weights_block_kernel(const uint16_t* w, int64_t N, int64_t K, uint8_t* q,
                                                                float* scale, uint8_t* q_t, float* scale_t) {
   __shared__ float red[8];
+  __shared__ __align__(16) uint8_t tile[128 * 128], tile_t[128 * 128];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kbs = static_cast<int>(K / 128), nbs = static_cast<int>((N + 127) / 128);
   const int kb = blockIdx.x % kbs, nb = static_cast<int>(blockIdx.x / kbs % nbs);
@@ -602,46 +612,67 @@ __global__ void __launch_bounds__(256, 3) weights_block_kernel(const uint16_t* w
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 8; ++j) amax = fmaxf(amax, red[j]);
-  const float s = absmax_scale(amax);
+  const float s = absmax_scale(amax), inv = __frcp_rn(s);
   if (tid == 0) {
     scale[(e * nbs + nb) * kbs + kb] = s;
     if (scale_t) scale_t[(e * kbs + kb) * nbs + nb] = s;
   }
+  // codes through shared memory, so that a warp stores whole 128-byte rows: rows of 128 bytes, 16-byte
+  // pieces swapped so that neither side meets in a bank
+  const int rl = (warp & 3) * 32 + (lane >> 3) * 8, cl = (warp >> 2) * 64 + (lane & 7) * 8;
   uint2 c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float x[8], v[8];
     unpack8(d[i], x);
-    quant_any<8>(x, s, v);
+    quant_any<8>(x, s, inv, v);
     c[i] = pack_e4m3x8(v);
-    if (n0 + i < N) *reinterpret_cast<uint2*>(q + (e * N + n0 + i) * K + k0) = c[i];
+    const int r = rl + i;
+    *reinterpret_cast<uint2*>(tile + r * 128 + (((cl >> 4) ^ ((r >> 1) & 4)) << 4) + (cl & 8)) = c[i];
   }
-  if (!q_t) return;  // (N % 128 == 0 from here on)
+  if (q_t) {  // (N % 128 == 0)
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // 4 columns: the low or high words of the 8 rows
-    uint32_t r[8];
+    for (int h = 0; h < 2; ++h) {  // 4 columns: the low or high words of the 8 rows
+      uint32_t r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = h ? c[i].y : c[i].x;
-    uint32_t o[4][2];
+      for (int i = 0; i < 8; ++i) r[i] = h ? c[i].y : c[i].x;
+      uint32_t o[4][2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const uint32_t t0 = __byte_perm(r[4 * g], r[4 * g + 1], 0x5140), t1 = __byte_perm(r[4 * g + 2], r[4 * g + 3], 0x5140);
-      const uint32_t t2 = __byte_perm(r[4 * g], r[4 * g + 1], 0x7362), t3 = __byte_perm(r[4 * g + 2], r[4 * g + 3], 0x7362);
-      o[0][g] = __byte_perm(t0, t1, 0x5410);
-      o[1][g] = __byte_perm(t0, t1, 0x7632);
-      o[2][g] = __byte_perm(t2, t3, 0x5410);
-      o[3][g] = __byte_perm(t2, t3, 0x7632);
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t t0 = __byte_perm(r[4 * g], r[4 * g + 1], 0x5140), t1 = __byte_perm(r[4 * g + 2], r[4 * g + 3], 0x5140);
+        const uint32_t t2 = __byte_perm(r[4 * g], r[4 * g + 1], 0x7362), t3 = __byte_perm(r[4 * g + 2], r[4 * g + 3], 0x7362);
+        o[0][g] = __byte_perm(t0, t1, 0x5410);
+        o[1][g] = __byte_perm(t0, t1, 0x7632);
+        o[2][g] = __byte_perm(t2, t3, 0x5410);
+        o[3][g] = __byte_perm(t2, t3, 0x7632);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r2 = cl + 4 * h + j;
+        *reinterpret_cast<uint2*>(tile_t + r2 * 128 + (((rl >> 4) ^ ((r2 >> 3) & 7)) << 4) + (rl & 8)) =
+            make_uint2(o[j][0], o[j][1]);
+      }
     }
+  }
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint2*>(q_t + (e * K + k0 + 4 * h + j) * N + n0) = make_uint2(o[j][0], o[j][1]);
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 32 + (tid >> 3), p = tid & 7;
+    const int64_t n = nb * 128ll + r;
+    if (n < N)
+      *reinterpret_cast<uint4*>(q + (e * N + n) * K + kb * 128ll + p * 16) =
+          *reinterpret_cast<const uint4*>(tile + r * 128 + ((p ^ ((r >> 1) & 4)) << 4));
+    if (q_t)
+      *reinterpret_cast<uint4*>(q_t + (e * K + kb * 128ll + r) * N + nb * 128ll + p * 16) =
+          *reinterpret_cast<const uint4*>(tile_t + r * 128 + ((p ^ ((r >> 3) & 7)) << 4));
   }
 }
 
 // SwiGLU backward with one scale per row and 128 columns of dA = [dA0 | dA1] (SwigluBwdOp's
 // arithmetic), and h = bf16(silu(a0) a1), which the backward's weight gradient of wo
 // contracts, from the same silu.  A CTA a row; 16 lanes hold 128 columns of both halves.
-// Bound by its arithmetic (exact quotients): 1.0 ms for 16384 x 2 14336, whose bytes take 0.49.
+// Bound by its arithmetic (exact quotients, their tests joined without branches): 0.74 ms for
+// 16384 x 2 14336, whose bytes take 0.49.
 __global__ void __launch_bounds__(256) swiglu_bwd_block_kernel(const uint16_t* dH, const uint16_t* a, int64_t F,
                                                                uint16_t* dA, uint16_t* h, uint8_t* q, float* scale) {
   const int units = static_cast<int>(F / 8);  // (a multiple of 16)
@@ -654,13 +685,15 @@ __global__ void __launch_bounds__(256) swiglu_bwd_block_kernel(const uint16_t* d
     unpack8(ldg16(dH + row * F + c), dh);
     bool fast = true;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fast = fast && swiglu_fast_range(z[j]);
+    for (int j = 0; j < 8; ++j) fast = fast & swiglu_fast_range(z[j]);
     bool ok = fast;
     if (fast) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = __fadd_rn(1.0f, exp_fast(-z[j]));
-        const float sig = div_checked(1.0f, d, ok), silu = div_checked(z[j], d, ok);
+        bool ok0 = true, ok1 = true;
+        const float sig = div_checked(1.0f, d, ok0), silu = div_checked(z[j], d, ok1);
+        ok = ok & ok0 & ok1;
         bwd_elem(z[j], a1[j], dh[j], sig, silu, v[0][j], v[1][j]);
         hv[j] = __fmul_rn(silu, a1[j]);
       }
@@ -686,7 +719,7 @@ __global__ void __launch_bounds__(256) swiglu_bwd_block_kernel(const uint16_t* d
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
       const float s = absmax_scale(m);
       float y[8];
-      quant_any<8>(v[p], s, y);
+      quant_any<8>(v[p], s, __frcp_rn(s), y);
       *reinterpret_cast<uint2*>(q + row * 2 * F + p * F + c) = pack_e4m3x8(y);
       if ((u & 15) == 0) scale[row * (F / 64) + p * (F / 128) + u / 16] = s;
     }

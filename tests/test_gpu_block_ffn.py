@@ -183,3 +183,26 @@ def test_refusals():
         moe.ffn_decode(x, ids, w, W)
     with pytest.raises(moe.MoEError):
         moe.prepare_weights(w_in[:, :, :64].contiguous(), w_out[:, :64].contiguous(), moe.PER_BLOCK128)
+
+
+def test_rows_of_tiny_values_with_zeros_among_them():
+    """Block scales whose reciprocals are past fp32: exact quotients, and zeros stay zeros."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(9, 512, generator=g, device="cuda") * 2.0 ** -122
+    x[:, ::3] = 0
+    x[3] *= 2.0 ** 100
+    x[4, 128:256] *= 2.0 ** 121
+    x = x.bfloat16()
+    vq, vs = ref.quantise_rows128(x)
+    src = torch.arange(9, dtype=torch.int32, device="cuda")
+    dO, q, s = moe.gather_scale_quant_block(x, None, src, 1)
+    assert torch.equal(dO, x) and torch.equal(s.double(), vs) and torch.equal(ref.e4m3(q), vq)
+    q, s = moe.quantize_rows(x, moe.PER_ROW_BLOCK128)
+    assert torch.equal(s.double(), vs) and torch.equal(ref.e4m3(q), vq)
+    # dA1 = dH silu(a0), a0 = 1; dA0 = 0 (a1 = 0), scale 1
+    a = torch.zeros(9, 1024, device="cuda", dtype=torch.bfloat16)
+    a[:, :512] = 1
+    dA, q, s, h = moe.swiglu_bwd_quant_block(x, a)
+    vq, vs = ref.quantise_rows128(dA)
+    assert not dA[:, :512].any() and not h.any()
+    assert torch.equal(s.double(), vs) and torch.equal(ref.e4m3(q), vq)
