@@ -12,6 +12,14 @@
 // off to the same side).  Division by it is exact: the code is e4m3's rounding of the
 // value alone.
 //
+// e4m3 has no infinity.  A block with one gets the scale kInfCode, which no other block has,
+// and its infinities the code 448, far above the block's finite values but not above what a
+// small value of the other operand brings back into fp32's range.  So that an overflow in a
+// gradient is never lost, the product's epilogue warps read the bf16 operands again where the
+// scales say that there is an infinity, and add its products with values other than zero to
+// the sums (add_infinities).  Where there is none this costs a word for each CTA that rounds,
+// read while the first tile's MMAs run.
+//
 // Two kernels:
 //   round_rows_kernel  both operands to codes in the workspace, transposed: for 128 rows
 //     of an expert (padded with zeros) and 128 columns a 16 KB tile, the image that the MMA
@@ -150,6 +158,12 @@ struct Operand {
   uint8_t* sf;         // [row blocks][nrb][512]
 };
 
+constexpr int kInfCode = 253;  // (finite values: 247 at the most; NaN among them: 248)
+// What stands for an infinity's bits, 0x7F80, in block_scale: one test for a lane's eight
+// columns, and block_scale gives kInfCode without one of its own.
+constexpr uint32_t kInfBits = 0x7F80, kInfMark = (kInfCode + 8) << 7;
+constexpr int kRoundCtas = 1024;       // CTAs that round, at the most: each has a word for "an infinity seen"
+
 // Power-of-two scale of a block from the bf16 bits of its largest magnitude:
 // the E8M0 code X + 127 and, through inv, 2^-X.
 __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float& inv) {
@@ -160,7 +174,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float& inv) 
 }
 
 __global__ void __launch_bounds__(256, 4) round_rows_kernel(const Operand oa, const Operand ob, const int32_t* sizes,
-                                                            int E, int g0, int El, int64_t M) {
+                                                            int E, int g0, int El, int64_t M, int* inf_seen) {
   __shared__ Tables t;
   __shared__ __align__(16) uint8_t sfs[2][kAtom];
   __shared__ __align__(128) uint8_t tile[2][kTileBytes];
@@ -172,6 +186,7 @@ __global__ void __launch_bounds__(256, 4) round_rows_kernel(const Operand oa, co
   const int per = oa.ncb + ob.ncb;
   const int64_t total = static_cast<int64_t>(t.kstart[El]) * per;
   int sel = 0;
+  bool inf = false;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x, sel ^= 1) {
     const int kb = static_cast<int>(w / per);
     int cb = static_cast<int>(w - static_cast<int64_t>(kb) * per);
@@ -220,6 +235,20 @@ __global__ void __launch_bounds__(256, 4) round_rows_kernel(const Operand oa, co
       m[c] = __vmaxu2(m[c], __shfl_xor_sync(0xffffffffu, m[c], 8));
       m[c] = __vmaxu2(m[c], __shfl_xor_sync(0xffffffffu, m[c], 16));
     }
+    const uint32_t top = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+    if (max(top >> 16, top & 0xFFFFu) >= kInfBits) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if ((m[c] & 0xFFFFu) == kInfBits) {
+          m[c] ^= kInfBits ^ kInfMark;
+          inf = true;
+        }
+        if (m[c] >> 16 == kInfBits) {
+          m[c] ^= (kInfBits ^ kInfMark) << 16;
+          inf = true;
+        }
+      }
+    }
     // column 64 (warp / 4) + 8 (lane % 8) + c is line 16 c + 8 (warp / 4) + lane % 8
     const int line0 = 8 * (warp >> 2) + (lane & 7);
     uint8_t* t0 = tile[sel] + line0 * 128 + (((2 * j + (rl >> 1)) ^ (lane & 7)) << 4) + 8 * (rl & 1);
@@ -248,7 +277,11 @@ __global__ void __launch_bounds__(256, 4) round_rows_kernel(const Operand oa, co
       *reinterpret_cast<uint4*>(o.sf + (static_cast<int64_t>(kb) * o.nrb + cb) * kAtom + 16 * tid) =
           *reinterpret_cast<const uint4*>(&sfs[sel][16 * tid]);
   }
-  if (tid == 0) bulk_wait_all();
+  const int any = __syncthreads_or(inf);
+  if (tid == 0) {
+    inf_seen[blockIdx.x] = any;
+    bulk_wait_all();
+  }
 }
 
 // ---- product -------------------------------------------------------------
@@ -276,6 +309,13 @@ struct Params {
   int nrb_a, nrb_b;
   const uint8_t* sf_a;
   const uint8_t* sf_b;
+  const int* inf_seen;  // a word for each CTA that rounded
+  int round_ctas;
+  const uint16_t* lhs;  // the operands themselves, for add_infinities
+  const int32_t* lhs_index;
+  int lhs_k;
+  int64_t lhs_rows;
+  const uint16_t* rhs;
   float* out;
   uint64_t stall_ns;  // test hook (moe_test_stall_consumers): 0, or the wait limit in ns
 };
@@ -331,6 +371,61 @@ __device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, 
       "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
+}
+
+// Whether a 512-byte scale atom holds kInfCode (all lanes of a warp).
+__device__ __forceinline__ bool atom_has_inf(const uint8_t* atom, int lane) {
+  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(atom) + lane);  // (written while this kernel waited)
+  constexpr uint32_t c = kInfCode * 0x01010101u;
+  return __any_sync(0xffffffffu, (__vcmpeq4(v.x, c) | __vcmpeq4(v.y, c) | __vcmpeq4(v.z, c) | __vcmpeq4(v.w, c)) != 0);
+}
+
+// The products that an infinity enters with a value other than zero, added to the sums that
+// this warp has stored for a tile: the lane's row k and the 128 columns from n0 on.
+__device__ void add_infinities(const Params& p, const Ctl* c, const Tile& tl, int k, int n0) {
+  const int lane = threadIdx.x & 31, n4 = n0 + 4 * lane;  // (operands: the lane's k, and four columns)
+  const int first = c->t.start[tl.el], nkb = (tl.rows + kRB - 1) / kRB;
+  const bool k_in = k < p.K, n_in = n4 < p.N;
+  float* out = p.out + static_cast<int64_t>(tl.el) * p.K * p.N;
+  __syncwarp();  // the other lanes' stores of the tile
+  if (tl.k0 >= p.K || n0 >= p.N) return;
+  for (int kb = 0; kb < nkb; ++kb) {
+    const int64_t at = tl.kb0 + kb;
+    const bool in_a = atom_has_inf(p.sf_a + (at * p.nrb_a + tl.k0 / 128) * kAtom, lane);
+    const bool in_b = atom_has_inf(p.sf_b + (at * p.nrb_b + n0 / 128) * kAtom, lane);
+    if (!in_a && !in_b) continue;
+    const int left = min(tl.rows - kb * kRB, kRB);
+    for (int i = 0; i < left; ++i) {
+      const int64_t m = first + kb * kRB + i;
+      int64_t src = m;
+      if (p.lhs_index) {
+        const int pick = __ldg(p.lhs_index + m);
+        src = pick < 0 ? -1 : pick / p.lhs_k;
+        if (src >= p.lhs_rows) src = -1;  // (a row of zeros, reported where it was rounded)
+      }
+      const float a = k_in && src >= 0 ? __uint_as_float(static_cast<uint32_t>(__ldg(p.lhs + src * p.K + k)) << 16) : 0.0f;
+      uint2 d = make_uint2(0, 0);
+      if (n_in) d = __ldg(reinterpret_cast<const uint2*>(p.rhs + m * p.N + n4));
+      const float b[4] = {bf16lo(d.x), bf16hi(d.x), bf16lo(d.y), bf16hi(d.y)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)  // an infinity of the rhs: every row k of the warp
+        for (unsigned who = __ballot_sync(0xffffffffu, isinf(b[j])); who; who &= who - 1) {
+          const int l = __ffs(who) - 1;
+          const float v = __shfl_sync(0xffffffffu, b[j], l);
+          if (a != 0.0f) out[static_cast<int64_t>(k) * p.N + n0 + 4 * l + j] += a * v;
+          __syncwarp();
+        }
+      for (unsigned who = __ballot_sync(0xffffffffu, isinf(a)); who; who &= who - 1) {  // of the lhs
+        const int l = __ffs(who) - 1;
+        const float v = __shfl_sync(0xffffffffu, a, l);
+        const int64_t row = __shfl_sync(0xffffffffu, k, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (b[j] != 0.0f && !isinf(b[j])) out[row * p.N + n4 + j] += v * b[j];
+        __syncwarp();
+      }
+    }
+  }
 }
 
 // Four 32-bit columns of this warp's lane quarter.
@@ -540,6 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + half * (kBN / 2);
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     uint32_t acc = 0;
+    int inf = 0;
+    for (int i = lane; i < p.round_ctas; i += 32) inf |= __ldcg(p.inf_seen + i);
     if (p.stall_ns && !mbar_wait_bounded_warp(smem_u32(&ctl->never), 0, abort_flag, p.stall_ns)) timed_out = true;
     for (int t = t0; t < total && !timed_out; t += step) {
       const Tile tl = get_tile(p, ctl, t, rank);
@@ -604,6 +701,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             store8(p.out + (static_cast<int64_t>(tl.el) * p.K + k + 8 * j) * p.N + n + 32 * i, y[j], wide);
       }
     }
+    if (__any_sync(0xffffffffu, inf) && !timed_out) {  // (after all tiles: no role waits for it)
+      for (int t = t0; t < total; t += step) {
+        const Tile tl = get_tile(p, ctl, t, rank);
+        add_infinities(p, ctl, tl, tl.k0 + 64 * ((lane >> 3) & 1) + 8 * (lane & 7) + (lane >> 4) + 2 * q4,
+                       tl.n0 + half * (kBN / 2));
+      }
+    }
     if (timed_out) {
       *abort_flag = 1;
       ctl->err = 2;
@@ -627,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct Layout {
   int64_t blocks;
   int ncb_a, ncb_b, nrb_a, nrb_b;
-  int64_t q_a, q_b, sf_a, sf_b, bytes;
+  int64_t q_a, q_b, sf_a, sf_b, inf, bytes;
 };
 
 bool make_layout(int64_t M, int64_t K, int64_t N, int El, Layout* l) {
@@ -645,7 +749,8 @@ bool make_layout(int64_t M, int64_t K, int64_t N, int El, Layout* l) {
   l->q_b = l->q_a + l->blocks * l->ncb_a * kTileBytes;
   l->sf_a = l->q_b + l->blocks * l->ncb_b * kTileBytes;
   l->sf_b = l->sf_a + l->blocks * l->nrb_a * kAtom;
-  l->bytes = l->sf_b + l->blocks * l->nrb_b * kAtom;
+  l->inf = l->sf_b + l->blocks * l->nrb_b * kAtom;
+  l->bytes = l->inf + kRoundCtas * 4;
   return true;
 }
 
@@ -703,12 +808,14 @@ extern "C" moe_status tgmm_fp8_mx(const uint16_t* lhs, int64_t lhs_rows, const i
   const Operand ob{rhs, nullptr, 1, M, static_cast<int>(N), l.ncb_b, l.nrb_b,
                    ws + l.q_b, ws + l.sf_b};
   const int64_t rounds = l.blocks * (oa.ncb + ob.ncb);
-  round_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(rounds, sms * 4)), 256, 0, st>>>(
-      oa, ob, group_sizes, E, group_offset, E_local, M);
+  const int round_ctas = static_cast<int>(std::min<int64_t>(rounds, std::min(sms * 4, kRoundCtas)));
+  int* inf_seen = reinterpret_cast<int*>(ws + l.inf);
+  round_rows_kernel<<<static_cast<unsigned>(round_ctas), 256, 0, st>>>(oa, ob, group_sizes, E, group_offset, E_local, M,
+                                                                       inf_seen);
   MOE_CUDA_TRY(cudaGetLastError());
   const Params p{group_sizes, E, group_offset, E_local, M, static_cast<int>(K), static_cast<int>(N),
-                 static_cast<int>(ktiles), static_cast<int>(ntiles), l.ncb_a, l.ncb_b, l.nrb_a, l.nrb_b, ws + l.sf_a, ws + l.sf_b, out,
-                 moe_detail_stall_ns()};
+                 static_cast<int>(ktiles), static_cast<int>(ntiles), l.ncb_a, l.ncb_b, l.nrb_a, l.nrb_b, ws + l.sf_a, ws + l.sf_b,
+                 inf_seen, round_ctas, lhs, lhs_index, k, lhs_rows, rhs, out, moe_detail_stall_ns()};
   static SmemLimit limit;
   MOE_CUDA_TRY(limit.set(tgmm_mx_kernel, kSmem, dev));
   cudaLaunchConfig_t cfg{};
