@@ -184,7 +184,7 @@ __device__ __forceinline__ float silu_f32(float z) { return __fdiv_rn(z, __fadd_
 // range, so that a thread's elements form one basic block the compiler can
 // interleave.  Each helper flags the rare inputs it does not cover and the
 // caller recomputes those with the exact per-element path, so the values are
-// bit-identical to exp_f32 / __fdiv_rn / quant_quotient.
+// bit-identical to exp_f32 / __fdiv_rn.
 
 __device__ __forceinline__ float rcp_approx(float b) {
   float y;
@@ -321,27 +321,50 @@ __device__ __forceinline__ bool quant_needs_division(float y) {
   return ((__float_as_uint(v) & 0xFFFFFu) - 0x80000u + 8u) <= 16u;
 }
 
-// out[j] = fp32(x[j] / s) as far as e4m3 rounding can tell, for N elements.
+// Below this a scale's reciprocal may overflow, and a zero times it is NaN: such scales divide.
+constexpr float kTinyScale = 0x1p-125f;
+
+// out[j] = fp32(x[j] / s) as far as e4m3 rounding can tell, for N elements and any scale; inv = 1 / s.
+// The products in pairs (packed fp32, one rounding each), and one test for all N values, joined
+// without branches: with a branch a value, quantising weights by 128 x 128 blocks takes a quarter
+// longer, the fused SwiGLU epilogues a tenth to a quarter.
 template <int N>
-__device__ __forceinline__ void quant_n(const float* x, float s, float inv, float* out) {
-  bool slow = false;
-  const uint64_t inv2 = f2_pack(inv, inv);
+__device__ __forceinline__ void quant_any(const float* x, float s, float inv, float* out) {
+  const bool tiny = s < kTinyScale;
+  bool slow = tiny;
 #pragma unroll
-  for (int j = 0; j < N; j += 2) {  // the products in pairs (packed fp32, one rounding each)
-    f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), inv2), out[j], out[j + 1]);
-    slow = slow || quant_needs_division(out[j]) || quant_needs_division(out[j + 1]);
+  for (int j = 0; j < N; j += 2) {
+    f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(inv, inv)), out[j], out[j + 1]);
+    slow = slow | quant_needs_division(out[j]) | quant_needs_division(out[j + 1]);
   }
   if (slow) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (quant_needs_division(out[j])) out[j] = __fdiv_rn(x[j], s);
+      if (tiny || quant_needs_division(out[j])) out[j] = __fdiv_rn(x[j], s);
   }
 }
 
-// The quotient that e4m3 quantisation rounds, fp32(x / s), for one element.
-__device__ __forceinline__ float quant_quotient(float x, float s, float inv_s) {
-  const float y = __fmul_rn(x, inv_s);
-  return quant_needs_division(y) ? __fdiv_rn(x, s) : y;
+// The same with a scale for each of N elements; tiny: one of them is (all are divided then, on a
+// path of their own, which takes fewer registers: h_quant_rows_kernel 75 for 81, 947 against 980 us
+// on 16384 x 14336).
+template <int N>
+__device__ __forceinline__ void quant_each(const float* x, const float* s, const float* inv, bool tiny, float* out) {
+  if (tiny) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) out[j] = __fdiv_rn(x[j], s[j]);
+    return;
+  }
+  bool slow = false;
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(inv[j], inv[j + 1])), out[j], out[j + 1]);
+    slow = slow | quant_needs_division(out[j]) | quant_needs_division(out[j + 1]);
+  }
+  if (slow) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (quant_needs_division(out[j])) out[j] = __fdiv_rn(x[j], s[j]);
+  }
 }
 
 // ------------------------------------------------------------------------

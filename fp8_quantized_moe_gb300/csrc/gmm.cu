@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR_REQ>::THREADS, 1)
           }
           if (p.h_mode == MOE_SCALE_PER_TENSOR) {  // the chunk's codes (16 bytes) into hp[4 cc ..]
             float qv[CW];
-            quant_n<CW>(h, hs, hinv, qv);
+            quant_any<CW>(h, hs, hinv, qv);
             const uint2 lo8 = pack_e4m3x8(qv), hi8 = pack_e4m3x8(qv + 8);
             hp[4 * cc] = lo8.x;
             hp[4 * cc + 1] = lo8.y;
@@ -1024,7 +1024,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR_REQ>::THREADS, 1)
               x16[2 * j] = bf16lo(hp[g * 8 + j]);
               x16[2 * j + 1] = bf16hi(hp[g * 8 + j]);
             }
-            quant_n<16>(x16, sblk, inv, qv);
+            quant_any<16>(x16, sblk, inv, qv);
             const uint2 lo8 = pack_e4m3x8(qv), hi8 = pack_e4m3x8(qv + 8);
             cw[4 * g] = lo8.x;
             cw[4 * g + 1] = lo8.y;
@@ -1622,7 +1622,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR_REQ>::THREADS, 1)
                 *reinterpret_cast<uint4*>(p.h_out + row * p.F + hc) = make_uint4(hb[0], hb[1], hb[2], hb[3]);
               } else if (p.h_mode == MOE_SCALE_PER_TENSOR) {
                 float qv[8];
-                quant_n<8>(h, hs, hinv, qv);
+                quant_any<8>(h, hs, hinv, qv);
                 *reinterpret_cast<uint2*>(p.h_q + row * p.F + hc) = pack_e4m3x8(qv);
               }
             }
@@ -1660,7 +1660,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR_REQ>::THREADS, 1)
                   x16[2 * j] = bf16lo(hp[g * 8 + j]);
                   x16[2 * j + 1] = bf16hi(hp[g * 8 + j]);
                 }
-                quant_n<16>(x16, sblk, inv, qv);
+                quant_any<16>(x16, sblk, inv, qv);
                 const uint2 lo8 = pack_e4m3x8(qv), hi8 = pack_e4m3x8(qv + 8);
                 dst[g] = make_uint4(lo8.x, lo8.y, hi8.x, hi8.y);
               }
@@ -2405,6 +2405,8 @@ __global__ void __launch_bounds__(256) quant_transpose_pad_kernel(const uint16_t
       sc[j] = (c0 + j < C) ? __ldg(scale + static_cast<int64_t>(lo) * C + c0 + j) : 1.0f;
       inv[j] = __frcp_rn(sc[j]);
     }
+    const bool tiny = fminf(fminf(fminf(sc[0], sc[1]), fminf(sc[2], sc[3])),
+                            fminf(fminf(sc[4], sc[5]), fminf(sc[6], sc[7]))) < kTinyScale;
     uint4 d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -2426,17 +2428,7 @@ __global__ void __launch_bounds__(256) quant_transpose_pad_kernel(const uint16_t
         v[2 * j] = bf16lo(w[j]);
         v[2 * j + 1] = bf16hi(w[j]);
       }
-      bool slow = false;
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {  // products in pairs (packed fp32, one rounding each)
-        f2_unpack(f2_mul(f2_pack(v[j], v[j + 1]), f2_pack(inv[j], inv[j + 1])), y[j], y[j + 1]);
-        slow = slow || quant_needs_division(y[j]) || quant_needs_division(y[j + 1]);
-      }
-      if (slow) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (quant_needs_division(y[j])) y[j] = __fdiv_rn(v[j], sc[j]);
-      }
+      quant_each<8>(v, sc, inv, tiny, y);
       const uint2 code = pack_e4m3x8(y);  // zero rows (padding) give zero codes
       // 8 bytes: half of 16-byte unit (unit >> 1), swizzled by 16-row group
       *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(&tile[r][0]) + 16 * ((unit >> 1) ^ ((r >> 4) & 7)) +
@@ -2538,7 +2530,8 @@ __global__ void __launch_bounds__(256) h_quant_rows_kernel(const uint16_t* h, fl
             x8[2 * j] = bf16lo(w[j]);
             x8[2 * j + 1] = bf16hi(w[j]);
           }
-          quant_n<8>(x8, s, inv, qv);
+          const float s8[8] = {s, s, s, s, s, s, s, s}, inv8[8] = {inv, inv, inv, inv, inv, inv, inv, inv};
+          quant_each<8>(x8, s8, inv8, s < kTinyScale, qv);
           c[hh] = pack_e4m3x8(qv);
         }
         qr[v] = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);

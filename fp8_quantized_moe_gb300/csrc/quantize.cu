@@ -233,25 +233,6 @@ struct SwigluBwdOp {  // dA0 = (dH a1) silu'(a0), dA1 = dH silu(a0); also stores
   __device__ __forceinline__ int64_t col(int u, int uu) const { return 8 * static_cast<int64_t>(u) + uu * F; }
 };
 
-// quant_n for any scale: below 2^-125 its reciprocal may overflow, so that all are divided.
-// One test for all N values, joined without branches: with a branch a value, quantising weights
-// by 128 x 128 blocks takes a quarter longer.
-template <int N>
-__device__ __forceinline__ void quant_any(const float* x, float s, float inv, float* out) {
-  const bool tiny = s < 0x1p-125f;
-  bool slow = tiny;
-#pragma unroll
-  for (int j = 0; j < N; j += 2) {
-    f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(inv, inv)), out[j], out[j + 1]);
-    slow = slow | quant_needs_division(out[j]) | quant_needs_division(out[j + 1]);
-  }
-  if (slow) {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (tiny || quant_needs_division(out[j])) out[j] = __fdiv_rn(x[j], s);
-  }
-}
-
 // ---- the row kernel ------------------------------------------------------
 // MODE: MOE_SCALE_PER_ROW, MOE_SCALE_PER_ROW_BLOCK128, MOE_SCALE_PER_TENSOR
 // or kModeMx32 (MXFP8, OCP MX v1.0: per 32-column block the shared exponent
@@ -494,7 +475,7 @@ __device__ __forceinline__ int find_group(const int64_t* starts, int E, int64_t 
 }
 
 template <bool QUANT>
-__global__ void __launch_bounds__(256) group_cols_kernel(const uint16_t* g, int64_t M, int64_t N,
+__global__ void __launch_bounds__(256, QUANT ? 3 : 4) group_cols_kernel(const uint16_t* g, int64_t M, int64_t N,
                                                          const int32_t* sizes, int E, int g0, int El, uint8_t* q,
                                                          float* scale) {
   __shared__ int64_t starts[kMaxGroups + 1];
@@ -511,6 +492,7 @@ __global__ void __launch_bounds__(256) group_cols_kernel(const uint16_t* g, int6
   int grp = find_group(starts, E, r0);  // global group of row r0
   int64_t gend = starts[grp + 1];
   float m[8], sc[8], inv[8];
+  bool tiny = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m[j] = 0.0f;
   auto load_scales = [&](int gg) {
@@ -518,6 +500,7 @@ __global__ void __launch_bounds__(256) group_cols_kernel(const uint16_t* g, int6
     for (int j = 0; j < 8; ++j) {
       sc[j] = scale[static_cast<int64_t>(gg - g0) * N + c0 + j];
       inv[j] = __frcp_rn(sc[j]);
+      tiny = tiny | (sc[j] < kTinyScale);
     }
   };
   auto flush = [&](int gg) {
@@ -572,6 +555,18 @@ __global__ void __launch_bounds__(256) group_cols_kernel(const uint16_t* g, int6
     }
   }
   if (!QUANT) flush(grp);
+  if (QUANT && tiny) {  // the strip again, divided (beside the fast path this took it 4 to 70 % longer)
+    grp = find_group(starts, E, r0);
+#pragma unroll 1
+    for (int64_t row = r0; row < r1; ++row) {
+      while (row >= starts[grp + 1]) ++grp;
+      float v[8], y[8];
+      unpack8(ldg16(g + row * N + c0), v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(v[j], __ldg(scale + static_cast<int64_t>(grp - g0) * N + c0 + j));
+      *reinterpret_cast<uint2*>(q + row * N + c0) = pack_e4m3x8(y);
+    }
+  }
 }
 
 __global__ void finalize_scales_kernel(float* scale, int64_t n) {
