@@ -1984,10 +1984,11 @@ __global__ void __launch_bounds__(W8Cfg<TOK, XF16>::WARPS * 32, 1)
       const int ch = tl.n0 + 128 * h + r;
       const bool ch_ok = ch < p.N;
       const float* s_blk = p.rhs_scale + static_cast<int64_t>(tl.el) * p.kblocks * p.N + (ch_ok ? ch : 0);
-      float inv_smax = 0.0f;
+      float inv_smax = 0.0f, up = 1.0f;  // up: brings scales whose reciprocal is past fp32 into range (exact)
       if (w_blk) {
         const float m = w8_block_smax(s_blk, p.kblocks, p.N, ch_ok);
-        inv_smax = m > 0.0f ? __frcp_rn(m) : 0.0f;
+        if (m < 0x1p-100f) up = 0x1p64f;
+        inv_smax = m > 0.0f ? __frcp_rn(__fmul_rn(m, up)) : 0.0f;
       }
       uint32_t rhi2 = 0x3C003C00u, rlo2 = 0u;  // f16x2 (1, 1) and (0, 0)
       int kb_have = -1;                        // the K block rhi2 / rlo2 belong to
@@ -2012,7 +2013,8 @@ __global__ void __launch_bounds__(W8Cfg<TOK, XF16>::WARPS * 32, 1)
         if (lane == 0) mbar_arrive(smem_u32(&ctl->rempty[s]));
         if (w_blk && (ks >> 1) != kb_have) {  // a new 128-wide K block (two stages)
           kb_have = ks >> 1;
-          const float rel = ch_ok ? __fmul_rn(__ldg(s_blk + static_cast<int64_t>(kb_have) * p.N), inv_smax) : 0.0f;
+          const float rel =
+              ch_ok ? __fmul_rn(__fmul_rn(__ldg(s_blk + static_cast<int64_t>(kb_have) * p.N), up), inv_smax) : 0.0f;
           const __half hi = __float2half_rn(rel);
           const uint32_t hb = __half_as_ushort(hi);
           const uint32_t lb = __half_as_ushort(__float2half_rn(__fsub_rn(rel, __half2float(hi))));

@@ -7,8 +7,9 @@ import pytest
 import torch
 
 import oracle
-from tests.gpu_helpers import dev, host, rand_codes, ragged_sizes
-from tests.test_gpu_gmm import R0, RB, RT, GC
+from tests.gpu_helpers import assert_close, dev, host, rand_codes, ragged_sizes
+from tests.test_gpu_gmm import GC, R0, RB, RT
+from tests.test_gpu_w8 import make_w8_case, w8_args, w8_both
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,18 @@ def test_fused_swiglu_of_tiny_activations(M, K, F, E, amode, wmode, hmode):
     if hmode != RT:
         assert (s_or < 2.0 ** -128).any()
         assert np.array_equal(host(hs_ref), s_or) and np.array_equal(host(hsc), s_or)
+
+
+@pytest.mark.parametrize("M,K,N,E", [(200, 256, 512, 3), (700, 768, 384, 2)])
+def test_int8_weights_with_tiny_block_scales(M, K, N, E):
+    sizes, a, sa, q, sw = make_w8_case(M, M, K, N, E, w_mode=RB, spread=4)
+    sw = np.ldexp(sw, -118).astype(np.float32)
+    sw[:, :, ::2] = np.ldexp(sw[:, :, ::2], 40)  # beside ordinary channels
+    sa = np.ldexp(sa, 90).astype(np.float32)
+    assert 0 < sw.min() < 2.0 ** -130
+    ref = oracle.gmm_w8(a, sa, R0, q, sw, RB, sizes)
+    out = w8_both(w8_args(a, sa, R0, q, sw, RB, sizes), M, K)
+    assert moe.device_error() == 0
+    # each channel by itself: the tolerance of blockwise int8 weights
+    for part in (slice(0, None, 2), slice(1, None, 2)):
+        assert_close(np.ascontiguousarray(out[:, part]), np.ascontiguousarray(ref[:, part]), "tiny block scales")
