@@ -135,16 +135,50 @@ def device_error() -> int:
     return code.value
 
 
+def _scale_shape(mode: int, rows: int, cols: int):
+    """Type and shape of the scales of [rows, cols] in this mode, or None for one scale."""
+    if mode == PER_ROW:
+        return torch.float32, (rows,)
+    if mode == PER_ROW_BLOCK128:
+        return torch.float32, (rows, _nb(cols))
+    if mode in (MX32, MX4):
+        return torch.uint8, (cols // 128, rows, 4)
+    return None
+
+
 def _scale_buf(mode: int, rows: int, cols: int, device, out=None):
     if out is not None:
         return out
-    if mode == PER_ROW:
-        return torch.empty(rows, dtype=torch.float32, device=device)
-    if mode == PER_ROW_BLOCK128:
-        return torch.empty(rows, _nb(cols), dtype=torch.float32, device=device)
-    if mode in (MX32, MX4):
-        return torch.empty(cols // 128, rows, 4, dtype=torch.uint8, device=device)
-    return None
+    made = _scale_shape(mode, rows, cols)
+    return None if made is None else torch.empty(made[1], dtype=made[0], device=device)
+
+
+def _sort_buffers(what: str, out: Optional[dict], x: torch.Tensor, topk_ids: torch.Tensor, E: int, mode: int):
+    """The dict of a sort: `out`, or a new one.  Its tensors are allocated where it is empty; those that it holds
+    have to be of this call's shapes (a captured graph may write them, so they are not replaced)."""
+    T, k = _arg(f"{what} topk_ids", topk_ids, torch.int32, 2).shape
+    if x.dim() != 2 or x.shape[0] < T:
+        raise MoEError(f"{what}: topk_ids are of {T} tokens, x is {list(x.shape)}")
+    R, D, dev = T * k, x.shape[1], x.device
+    o = out if out is not None else {}
+    if "sorted_src" not in o:
+        o["sorted_src"] = torch.empty(R, dtype=torch.int32, device=dev)
+        o["pos"] = torch.empty(R, dtype=torch.int32, device=dev)
+        o["group_sizes"] = torch.empty(E, dtype=torch.int32, device=dev)
+        o["group_offsets"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        o["xs_q"] = torch.empty(R, D, dtype=torch.uint8, device=dev)
+        o["xs_scale"] = _scale_buf(mode, R, D, dev)
+        return o
+    i32 = torch.int32
+    for key, want in (("sorted_src", (i32, (R,))), ("pos", (i32, (R,))), ("group_sizes", (i32, (E,))),
+                      ("group_offsets", (i32, (E + 1,))), ("xs_q", (torch.uint8, (R, D))),
+                      ("xs_scale", _scale_shape(mode, R, D))):
+        t = o[key]
+        if want is not None and (t is None or t.shape != want[1] or t.dtype is not want[0] or t.device != dev):
+            held = "nothing" if t is None else f"{t.dtype} {list(t.shape)} on {t.device}"
+            raise MoEError(f"{what}: the given buffers were made for another shape: {key} is {held}, "
+                           f"expected {want[0]} {list(want[1])} on {dev}")
+    return o
 
 
 def quantize_rows(x: torch.Tensor, mode: int, static_scale: Optional[torch.Tensor] = None, q=None, scale=None):
@@ -207,17 +241,8 @@ def ragged_sort(topk_ids: torch.Tensor, E: int, x_q: torch.Tensor, x_scale: Opti
                 out: Optional[dict] = None):
     """Returns dict(sorted_src, pos, group_sizes, group_offsets, xs_q, xs_scale)."""
     T, k = topk_ids.shape
-    D = x_q.shape[1]
-    R = T * k
-    dev = x_q.device
-    o = out if out is not None else {}
-    if "sorted_src" not in o:
-        o["sorted_src"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["pos"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["group_sizes"] = torch.empty(E, dtype=torch.int32, device=dev)
-        o["group_offsets"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        o["xs_q"] = torch.empty(R, D, dtype=torch.uint8, device=dev)
-        o["xs_scale"] = _scale_buf(mode, R, D, dev)
+    D, dev = x_q.shape[1], x_q.device
+    o = _sort_buffers("ragged_sort", out, x_q, topk_ids, E, mode)
     nws = lib().moe_ragged_sort_workspace_bytes(T, k, E)
     if "sort_ws" not in o or o["sort_ws"].numel() < nws:
         o["sort_ws"] = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
@@ -233,17 +258,8 @@ def quantize_sort(x: torch.Tensor, topk_ids: torch.Tensor, E: int, mode: int,
     """Steps 1 + 2 fused: sort indices and the gathered codes/scales of x.
     Returns the same dict as ragged_sort (bit-identical xs_q / xs_scale)."""
     T, k = topk_ids.shape
-    D = x.shape[1]
-    R = T * k
-    dev = x.device
-    o = out if out is not None else {}
-    if "sorted_src" not in o:
-        o["sorted_src"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["pos"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["group_sizes"] = torch.empty(E, dtype=torch.int32, device=dev)
-        o["group_offsets"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        o["xs_q"] = torch.empty(R, D, dtype=torch.uint8, device=dev)
-        o["xs_scale"] = _scale_buf(mode, R, D, dev)
+    D, dev = x.shape[1], x.device
+    o = _sort_buffers("quantize_sort", out, x, topk_ids, E, mode)
     nws = lib().moe_ragged_sort_workspace_bytes(T, k, E)
     if "sort_ws" not in o or o["sort_ws"].numel() < nws:
         o["sort_ws"] = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
@@ -257,17 +273,8 @@ def quantize_sort(x: torch.Tensor, topk_ids: torch.Tensor, E: int, mode: int,
 def quantize_sort_mx(x: torch.Tensor, topk_ids: torch.Tensor, E: int, out: Optional[dict] = None):
     """MXFP8 steps 1 + 2: the dict of quantize_sort with xs_scale = E8M0 codes [D/128, T*k, 4]."""
     T, k = topk_ids.shape
-    D = x.shape[1]
-    R = T * k
-    dev = x.device
-    o = out if out is not None else {}
-    if "sorted_src" not in o:
-        o["sorted_src"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["pos"] = torch.empty(R, dtype=torch.int32, device=dev)
-        o["group_sizes"] = torch.empty(E, dtype=torch.int32, device=dev)
-        o["group_offsets"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        o["xs_q"] = torch.empty(R, D, dtype=torch.uint8, device=dev)
-        o["xs_scale"] = _scale_buf(MX32, R, D, dev)
+    D, dev = x.shape[1], x.device
+    o = _sort_buffers("quantize_sort_mx", out, x, topk_ids, E, MX32)
     nws = lib().moe_ragged_sort_workspace_bytes(T, k, E)
     if "sort_ws" not in o or o["sort_ws"].numel() < nws:
         o["sort_ws"] = torch.empty(max(nws, 16), dtype=torch.uint8, device=dev)
@@ -1009,12 +1016,25 @@ class FFNBuffers:
         return self._w8_ws
 
     def tgmm_workspace(self, E: int) -> torch.Tensor:
-        """tgmm_mx's workspace for either weight gradient of E experts, allocated on first use."""
-        if self._tgmm_ws is None:
-            R = self.T * self.k
-            n = max(tgmm_mx_workspace_bytes(R, self.D, 2 * self.F, E), tgmm_mx_workspace_bytes(R, self.F, self.D, E))
-            self._tgmm_ws = torch.empty(max(n, 16), dtype=torch.uint8, device=self.y.device)
+        """tgmm_mx's workspace for either weight gradient of E experts, allocated on first use (and again for
+        more experts)."""
+        R = self.T * self.k
+        n = max(tgmm_mx_workspace_bytes(R, self.D, 2 * self.F, E), tgmm_mx_workspace_bytes(R, self.F, self.D, E), 16)
+        if self._tgmm_ws is None or self._tgmm_ws.numel() < n:
+            self._tgmm_ws = torch.empty(n, dtype=torch.uint8, device=self.y.device)
         return self._tgmm_ws
+
+    def check(self, what: str, W: "ExpertWeights", topk_w: Optional[torch.Tensor], T: int, k: int):
+        """Refuse a call of T tokens and k choices, or weights, that these buffers were not made for."""
+        if T != self.T or k != self.k:
+            raise MoEError(f"{what}: the buffers were made for {self.T} tokens of {self.k} experts, got {T} of {k}")
+        half = 2 if W.in_mode == MX4 else 1
+        E, D, F = W.w_in.shape[0], self.D, self.F
+        if W.w_in.shape != (E, 2 * F, D // half) or W.w_out.shape != (E, D, F // half):
+            raise MoEError(f"{what}: the buffers were made for D = {D} and F = {F}, got weights {list(W.w_in.shape)} "
+                           f"and {list(W.w_out.shape)}")
+        if topk_w is not None and (topk_w.dtype is not torch.float32 or topk_w.numel() != T * k):
+            raise MoEError(f"{what} topk_w: expected {torch.float32} {[T, k]}, got {topk_w.dtype} {list(topk_w.shape)}")
 
 
 def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, act_mode: int,
@@ -1027,9 +1047,14 @@ def ffn_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, W
     then not written), and where the scale modes allow it steps 3 and 4 run as
     one fused kernel (gmm_fp8_swiglu, bit-identical to gmm_fp8 +
     moe_swiglu_quant); buf.a then holds a only when the buffers were made for
-    a backward pass."""
+    a backward pass.  Buffers made for another shape or scale mode are refused."""
     E = W.w_in.shape[0]
-    k = topk_ids.shape[1]
+    T, k = _arg("ffn_forward topk_ids", topk_ids, torch.int32, 2).shape
+    if x.dtype is not torch.bfloat16 or x.shape != (T, buf.D):
+        raise MoEError(f"ffn_forward x: expected {torch.bfloat16} {[T, buf.D]}, got {x.dtype} {list(x.shape)}")
+    buf.check("ffn_forward", W, topk_w, T, k)
+    if act_mode != buf.act_mode and (act_mode != PER_TENSOR or buf.act_mode == MX4):
+        raise MoEError(f"ffn_forward: the buffers were made for scale mode {buf.act_mode}, got {act_mode}")
     if act_mode == MX32:
         if W.in_mode != MX32:
             raise MoEError("the MXFP8 forward needs MXFP8 weights")
@@ -1188,11 +1213,21 @@ def ffn_backward(dY: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, buf: 
     of the last two) are stored in it."""
     s = buf.sort
     k = buf.k
+    if dY.dtype is not torch.bfloat16 or dY.shape != (buf.T, buf.D):
+        raise MoEError(f"ffn_backward dY: expected {torch.bfloat16} {[buf.T, buf.D]}, got {dY.dtype} {list(dY.shape)}")
+    buf.check("ffn_backward", W, topk_w, buf.T, k)
     if W.in_mode == PER_BLOCK128:
         if W.w_in_t is None or x is None:
             raise MoEError("ffn_backward: PER_BLOCK128 weights made with for_backward, and x, are needed")
-        if not buf.keep_a:
-            raise MoEError("ffn_backward: buffers made with backward=True are needed")
+        if x.shape != dY.shape:
+            raise MoEError(f"ffn_backward x: expected {list(dY.shape)}, got {list(x.shape)}")
+    elif static_x is None or static_h is None:
+        raise MoEError("ffn_backward: the static scheme needs static_x and static_h")
+    if not buf.keep_a:
+        raise MoEError("ffn_backward: buffers made with backward=True are needed")
+    if not s or s["group_sizes"].shape[0] != W.w_in.shape[0]:
+        raise MoEError("ffn_backward: ffn_forward has to run on these buffers first, on the same weights")
+    if W.in_mode == PER_BLOCK128:
         sizes, ws = s["group_sizes"], buf.tgmm_workspace(W.w_in.shape[0])
         dO, dO_q, dO_s = gather_scale_quant_block(dY, topk_w, s["sorted_src"], k)
         gmm_block(dO_q, dO_s, W.w_out_t, W.s_out_t, sizes, out=buf.dH)
@@ -1205,8 +1240,6 @@ def ffn_backward(dY: torch.Tensor, topk_w: torch.Tensor, W: ExpertWeights, buf: 
         if keep is not None:
             keep.update(dO=dO, dO_q=dO_q, dO_s=dO_s, dA=dA, dA_q=dA_q, dA_s=dA_s, h=h)
         return buf.dX, dW_in, dW_out
-    if static_x is None or static_h is None:
-        raise MoEError("ffn_backward: the static scheme needs static_x and static_h")
     dO, dO_q, dO_s = gather_scale_quant(dY, topk_w, s["sorted_src"], k)
     gmm(dO_q, dO_s, PER_ROW, W.w_out_t, W.s_out, PER_TENSOR, s["group_sizes"], out=buf.dH)
     dA, dA_q, dA_s = swiglu_bwd_quant(buf.dH, buf.a)
