@@ -245,17 +245,18 @@ __global__ void __launch_bounds__(32 * kFinishWarps) balance_finish_kernel(Shape
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seq = blockIdx.x, e = blockIdx.y * 32 + lane;
   grid_wait_previous();
+  // (not __ldg: the kernel before wrote these while this one lived)
   const int64_t b0 = static_cast<int64_t>(seq) * s.per;
   float p = 0.0f;
   int c = 0, n = 0;
 #pragma unroll 8
   for (int b = warp; b < s.per; b += kFinishWarps) {
     if (e < s.E) {
-      p = __fadd_rn(p, __ldg(w.p + (b0 + b) * s.E + e));
-      c += __ldg(w.counts + (b0 + b) * s.E + e);
+      p = __fadd_rn(p, __ldcg(w.p + (b0 + b) * s.E + e));
+      c += __ldcg(w.counts + (b0 + b) * s.E + e);
     }
   }
-  for (int b = threadIdx.x; b < s.per; b += 32 * kFinishWarps) n += __ldg(w.tokens + b0 + b);
+  for (int b = threadIdx.x; b < s.per; b += 32 * kFinishWarps) n += __ldcg(w.tokens + b0 + b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   ps[warp][lane] = p;
