@@ -44,17 +44,18 @@ struct Shape {
   bool vec;       // 16-byte loads: rows start on 16 bytes
 };
 
-// The four columns 4 (lane + LPR i) .. of a row; past E: -inf.
+// The four columns 4 (lane + LPR i) .. of a row; past E: -inf.  (Plain loads: the gradient may be
+// written over the logits, each row by the lanes that have read it whole.)
 template <int LPR>
 __device__ __forceinline__ float4 load4(const float* row, int i, int sub, const Shape& s, bool on) {
   const int c = 4 * (sub + LPR * i);
   float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   if (!on || c >= s.E) return v;
-  if (s.vec) return __ldg(reinterpret_cast<const float4*>(row + c));
-  v.x = __ldg(row + c);
-  if (c + 1 < s.E) v.y = __ldg(row + c + 1);
-  if (c + 2 < s.E) v.z = __ldg(row + c + 2);
-  if (c + 3 < s.E) v.w = __ldg(row + c + 3);
+  if (s.vec) return *reinterpret_cast<const float4*>(row + c);
+  v.x = row[c];
+  if (c + 1 < s.E) v.y = row[c + 1];
+  if (c + 2 < s.E) v.z = row[c + 2];
+  if (c + 3 < s.E) v.w = row[c + 3];
   return v;
 }
 

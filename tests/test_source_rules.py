@@ -42,3 +42,12 @@ def test_what_an_overlapped_kernel_writes_is_not_read_as_constant():
                 seen += 1
                 assert "__ldg(" not in after, f"{name}: {fn}"
     assert seen >= 2
+
+
+def test_logits_that_the_gradient_may_overwrite_are_not_read_as_constant():
+    """moe_router_balance_backward's dlogits may be its logits: the kernel that writes them must not
+    promise, by __ldg, that they stay as they are."""
+    code = functions("balance.cu")
+    assert "load4" in code["balance_grad_kernel"]
+    assert "__ldg(" not in code["load4"]
+    assert not re.search(r"__ldg\(\s*(?:logits|dlogits)", code["balance_grad_kernel"])
