@@ -609,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             timed_out = true;
             break;
           }
+          tc_fence_after();  // (behind the MMAs that read the columns: commit, empty, producer, sfull)
           const uint8_t* sf = bp + kStages * kStageBytes + s * kSfBytes + 16 * lane;
           tmem_st_x4(tq + s * kSfCols, *reinterpret_cast<const uint4*>(sf));
           tmem_st_x4(tq + s * kSfCols + 4, *reinterpret_cast<const uint4*>(sf + kAtom));

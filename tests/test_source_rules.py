@@ -51,3 +51,23 @@ def test_logits_that_the_gradient_may_overwrite_are_not_read_as_constant():
     assert "load4" in code["balance_grad_kernel"]
     assert "__ldg(" not in code["load4"]
     assert not re.search(r"__ldg\(\s*(?:logits|dlogits)", code["balance_grad_kernel"])
+
+
+def test_tensor_memory_is_written_behind_a_fence():
+    """A warp that waits on a barrier and then touches tensor memory that other threads' tcgen05
+    operations used orders the two by tcgen05.fence::after_thread_sync (tc_fence_after)."""
+    seen = 0
+    for name in sorted(os.listdir(CSRC)):
+        if not name.endswith(".cu"):
+            continue
+        for fn, code in functions(name).items():
+            # a wait's condition, its way out, and what follows up to the first operation
+            for m in re.finditer(r"(?:wait_uniform|wait_warp|mbar_wait_bounded\w*)\s*\(", code):
+                rest = code[m.end():]
+                op = re.search(r"\b(?:tmem_st_\w+|tmem_ld_\w+|mma_\w+|tc_mma\w*)\s*\(", rest)
+                again = re.search(r"(?:wait_uniform|wait_warp|mbar_wait_bounded\w*)\s*\(", rest)
+                if not op or (again and again.start() < op.start()) or rest[op.start():].startswith("mma_commit"):
+                    continue
+                seen += 1
+                assert "tc_fence_after()" in rest[:op.start()], f"{name}: {fn}: {op.group(0)}"
+    assert seen >= 4
