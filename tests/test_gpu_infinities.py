@@ -93,6 +93,24 @@ def test_infinities_among_zeros_and_both_signs(M, K, N, sizes, g0, El, picked):
     assert torch.equal(out.nan_to_num(7.0), moe.tgmm_mx(x, d, *args).nan_to_num(7.0))
 
 
+def test_nothing_but_infinities():
+    """A step whose gradient has overflowed everywhere."""
+    x, d = operands(12, 3000, 528, 784)
+    x[:, ::5] = 0
+    d[:] = torch.where(d > 0, INF, -INF)
+    d[:, 3] = INF
+    x[:, 7] = x[:, 7].abs() + 1
+    out = moe.tgmm_mx(x, d, sizes_tensor([1000, 0, 2000]))
+    assert moe.device_error() == 0
+    assert not out[1].any()
+    for e, r, n in ((0, 0, 1000), (2, 1000, 2000)):
+        assert out[e][7, 3] == INF and not out[e][::5].any()
+        rest = torch.ones(528, dtype=torch.bool, device="cuda")
+        rest[::5] = False
+        assert not out[e][rest].isfinite().any()
+        assert out[e][rest].isnan().float().mean() > 0.99  # both signs meet nearly everywhere
+
+
 def test_infinities_of_other_shards_do_nothing():
     x, d = operands(9, 300, 64, 64)
     sizes = sizes_tensor([100, 100, 100])
