@@ -15,10 +15,12 @@
 // and then over the blocks of a sequence in a fixed order (no floating-point atomics:
 // the result does not depend on timing); counts are integers.
 //
-// Measured, both passes: 24 rows of 128 experts 6.8 us, 4 x 4096 of 256 experts 19 us (8, 8 and
-// 10 for the three kernels; bytes 5), 32 x 8192 of 64 experts 55 us (21, 6, 25; bytes 21): the
-// small ones are launches and round trips, the last one shuffles and exponentials beside
-// the memory.  (exp_f32 and one load a lane: 84 us.)
+// Measured, both passes back to back: 24 rows of 128 experts 6.8 us, 4 x 4096 of 256 experts
+// 20 us (12 for the sums, 8 for the gradient; bytes 5), 32 x 8192 of 64 experts 53 us (19, 34;
+// bytes 21): the small ones are launches and round trips.  The last one's kernels keep their issue slots
+// 66 and 57 % busy and DRAM 45 and 34 % (L2 30 and 21), and their warps wait for loads most: a
+// warp asks for its rows, then computes them, and the other warps cover that only in part.
+// (exp_f32 and one load a lane: 84 us when the rest took 57.)
 //
 // The gradient takes counts relative to the row's most probable expert e*: with
 // c'_e = c_e - c_{e*} the formula is the same, and where p_{e*} is near 1 the two terms
@@ -306,8 +308,8 @@ __global__ void __launch_bounds__(32 * kFinishWarps) balance_finish_kernel(Shape
   }
 }
 
-// (NV == 6: 80 registers, so that three blocks are resident as in the other pass; 67 us for 90
-// at 65536 rows of 768 experts.)
+// (NV == 6: 80 registers, so that three blocks are resident as in the other pass; 67 us for
+// 65536 rows of 768 experts.)
 template <int LPR, int NV>
 __global__ void __launch_bounds__(kThreads, NV == 6 ? 3 : 1)
     balance_grad_kernel(const float* logits, const uint8_t* valid, Shape s, const int* counts, const int* tokens,
@@ -388,11 +390,10 @@ __global__ void __launch_bounds__(kThreads, NV == 6 ? 3 : 1)
 }
 
 // Lanes a row and loads a lane.  Two loads a lane where they do: half the lanes, so fewer
-// shuffles a row and more rows an instruction than with one (262144 rows of 64 experts: 23
-// against 26.7 us for the sums, 25 against 32 for the gradient).  Three between the powers of
-// two, for lanes past the last expert do all the work of the others (sums and gradient, 65536
-// rows of 192 experts: 34 against 44.5 us; 131072 of 96: 40 against 49; 32768 of 384: 34
-// against 48; six loads, 65536 of 768: 122 against 140).
+// shuffles a row and more rows an instruction than with one (32 x 8192 rows of 64 experts, both
+// passes: 53 against 59 us).  Three between the powers of two, for lanes past the last expert do
+// all the work of the others (65536 rows of 192 experts: 43 against 49 us; 131072 of 96: 43
+// against 54; 32768 of 384: 45 against 53; six loads, 65536 of 768: 117 against 191).
 template <class F>
 cudaError_t by_width(int E, F&& f) {
   if (E <= 32) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
@@ -407,9 +408,9 @@ cudaError_t by_width(int E, F&& f) {
   return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
 }
 
-// Blocks at most: those that the streaming multiprocessors hold at once, by the registers of
-// a row's columns (32768 rows of 512 experts, both passes: 44 us with three a multiprocessor,
-// 56 with four; 65536 of 1000: 155 with two, 166 with four).
+// Blocks at most: those that 152 multiprocessors hold at once, by the registers of a row's
+// columns (both passes: 32768 rows of 512 experts 57 us with three a multiprocessor, 59 with
+// four; 65536 of 768 117 and 144; 65536 of 1000 189 with two, 201 with four).
 int blocks_for(int E) { return 152 * (E <= 384 ? 4 : E <= 768 ? 3 : 2); }
 constexpr int kMinChunk = 32;
 

@@ -30,14 +30,17 @@
 // memory (the stages', which are done with) and every CTA adds up and stores a slice of
 // the columns, in the order of the CTAs.
 //
-// Bound and measurements.  A block is 554 clocks of MMA at the measured rate, and 768 of
-// loads (48 KB at the 64 bytes a clock that an SM takes in).  On 16384 x 4096 x 28672 over
-// 8 groups in bursts: 1.38 ms; the same loop without any fold 1.29 (both accumulators handed
-// back and forth), without fold and MMAs 1.03, the hand-over alone 0.81: what is left is
-// loads, MMAs and hand-over in turn.  Run back to back the power limit lowers the clock and it
-// takes 1.53 ms, 2.5 PFLOP/s; the plain product of gmm_fp8 (one accumulator a tile, no fold)
-// 1.40.  64 of 96 groups of 49152 x 4096 x 7168: 956 us (a last tile of some 60 of 128
-// rows in each group of 512); 16384 x 1536 x 2048 over 128 groups: 91 us, its bytes 72.
+// Bound and measurements.  A block's four MMAs take 523 clocks with their operands in place,
+// whatever their N (520 to 525 for N = 32, 64, 96, 128, 192 and 256).  On 16384 x 4096 x 28672
+// over 8 groups, some 3136 blocks an SM, in bursts (1.94 GHz): 1.38 ms, 854 clocks a block; the
+// same loop without any fold 798 clocks (1.29 ms, both accumulators handed back and forth),
+// without fold and MMAs 637 (1.03 ms: loads, 77 bytes a clock and SM), the hand-over alone 501
+// (0.81 ms).  So loads, MMAs and hand-over are each well below the whole and overlap only in part;
+// no unit is at its limit (8192 x 4096 x 7168, one group: tensor pipe 61 % busy, L1 and shared
+// memory 51, L2 41, DRAM 23).  Back to back the power limit lowers the clock: 1.53 to 1.67 ms,
+// 2.3 to 2.5 PFLOP/s; the plain product of gmm_fp8 (one accumulator a tile, no fold) 1.40.
+// 64 of 96 groups of 49152 x 4096 x 7168: 939 to 969 us (a last tile of some 60 of 128 rows
+// in each group of 512); 16384 x 1536 x 2048 over 128 groups: 90 us, its bytes 72.
 // On the way there (burst or back to back alike):
 //   - tensor-memory loads of 16 columns, two at a time, against 32 columns: 2.4 against
 //     1.7 PFLOP/s (32 registers in a row cost moves and spills);
@@ -46,9 +49,10 @@
 //     polls take shared memory's time from the MMA's operands;
 //   - scales two blocks ahead against one, and the issuing warp's early look at the next
 //     stage: 6 and 3 %;
-//   - pairs of CTAs on 256 x 256 tiles (half of B each): 3 % slower on the large groups and on
-//     64 of 96, 22 % on 128 small ones (256-row tiles leave more rows empty);
-//   - four accumulators of 128 columns (N = 128 MMAs read A twice as often): 25 % slower;
+//   - pairs of CTAs on 256 x 256 tiles (half of B each; these issuing loops and 16-column loads,
+//     scales one block ahead): 3 % slower on the large groups and on 64 of 96, 22 % on 128
+//     small ones (256-row tiles leave more rows empty);
+//   - four accumulators of 128 columns: 25 % slower (twice as many MMAs, each as long);
 //   - 16 epilogue warps of 64 columns: 10 % slower; the next block's first columns loaded
 //     before a block's last sums: 12 %.
 //

@@ -42,13 +42,13 @@
 //                  handed back, then whole 32-byte sectors to memory, beside the next
 //                  tile's MMAs.
 //     Tiles run expert-major, then n tile, then k tile.
-//     One CTA per 128 x 256 tile needs 48 KB a block and SM, 768 clocks at the 64 bytes a
-//     clock that an SM takes in; a pair needs 32 KB.
-//     Measured with the rounding, back to back: 16384 rows, 4096 x 28672, 8 experts 1.68 ms
-//     (rounding 0.26; in bursts 1.55: the power limit lowers the clock); there without the
-//     stores 1.33, without the MMAs 1.35, with neither 0.96: loads, MMAs and stores (3.8 GB)
-//     overlap only in part.  49152 rows, 4096 x 2816, 64 experts: 790 us (rounding 166,
-//     stores alone 475); 16384 rows, 2048 x 1536, 128 experts: 306 us (39, 260).  One CTA a
+//     One CTA per 128 x 256 tile needs 48 KB a block and SM, some 640 clocks (the 77 bytes a
+//     clock that gmm_block.cu's loads reach alone); a pair needs 32 KB.
+//     Measured with the rounding, back to back: 16384 rows, 4096 x 28672, 8 experts 1.68 to
+//     1.76 ms (rounding 0.26; in bursts 1.55: the power limit lowers the clock); there without
+//     the stores 1.33, without the MMAs 1.35, with neither 0.96: loads, MMAs and stores (3.8
+//     GB) overlap only in part.  49152 rows, 4096 x 2816, 64 experts: 780 to 820 us (rounding
+//     166, stores alone 475); 16384 rows, 2048 x 1536, 128 experts: 302 to 319 us (39, 260).  One CTA a
 //     128 x 256 tile, its issuing loops run by one lane and its scales by tcgen05.cp: 1.87 ms,
 //     980, 376 us; the pair with such loops: 1.75 ms; tiles stored by the lanes 3 % more
 //     (rounding 0.28 ms, 187, 47 us).  Gradients by TMA from shared memory instead of the

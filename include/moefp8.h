@@ -651,7 +651,8 @@ moe_status moe_quantize_weights_block(const uint16_t* w, int64_t E, int64_t N, i
  *   out[m, n] = bf16( sum_kb s_a[m, kb] s_b[g(m), n / 128, kb]
  *                     sum_{k in block kb} lhs_q[m, k] rhs_q[g(m), n, k] )
  * fp32 accumulation: 128 products on the tensor cores, the blocks' sums scaled and
- * added in fp32 registers.
+ * added in fp32 registers.  The two scales' product is an fp32 number: where it is below
+ * 2^-126 a block is off by up to 2^-125 more.
  *   lhs_q [M, K], lhs_scale [M, K / 128]; rhs_q [E_local, N, K], rhs_scale
  *   [E_local, ceil(N / 128), K / 128]; out bf16 [M, N].
  * Groups, group_offset and E_local are as in gmm_fp8: rows outside the local groups are

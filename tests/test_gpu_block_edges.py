@@ -110,3 +110,18 @@ def test_all_rows_in_one_expert():
     # as a whole: 512 additions of 32 products to one fp32 accumulator, each off by 2^-23 of it at the
     # most, and its size grows to the sum's own
     assert (out.double() - want).norm() <= (M / 32 + 32) * 2.0 ** -23 * want.norm()
+
+
+def test_products_of_scales_below_the_normal_numbers():
+    """The scales' product is an fp32 number: below 2^-126 it is off by 2^-150 at the most, a block of 128
+    products by 128 * 448^2 * 2^-150 < 2^-125."""
+    M, K, N = 130, 640, 272
+    lhs_q, lhs_s, rhs_q, rhs_s = product_case(9, M, K, N, 1)
+    for up in (-100, -110, -118, -126):
+        a = (lhs_q, lhs_s * 2.0 ** up, rhs_q, rhs_s * 2.0 ** -20)
+        out = moe.gmm_block(*a)
+        want, mag = ref.gmm(*a, [M])
+        tol = mag * (128 * 2.0 ** -23 + (K // 128 + 2) * 2.0 ** -24) + want.abs() * 2.0 ** -8
+        # (and bf16's own half step below its normal numbers, 2^-134)
+        assert ((out.double() - want).abs() <= tol + K // 128 * 2.0 ** -125 + 2.0 ** -134).all()
+    assert moe.device_error() == 0
