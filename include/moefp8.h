@@ -680,7 +680,7 @@ moe_status gmm_fp8_block(const uint8_t* lhs_q, const float* lhs_scale, const uin
  * A sum that an infinity enters with a value other than zero is that infinity, however small
  * the value (NaN where both signs meet): an overflow in a gradient is never lost.  With zeros
  * it adds nothing, and the finite values of its block count as zeros beside it.  A NaN makes
- * every product that its block enters NaN.
+ * every sum that it enters NaN, with zeros too.
  * K % 16 == 0, N % 16 == 0, E <= 1024; every pointer but lhs_index and group_sizes
  * 16-byte aligned.  MOE_ERR_UNSUPPORTED off sm_103. */
 size_t tgmm_fp8_mx_workspace_bytes(int64_t M, int64_t K, int64_t N, int E_local);
